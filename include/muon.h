@@ -262,6 +262,140 @@ muon_status muon_adamw_step(void* const* params, const void* const* grads, float
                             float lr, float b1, float b2, float eps, float wd, int64_t step,
                             void* stream);
 
+/* ---- Training operators beside the step ------------------------------------
+ * What a training loop runs next to the optimizer step, on the parameters it
+ * keeps apart: the norms and dropout of a block (their gains and biases take
+ * muon_adamw_step, whose `grads` the backward passes below write) and the
+ * router of an expert slab (its weight and the slab take muon_step).
+ *
+ * Conventions, beside those at the top of this file:
+ *   - The tensors and `stream` belong to the current device.
+ *   - A matrix [rows, cols] has contiguous rows, `ld` (>= cols) elements
+ *     apart; its pointer needs only the alignment of one element.  Elements
+ *     between the rows are neither read nor written.
+ *   - rows = 0 is allowed (tensor pointers may then be null): sums over rows
+ *     are written as 0.
+ *   - An output may not overlap another argument, except where said; column
+ *     slices of one buffer with the same ld do not overlap.
+ *   - Every sum, mean and softmax is formed in fp32 or wider; each output is
+ *     rounded once, to nearest even.  Results are the same from run to run
+ *     (no order depends on timing) and do not depend on ld or alignment.
+ *   - Nothing is kept between calls; every call enqueues kernels only and may
+ *     be recorded into a HIP graph.  A workspace needs no clearing and may be
+ *     shared by calls that are ordered on one stream. */
+
+/* Layer norm of every row: mean = sum x / cols, rstd = 1 / sqrt(sum (x -
+ * mean)^2 / cols + eps), y = (x - mean) * rstd * gamma + beta.
+ *   x, y        : [rows, cols] of dt (MUON_F32 or MUON_BF16), cols in 1 ..
+ *                 32768.
+ *   gamma, beta : cols elements of param_dt, or null for 1 and 0.
+ *   mean, rstd  : rows floats each, for the backward pass, or null.
+ *   eps         : finite, > 0. */
+muon_status muon_layer_norm_fwd(const void* x, int64_t ld_x, muon_dtype dt, const void* gamma, const void* beta,
+                                muon_dtype param_dt, int64_t rows, int64_t cols, float eps, void* y, int64_t ld_y,
+                                float* mean, float* rstd, void* stream);
+
+/* Bytes of workspace (16-byte aligned) of the two backward passes below for
+ * these sizes; 0 means that a null workspace will do.  Not needed when
+ * neither dgamma nor dbeta is asked for. */
+muon_status muon_layer_norm_workspace_bytes(int64_t rows, int64_t cols, size_t* bytes);
+
+/* Gradients of muon_layer_norm_fwd: with xh = (x - mean) rstd, g = dy gamma,
+ *   dx = rstd (g - mean(g) - xh mean(g xh)), dgamma = sum over rows of dy xh,
+ *   dbeta = sum over rows of dy.
+ *   dy, x, dx     : [rows, cols] of dt; mean, rstd as the forward pass wrote
+ *                   them.
+ *   dgamma, dbeta : cols elements of param_dt, overwritten; null if not
+ *                   wanted. */
+muon_status muon_layer_norm_bwd(const void* dy, int64_t ld_dy, const void* x, int64_t ld_x, muon_dtype dt,
+                                const void* gamma, muon_dtype param_dt, const float* mean, const float* rstd,
+                                int64_t rows, int64_t cols, void* dx, int64_t ld_dx, void* dgamma, void* dbeta,
+                                void* workspace, size_t workspace_bytes, void* stream);
+
+/* Dropout, with an optional residual: out = residual + keep * x * s.
+ * The mask is a function of (seed, offset, row, column) alone and is never
+ * stored: element (r, c) draws u = halfword c % 8 (low half of each word
+ * first) of Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random
+ * numbers: as easy as 1, 2, 3", 2011) with key (seed low, seed high) and
+ * counter (c / 8, r, low, high word of offset + *offset_dev), and is kept
+ * when u >= t = round(65536 p); s = 65536 / (65536 - t), so p is met to
+ * 2^-17 and the mean exactly.  A dropped element gives 0 whatever it holds;
+ * p = 1 drops all.
+ * The backward pass is the same call on the gradient, without a residual
+ * (whose gradient is the output's).
+ *   x, residual, out : [rows, cols] of dt, rows < 2^32, cols <= 2^34; residual
+ *                      may be null.  out may be x or residual itself.
+ *   p                : 0 .. 1.
+ *   seed, offset     : any 64 bits.  Calls that should draw different masks
+ *                      need different offsets.
+ *   offset_dev       : null, or a device word (8-byte aligned) that is added
+ *                      to offset (modulo 2^64) when the kernel runs, so that a
+ *                      recorded call draws a new mask on each replay. */
+muon_status muon_dropout(const void* x, int64_t ld_x, const void* residual, int64_t ld_res, muon_dtype dt,
+                         int64_t rows, int64_t cols, float p, uint64_t seed, uint64_t offset,
+                         const uint64_t* offset_dev, void* out, int64_t ld_out, void* stream);
+
+/* A block's residual branch in one pass: h = residual + dropout(x), rounded
+ * to dt as muon_dropout does, and y, mean, rstd = layer norm of that h, as
+ * muon_layer_norm_fwd does: the same bits as the two calls.  h may be the
+ * residual itself.  Arguments as there. */
+muon_status muon_dropout_add_layer_norm_fwd(const void* x, int64_t ld_x, const void* residual, int64_t ld_res,
+                                            muon_dtype dt, const void* gamma, const void* beta, muon_dtype param_dt,
+                                            int64_t rows, int64_t cols, float eps, float p, uint64_t seed,
+                                            uint64_t offset, const uint64_t* offset_dev, void* h, int64_t ld_h,
+                                            void* y, int64_t ld_y, float* mean, float* rstd, void* stream);
+
+/* Its gradients: g = (layer norm's gradient of dy at h) + dh, where dh is
+ * the gradient that reaches h by the residual path (null: 0); dresidual = g
+ * and dx = dropout(g) with the forward pass's mask, each rounded once. */
+muon_status muon_dropout_add_layer_norm_bwd(const void* dy, int64_t ld_dy, const void* dh, int64_t ld_dh,
+                                            const void* h, int64_t ld_h, muon_dtype dt, const void* gamma,
+                                            muon_dtype param_dt, const float* mean, const float* rstd, int64_t rows,
+                                            int64_t cols, float p, uint64_t seed, uint64_t offset,
+                                            const uint64_t* offset_dev, void* dx, int64_t ld_dx, void* dresidual,
+                                            int64_t ld_dres, void* dgamma, void* dbeta, void* workspace,
+                                            size_t workspace_bytes, void* stream);
+
+/* Expert router: of every token's logits, p = softmax, the k largest as
+ * choices (equal logits: the lower expert first) with their gates, the
+ * choices of each expert, and the balance loss
+ *   loss = coef * experts * sum_e f_e P_e,  f_e = counts_e / (k n),
+ *   P_e = (sum over tokens of p_e) / n,
+ * which is coef when experts are used evenly (0 when n = 0).
+ *   logits    : [tokens, experts] of dt; finite or -inf.  An expert at -inf is
+ *               shut off for the token and never chosen.
+ *   experts   : 1 .. 1024; k : 1 .. min(experts, 16); tokens * k < 2^31.
+ *   valid     : null, or one byte a token, 0 for a padding token (its logits
+ *               may hold anything).  Such a token, and one whose experts are
+ *               all shut off, has no choice and enters no sum.
+ *   renorm    : 1: the gates of a token are divided by their sum; 0: they are
+ *               p itself.
+ *   indices   : [tokens, k] int32, by falling logit; -1 where no expert is
+ *               left (gate 0).
+ *   gates     : [tokens, k] floats.
+ *   counts    : experts int32;  n_tokens : n, one int32.
+ *   prob_mean : experts floats, P_e, or null;  loss : one float.
+ *   workspace : muon_route_workspace_bytes(), 16-byte aligned. */
+muon_status muon_route_workspace_bytes(int64_t tokens, int32_t experts, size_t* bytes);
+muon_status muon_route_fwd(const void* logits, int64_t ld, muon_dtype dt, int64_t tokens, int32_t experts, int32_t k,
+                           const uint8_t* valid, int32_t renorm, float coef, int32_t* indices, float* gates,
+                           int32_t* counts, int32_t* n_tokens, float* prob_mean, float* loss, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* Gradient of the gates and the loss by the logits (counts, choices and n
+ * are constants):
+ *   dp_e = dloss * coef * experts * counts_e / (k n^2) + (chosen: its gate's),
+ *   dlogit = p (dp - sum_e p dp), 0 for tokens without a choice.
+ *   indices, counts, n_tokens : as the forward pass wrote them (an index
+ *                outside 0 .. experts - 1 counts as no choice).
+ *   dgates  : [tokens, k] floats, or null for 0;  dloss : one float on the
+ *             device, or null for 1.
+ *   dlogits : [tokens, experts] of dt. */
+muon_status muon_route_bwd(const void* logits, int64_t ld, muon_dtype dt, int64_t tokens, int32_t experts, int32_t k,
+                           const uint8_t* valid, int32_t renorm, float coef, const int32_t* indices,
+                           const int32_t* counts, const int32_t* n_tokens, const float* dgates, const float* dloss,
+                           void* dlogits, int64_t ld_d, void* stream);
+
 /* ---- Diagnostics of the skinny path ---------------------------------------
  * The skinny path (bf16, min(rows, cols) <= 32) runs one persistent launch
  * per chunk whose workgroups exchange partial sums, so they must all be

@@ -36,6 +36,9 @@ EXPORTS = ["muon_plan_create", "muon_plan_destroy", "muon_plan_workspace_bytes",
            "muon_plan_num_matrices", "muon_plan_assign", "muon_shard_update", "muon_adamw_step",
            "muon_workspace_status", "muon_set_wait_limit", "muon_set_side_stream", "muon_poll_timeout",
            "muon_step_noalloc",
+           "muon_layer_norm_fwd", "muon_layer_norm_workspace_bytes", "muon_layer_norm_bwd", "muon_dropout",
+           "muon_dropout_add_layer_norm_fwd", "muon_dropout_add_layer_norm_bwd",
+           "muon_route_workspace_bytes", "muon_route_fwd", "muon_route_bwd",
            "muon_kernel_timing", "muon_kernel_timing_read",
            "muon_status_str", "muon_last_error_detail", "muon_version"]
 
@@ -96,6 +99,28 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_shard_update.restype = i32
     lib.muon_adamw_step.argtypes = [P(vp), P(vp), P(vp), P(vp), P(i64), i32, i32, f32, f32, f32, f32, f32, i64, vp]
     lib.muon_adamw_step.restype = i32
+    u64 = ctypes.c_uint64
+    drop = [f32, u64, u64, vp]  # p, seed, offset, offset_dev
+    lib.muon_layer_norm_fwd.argtypes = [vp, i64, i32, vp, vp, i32, i64, i64, f32, vp, i64, vp, vp, vp]
+    lib.muon_layer_norm_fwd.restype = i32
+    lib.muon_layer_norm_workspace_bytes.argtypes = [i64, i64, P(sz)]
+    lib.muon_layer_norm_workspace_bytes.restype = i32
+    lib.muon_layer_norm_bwd.argtypes = [vp, i64, vp, i64, i32, vp, i32, vp, vp, i64, i64, vp, i64, vp, vp, vp, sz, vp]
+    lib.muon_layer_norm_bwd.restype = i32
+    lib.muon_dropout.argtypes = [vp, i64, vp, i64, i32, i64, i64, *drop, vp, i64, vp]
+    lib.muon_dropout.restype = i32
+    lib.muon_dropout_add_layer_norm_fwd.argtypes = [vp, i64, vp, i64, i32, vp, vp, i32, i64, i64, f32, *drop, vp, i64,
+                                                    vp, i64, vp, vp, vp]
+    lib.muon_dropout_add_layer_norm_fwd.restype = i32
+    lib.muon_dropout_add_layer_norm_bwd.argtypes = [vp, i64, vp, i64, vp, i64, i32, vp, i32, vp, vp, i64, i64, *drop,
+                                                    vp, i64, vp, i64, vp, vp, vp, sz, vp]
+    lib.muon_dropout_add_layer_norm_bwd.restype = i32
+    lib.muon_route_workspace_bytes.argtypes = [i64, i32, P(sz)]
+    lib.muon_route_workspace_bytes.restype = i32
+    lib.muon_route_fwd.argtypes = [vp, i64, i32, i64, i32, i32, vp, i32, f32, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.muon_route_fwd.restype = i32
+    lib.muon_route_bwd.argtypes = [vp, i64, i32, i64, i32, i32, vp, i32, f32, vp, vp, vp, vp, vp, vp, i64, vp]
+    lib.muon_route_bwd.restype = i32
     lib.muon_workspace_status.argtypes = [vp, vp, sz, vp, P(i32)]
     lib.muon_workspace_status.restype = i32
     lib.muon_set_wait_limit.argtypes = [ctypes.c_uint32]

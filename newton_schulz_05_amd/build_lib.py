@@ -23,7 +23,8 @@ DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
           "-Wno-unused-function", "-Wno-unused-variable"] + DEVICE_FLAGS
 
-SOURCES = ["plan.cpp", "validate.cpp", "api.cpp", "timer.cpp", "k_large.hip", "k_skinny.hip", "k_elem.hip"]
+SOURCES = ["plan.cpp", "validate.cpp", "validate_ops.cpp", "api.cpp", "api_ops.cpp", "timer.cpp",
+           "k_large.hip", "k_skinny.hip", "k_elem.hip", "k_norm.hip", "k_dropout.hip", "k_route.hip"]
 
 
 def _compile(src: str) -> str:

@@ -58,10 +58,16 @@ namespace {
 
 thread_local std::string g_detail;
 
-muon_status fail(muon_status s, const std::string& d) {
+}  // namespace
+
+muon_status muon::api_fail(muon_status s, const std::string& d) {
   g_detail = d;
   return s;
 }
+
+namespace {
+
+muon_status fail(muon_status s, const std::string& d) { return muon::api_fail(s, d); }
 
 constexpr unsigned kSpinLimit = 1u << 20;  // bounded barrier wait (polls, about a second)
 std::atomic<unsigned> g_spin_limit{kSpinLimit};
@@ -555,6 +561,6 @@ const char* muon_status_str(muon_status s) {
 
 const char* muon_last_error_detail(void) { return g_detail.c_str(); }
 
-int32_t muon_version(void) { return 200; }
+int32_t muon_version(void) { return 300; }
 
 }  // extern "C"

@@ -3,6 +3,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <string>
+
 #include "common.hpp"
 #include "plan.hpp"
 
@@ -92,5 +94,8 @@ struct AdamScalars {
   float lr, b1, b2, eps, wd, step_size, bc2_sqrt;  // step_size = lr / (1 - b1^t), bc2_sqrt = sqrt(1 - b2^t)
 };
 hipError_t run_adamw(const AdamTable& t, const AdamScalars& s, bool bf16, hipStream_t st);
+
+// Records the thread's error text (muon_last_error_detail) and returns s (api.cpp).
+muon_status api_fail(muon_status s, const std::string& d);
 
 }  // namespace muon

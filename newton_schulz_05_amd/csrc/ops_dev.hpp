@@ -1,0 +1,171 @@
+// Device helpers of the training operators: 8-element vector access at any
+// element alignment, reductions over lane groups, and the dropout generator.
+#pragma once
+
+#include "common.hpp"
+#include "ops.hpp"
+
+namespace muon {
+
+// ---- 8 consecutive elements --------------------------------------------------
+// gfx950 loads and stores 16 bytes at any address in global memory, so rows of
+// odd width or stride take the same 16-byte accesses as aligned ones; only
+// the last elements of a row that do not fill a vector go one by one.
+typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+
+template <typename T> struct Raw8;
+template <> struct Raw8<uint16_t> { u32x4 w; };
+template <> struct Raw8<float> { f32x4 a, b; };
+
+// The first n (any n, also <= 0 or > 8) of 8 elements at p; 0 in the others.
+__device__ __forceinline__ Raw8<uint16_t> load8(const uint16_t* p, int n) {
+  Raw8<uint16_t> r;
+  if (n >= 8) {
+    r.w = *(const u32x4_u*)p;
+  } else {
+    r.w = u32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) r.w[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
+  }
+  return r;
+}
+__device__ __forceinline__ Raw8<float> load8(const float* p, int n) {
+  Raw8<float> r;
+  if (n >= 8) {
+    r.a = *(const f32x4_u*)p;
+    r.b = *(const f32x4_u*)(p + 4);
+  } else {
+    r.a = f32x4{0, 0, 0, 0};
+    r.b = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) r.a[i] = p[i];
+#pragma unroll
+    for (int i = 4; i < 7; ++i)
+      if (i < n) r.b[i - 4] = p[i];
+  }
+  return r;
+}
+
+__device__ __forceinline__ void unpack8(const Raw8<uint16_t>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(r.w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(r.w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void unpack8(const Raw8<float>& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[i] = r.a[i];
+    v[4 + i] = r.b[i];
+  }
+}
+
+// One rounding to the stored type (none for fp32).
+__device__ __forceinline__ Raw8<uint16_t> pack8(const float (&v)[8], const uint16_t*) {
+  Raw8<uint16_t> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) r.w[i] = f2bf2(v[2 * i], v[2 * i + 1]);
+  return r;
+}
+__device__ __forceinline__ Raw8<float> pack8(const float (&v)[8], const float*) {
+  Raw8<float> r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.a[i] = v[i];
+    r.b[i] = v[4 + i];
+  }
+  return r;
+}
+
+__device__ __forceinline__ void store8(uint16_t* p, int n, const Raw8<uint16_t>& r) {
+  if (n >= 8) {
+    *(u32x4_u*)p = r.w;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 7; ++i)
+      if (i < n) p[i] = uint16_t(r.w[i >> 1] >> (16 * (i & 1)));
+  }
+}
+__device__ __forceinline__ void store8(float* p, int n, const Raw8<float>& r) {
+  if (n >= 8) {
+    *(f32x4_u*)p = r.a;
+    *(f32x4_u*)(p + 4) = r.b;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (i < n) p[i] = r.a[i];
+#pragma unroll
+    for (int i = 4; i < 7; ++i)
+      if (i < n) p[i] = r.b[i - 4];
+  }
+}
+
+// ---- reductions over groups of N adjacent lanes ---------------------------------
+// Every lane of the group ends with the result; the order of the operations
+// is fixed by the lane pattern.  Within 16 lanes by DPP (quad_perm, then
+// mirrors: once a quad holds one value, mirroring 8 or 16 lanes pairs the
+// quads), across them by the gfx950 row and half-wave swaps.
+template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t x) {
+  return uint32_t(__builtin_amdgcn_update_dpp(0, int(x), CTRL, 0xf, 0xf, true));
+}
+
+template <int N, typename V, typename F> __device__ __forceinline__ V lane_reduce(V v, F f) {
+  static_assert(sizeof(V) == 4 && (N == 8 || N == 16 || N == 64));
+  auto bits = [](V x) { return __builtin_bit_cast(uint32_t, x); };
+  auto val = [](uint32_t x) { return __builtin_bit_cast(V, x); };
+  v = f(v, val(dpp<0xB1>(bits(v))));   // quad_perm [1,0,3,2]
+  v = f(v, val(dpp<0x4E>(bits(v))));   // quad_perm [2,3,0,1]
+  v = f(v, val(dpp<0x141>(bits(v))));  // mirror of 8 lanes
+  if constexpr (N >= 16) v = f(v, val(dpp<0x140>(bits(v))));  // mirror of 16 lanes
+  if constexpr (N == 64) {
+    const auto a = __builtin_amdgcn_permlane16_swap(bits(v), bits(v), false, false);
+    v = f(val(a[0]), val(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(bits(v), bits(v), false, false);
+    v = f(val(b[0]), val(b[1]));
+  }
+  return v;
+}
+template <int N> __device__ __forceinline__ float lane_sum(float v) {
+  return lane_reduce<N>(v, [](float a, float b) { return a + b; });
+}
+
+// ---- dropout's generator -------------------------------------------------------
+// Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
+// easy as 1, 2, 3", 2011): ten rounds of two 32 x 32 -> 64 bit products, keyed
+// by the seed.  The counter is (column / 8, row, offset): element c of a row
+// takes halfword c % 8 of the 128 bits, low half of each word first, so the
+// mask of an element depends on nothing but (seed, offset, row, column) and
+// is formed again wherever it is needed.
+__device__ __forceinline__ u32x4 philox(uint32_t c0, uint32_t c1, uint32_t c2, uint32_t c3, uint32_t k0,
+                                        uint32_t k1) {
+#pragma unroll
+  for (int i = 0; i < 10; ++i) {
+    const uint64_t a = uint64_t(c0) * 0xD2511F53u, b = uint64_t(c2) * 0xCD9E8D57u;
+    const uint32_t n0 = uint32_t(b >> 32) ^ c1 ^ k0, n2 = uint32_t(a >> 32) ^ c3 ^ k1;
+    c1 = uint32_t(b);
+    c3 = uint32_t(a);
+    c0 = n0;
+    c2 = n2;
+    k0 += 0x9E3779B9u;
+    k1 += 0xBB67AE85u;
+  }
+  return u32x4{c0, c1, c2, c3};
+}
+
+__device__ __forceinline__ uint64_t drop_offset(const DropArgs& d) {
+  return d.offset + (d.offset_dev ? *d.offset_dev : 0);
+}
+
+// The 8 draws of one vector.
+__device__ __forceinline__ u32x4 drop_draws(const DropArgs& d, uint64_t off, uint32_t row, uint32_t block) {
+  return philox(block, row, uint32_t(off), uint32_t(off >> 32), d.k0, d.k1);
+}
+__device__ __forceinline__ bool drop_keeps(const u32x4& w, int i, uint32_t thresh) {
+  return ((i & 1) ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu) >= thresh;
+}
+
+}  // namespace muon

@@ -1,0 +1,286 @@
+"""Binding of the training operators beside the step (include/muon.h): layer
+norm, dropout, the two fused with the residual add, and the expert router.
+
+Argument marshalling only, like ``binding``: the caller gives the output
+tensors, every call is one C call on the current stream of the tensors'
+device (or on ``stream``), and nothing is kept between calls.  A matrix
+argument is any tensor whose last dimension is contiguous and whose leading
+dimensions lie one row stride apart (a column slice of a wider buffer, a
+[batch, time, cols] activation).
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import Optional, Tuple
+
+import torch
+
+from .binding import MuonError, _check, _dtype_code, load_library
+
+
+def _matrix(t: torch.Tensor, what: str) -> Tuple[int, int, int]:
+    """(rows, cols, row stride) of a matrix argument."""
+    shape, stride = t.shape, t.stride()
+    if not shape:
+        raise MuonError(2, f"{what} needs at least one dimension")
+    cols = shape[-1]
+    if stride[-1] != 1 and cols > 1:
+        raise MuonError(1, f"{what}: the last dimension is not contiguous")
+    if len(shape) == 2 and shape[0] > 1:
+        return shape[0], cols, stride[0]
+    rows, ld = 1, None
+    for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
+        if n == 0:
+            return 0, cols, cols
+        if n == 1:
+            continue
+        if ld is None:
+            ld = s
+        elif s != ld * rows:
+            raise MuonError(1, f"{what}: the rows do not lie one stride apart")
+        rows *= n
+    return rows, cols, cols if ld is None else ld
+
+
+def _same(t: torch.Tensor, like: torch.Tensor, what: str) -> int:
+    """Row stride of a matrix that has to match `like`."""
+    if t.dtype != like.dtype:
+        raise MuonError(3, f"{what} has dtype {t.dtype}, expected {like.dtype}")
+    if t.shape != like.shape:
+        raise MuonError(2, f"{what} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    return _matrix(t, what)[2]
+
+
+def _flat(t: Optional[torch.Tensor], n: int, dtypes, what: str) -> Optional[int]:
+    """Pointer of a contiguous argument of n elements, or None."""
+    if t is None:
+        return None
+    if t.dtype not in dtypes:
+        raise MuonError(3, f"{what} has dtype {t.dtype}, expected {' or '.join(map(str, dtypes))}")
+    if t.numel() != n:
+        raise MuonError(2, f"{what} has {t.numel()} elements, expected {n}")
+    if not t.is_contiguous():
+        raise MuonError(1, f"{what} is not contiguous")
+    return t.data_ptr()
+
+
+_F32, _I32, _MASK, _WORD = (torch.float32,), (torch.int32,), (torch.uint8, torch.bool), (torch.int64,)
+
+
+class _On:
+    """The device of a call's tensors, made current for its time, and the
+    stream to run on."""
+
+    def __init__(self, stream, *tensors):
+        dev = None
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise MuonError(1, "every tensor must be a device tensor")
+            if dev is None:
+                dev = t.device
+            elif t.device != dev:
+                raise MuonError(1, f"tensors on {dev} and {t.device}")
+        if stream is not None and stream.device != dev:
+            raise MuonError(1, f"a stream of {stream.device} for tensors on {dev}")
+        self.dev = dev
+        self.given = stream
+        self._guard = None
+
+    def __enter__(self):
+        if torch.cuda.current_device() != self.dev.index:
+            self._guard = torch.cuda.device(self.dev)
+            self._guard.__enter__()
+        self.stream = self.given if self.given is not None else torch.cuda.current_stream()
+        self.handle = self.stream.cuda_stream
+        return self
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+        return False
+
+    def workspace(self, given: Optional[torch.Tensor], need: int):
+        """(tensor, pointer, bytes): the caller's workspace, or one from
+        torch's allocator that belongs to the call's stream."""
+        if given is not None:
+            if not given.is_contiguous():
+                raise MuonError(5, "workspace is not contiguous")
+            return given, given.data_ptr(), given.numel() * given.element_size()
+        if need == 0:
+            return None, None, 0
+        if self.given is None:
+            t = torch.empty(need, dtype=torch.uint8, device=self.dev)
+        else:
+            with torch.cuda.stream(self.given):
+                t = torch.empty(need, dtype=torch.uint8, device=self.dev)
+        return t, t.data_ptr(), need
+
+
+def _param_code(gamma, beta, x) -> int:
+    p = gamma if gamma is not None else beta
+    return _dtype_code(x.dtype if p is None else p.dtype)
+
+
+def _param(t: Optional[torch.Tensor], first: Optional[torch.Tensor], cols: int, what: str) -> Optional[int]:
+    if t is None:
+        return None
+    return _flat(t, cols, (t.dtype,) if first is None else (first.dtype,), what)
+
+
+def _u64(v: int, what: str) -> int:
+    v = int(v)
+    if not 0 <= v < 1 << 64:
+        raise MuonError(1, f"{what} must be an unsigned 64-bit integer")
+    return v
+
+
+def layer_norm(x, gamma, beta, y, *, mean=None, rstd=None, eps: float = 1e-5, stream=None) -> None:
+    """y = layer norm of x's rows (muon_layer_norm_fwd); gamma and beta may be
+    None (1 and 0).  mean and rstd, float32 of one element a row, receive
+    what layer_norm_backward needs."""
+    rows, cols, ld = _matrix(x, "x")
+    ld_y = _same(y, x, "y")
+    g = _param(gamma, None, cols, "gamma")
+    b = _param(beta, gamma, cols, "beta")
+    m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
+    with _On(stream, x, y, gamma, beta, mean, rstd) as on:
+        _check(load_library().muon_layer_norm_fwd(x.data_ptr(), ld, _dtype_code(x.dtype), g, b,
+                                                  _param_code(gamma, beta, x), rows, cols, eps, y.data_ptr(), ld_y, m,
+                                                  r, on.handle))
+
+
+def _norm_workspace(rows: int, cols: int, wanted: bool) -> int:
+    if not wanted:
+        return 0
+    n = ctypes.c_size_t()
+    _check(load_library().muon_layer_norm_workspace_bytes(rows, cols, ctypes.byref(n)))
+    return n.value
+
+
+def _grad_params(gamma, dgamma, dbeta, x, cols: int):
+    first = next((t for t in (gamma, dgamma, dbeta) if t is not None), None)
+    ptrs = [_param(t, first, cols, w) for t, w in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta"))]
+    return _dtype_code(x.dtype if first is None else first.dtype), ptrs
+
+
+def layer_norm_backward(dy, x, gamma, mean, rstd, dx, *, dgamma=None, dbeta=None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of layer_norm (muon_layer_norm_bwd): dx, and dgamma and dbeta
+    where given, in gamma's dtype (the `grads` of adamw_step)."""
+    rows, cols, ld = _matrix(x, "x")
+    ld_dy, ld_dx = _same(dy, x, "dy"), _same(dx, x, "dx")
+    code, (g, dg, db) = _grad_params(gamma, dgamma, dbeta, x, cols)
+    m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
+    with _On(stream, x, dy, dx, gamma, mean, rstd, dgamma, dbeta, workspace) as on:
+        need = _norm_workspace(rows, cols, dg is not None or db is not None)
+        keep, ws, ws_bytes = on.workspace(workspace, need)
+        _check(load_library().muon_layer_norm_bwd(dy.data_ptr(), ld_dy, x.data_ptr(), ld, _dtype_code(x.dtype), g,
+                                                  code, m, r, rows, cols, dx.data_ptr(), ld_dx, dg, db, ws, ws_bytes,
+                                                  on.handle))
+
+
+def dropout(x, out, *, p: float, seed: int, offset: int = 0, offset_dev: Optional[torch.Tensor] = None,
+            residual: Optional[torch.Tensor] = None, stream=None) -> None:
+    """out = [residual +] dropout(x) with a counter-based mask (muon_dropout).
+    out may be x or residual itself.  The backward pass is the same call on
+    the gradient, with the same p, seed and offset and no residual.
+    offset_dev: an int64 tensor of one element added to offset on the device."""
+    rows, cols, ld = _matrix(x, "x")
+    ld_out = _same(out, x, "out")
+    ld_res = 0 if residual is None else _same(residual, x, "residual")
+    od = _flat(offset_dev, 1, _WORD, "offset_dev")
+    with _On(stream, x, out, residual, offset_dev) as on:
+        _check(load_library().muon_dropout(x.data_ptr(), ld, None if residual is None else residual.data_ptr(),
+                                           ld_res, _dtype_code(x.dtype), rows, cols, p, _u64(seed, "seed"),
+                                           _u64(offset, "offset"), od, out.data_ptr(), ld_out, on.handle))
+
+
+def dropout_add_layer_norm(x, residual, gamma, beta, h, y, *, p: float, seed: int, offset: int = 0,
+                           offset_dev: Optional[torch.Tensor] = None, mean=None, rstd=None, eps: float = 1e-5,
+                           stream=None) -> None:
+    """h = residual + dropout(x) and y = layer norm of h in one pass
+    (muon_dropout_add_layer_norm_fwd): the bits of dropout(residual=) followed
+    by layer_norm.  h may be the residual itself."""
+    rows, cols, ld = _matrix(x, "x")
+    ld_res, ld_h, ld_y = _same(residual, x, "residual"), _same(h, x, "h"), _same(y, x, "y")
+    g = _param(gamma, None, cols, "gamma")
+    b = _param(beta, gamma, cols, "beta")
+    m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
+    od = _flat(offset_dev, 1, _WORD, "offset_dev")
+    with _On(stream, x, residual, gamma, beta, h, y, mean, rstd, offset_dev) as on:
+        _check(load_library().muon_dropout_add_layer_norm_fwd(
+            x.data_ptr(), ld, residual.data_ptr(), ld_res, _dtype_code(x.dtype), g, b, _param_code(gamma, beta, x),
+            rows, cols, eps, p, _u64(seed, "seed"), _u64(offset, "offset"), od, h.data_ptr(), ld_h, y.data_ptr(),
+            ld_y, m, r, on.handle))
+
+
+def dropout_add_layer_norm_backward(dy, h, gamma, mean, rstd, dx, dresidual, *, p: float, seed: int, offset: int = 0,
+                                    offset_dev: Optional[torch.Tensor] = None, dh=None, dgamma=None, dbeta=None,
+                                    workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of dropout_add_layer_norm (muon_dropout_add_layer_norm_bwd).
+    dh is the gradient that reaches h by the residual path (None: 0);
+    dresidual is the residual's gradient, dx that of x."""
+    rows, cols, ld = _matrix(h, "h")
+    ld_dy, ld_dx, ld_dres = _same(dy, h, "dy"), _same(dx, h, "dx"), _same(dresidual, h, "dresidual")
+    ld_dh = 0 if dh is None else _same(dh, h, "dh")
+    code, (g, dg, db) = _grad_params(gamma, dgamma, dbeta, h, cols)
+    m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
+    od = _flat(offset_dev, 1, _WORD, "offset_dev")
+    with _On(stream, h, dy, dx, dresidual, dh, gamma, mean, rstd, dgamma, dbeta, offset_dev, workspace) as on:
+        need = _norm_workspace(rows, cols, dg is not None or db is not None)
+        keep, ws, ws_bytes = on.workspace(workspace, need)
+        _check(load_library().muon_dropout_add_layer_norm_bwd(
+            dy.data_ptr(), ld_dy, None if dh is None else dh.data_ptr(), ld_dh, h.data_ptr(), ld,
+            _dtype_code(h.dtype), g, code, m, r, rows, cols, p, _u64(seed, "seed"), _u64(offset, "offset"), od,
+            dx.data_ptr(), ld_dx, dresidual.data_ptr(), ld_dres, dg, db, ws, ws_bytes, on.handle))
+
+
+def _choices(t: torch.Tensor, rows: int, dtypes, what: str, k: Optional[int] = None) -> int:
+    """k of a [tokens, k] argument."""
+    n = t.shape[-1] if t.dim() else 0
+    if t.dim() < 1 or (k is not None and n != k):
+        raise MuonError(2, f"{what} has shape {tuple(t.shape)}, expected [{rows}, {'k' if k is None else k}]")
+    _flat(t, rows * n, dtypes, what)
+    return n
+
+
+def route(logits, indices, gates, counts, n_tokens, loss, *, coef: float = 1.0, renorm: bool = True, valid=None,
+          prob_mean=None, workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Top-k choices of every token's logits, their gates, the experts' counts
+    and the balance loss (muon_route_fwd); k is indices.shape[-1].  valid: a
+    uint8 or bool tensor, 0 for padding tokens."""
+    rows, experts, ld = _matrix(logits, "logits")
+    k = _choices(indices, rows, _I32, "indices")
+    _choices(gates, rows, _F32, "gates", k)
+    c, n = _flat(counts, experts, _I32, "counts"), _flat(n_tokens, 1, _I32, "n_tokens")
+    lo, pm = _flat(loss, 1, _F32, "loss"), _flat(prob_mean, experts, _F32, "prob_mean")
+    v = _flat(valid, rows, _MASK, "valid")
+    with _On(stream, logits, indices, gates, counts, n_tokens, loss, valid, prob_mean, workspace) as on:
+        lib = load_library()
+        need = ctypes.c_size_t()
+        _check(lib.muon_route_workspace_bytes(rows, experts, ctypes.byref(need)))
+        keep, ws, ws_bytes = on.workspace(workspace, need.value)
+        _check(lib.muon_route_fwd(logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, experts, k, v,
+                                  int(bool(renorm)), coef, indices.data_ptr(), gates.data_ptr(), c, n, pm, lo, ws,
+                                  ws_bytes, on.handle))
+
+
+def route_backward(logits, indices, counts, n_tokens, dlogits, *, dgates=None, dloss=None, coef: float = 1.0,
+                   renorm: bool = True, valid=None, stream=None) -> None:
+    """Gradient of route's gates and loss by the logits (muon_route_bwd).
+    dgates (None: 0) and dloss (a device float; None: 1) are the gradients
+    that reach them; coef, renorm and valid as in the forward call."""
+    rows, experts, ld = _matrix(logits, "logits")
+    ld_d = _same(dlogits, logits, "dlogits")
+    k = _choices(indices, rows, _I32, "indices")
+    if dgates is not None:
+        _choices(dgates, rows, _F32, "dgates", k)
+    c, n = _flat(counts, experts, _I32, "counts"), _flat(n_tokens, 1, _I32, "n_tokens")
+    dl, v = _flat(dloss, 1, _F32, "dloss"), _flat(valid, rows, _MASK, "valid")
+    with _On(stream, logits, indices, counts, n_tokens, dlogits, dgates, dloss, valid) as on:
+        _check(load_library().muon_route_bwd(logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, experts, k, v,
+                                             int(bool(renorm)), coef, indices.data_ptr(), c, n,
+                                             None if dgates is None else dgates.data_ptr(), dl, dlogits.data_ptr(),
+                                             ld_d, on.handle))

@@ -1,0 +1,286 @@
+"""GPU expert router (choices, gates, counts, balance loss, and their
+gradients) against the fp64 oracle."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from newton_schulz_05_amd import MuonError, route, route_backward
+from oracle import ops_ref as R
+from tests.ops_helpers import DEV, DTYPES, K, U, draw, h64, half_step, within
+
+pytestmark = pytest.mark.gpu
+
+
+def _outputs(rows, experts, k):
+    return dict(idx=torch.full((rows, k), 77, dtype=torch.int32, device=DEV), gates=torch.full((rows, k), 7.0, device=DEV),
+                counts=torch.full((experts,), 77, dtype=torch.int32, device=DEV),
+                n=torch.full((1,), 77, dtype=torch.int32, device=DEV), mean=torch.full((experts,), 7.0, device=DEV),
+                loss=torch.full((1,), 7.0, device=DEV))
+
+
+def _run(x, k, coef, renorm, valid, **kw):
+    o = _outputs(x.shape[0], x.shape[1], k)
+    route(x, o["idx"], o["gates"], o["counts"], o["n"], o["loss"], coef=coef, renorm=renorm, valid=valid,
+          prob_mean=o["mean"], **kw)
+    return o
+
+
+def _spread(xs):
+    """Largest distance of a finite logit from its row's maximum: the rounding
+    of the difference enters the exponential."""
+    f = xs[np.isfinite(xs)]
+    return float(f.max() - f.min()) if f.size else 0.0
+
+
+def _check(x, k, coef, renorm, valid, o):
+    xs = h64(x)
+    v = None if valid is None else valid.cpu().numpy()
+    idx, gates, counts, n, mean, loss = R.route(xs, k, coef, renorm, v)
+    assert np.array_equal(o["idx"].cpu().numpy(), idx)
+    assert np.array_equal(o["counts"].cpu().numpy(), counts)
+    assert int(o["n"]) == n
+    # exponential and sums of a row (K u), the difference under the exponential, and for the means the additions
+    # over tokens: at most rows / 16 in a thread, then 8 joins and 256 workgroups in at most 256 steps
+    rel = (K + _spread(xs)) * U
+    over = rel + (x.shape[0] / 16 + 280) * U
+    within(o["gates"], gates, 2 * rel * gates, "gates")
+    within(o["mean"], mean, over * mean, "prob_mean")
+    within(o["loss"], np.array([loss]), np.array([over * abs(loss)]), "loss")
+
+
+def _logits(rows, experts, dt, seed, std=2.0):
+    x = draw((rows, experts), seed, std, 0.0, DTYPES[dt])
+    return x.to(DEV)
+
+
+EXPERTS = [1, 2, 3, 7, 8, 9, 16, 17, 24, 32, 33, 64, 65, 128, 129, 255, 256, 257, 512, 513, 1000, 1024]
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("experts", EXPERTS)
+def test_forward_and_backward_match_the_oracle(experts, dt):
+    for rows, k, renorm in ((1, 1, True), (37, min(experts, 2), False), (530, min(experts, 16), True)):
+        x = _logits(rows, experts, dt, experts + rows)
+        o = _run(x, k, 0.3, renorm, None)
+        _check(x, k, 0.3, renorm, None, o)
+        _check_grad(x, k, 0.3, renorm, None, o, 900 + experts)
+
+
+def _check_grad(x, k, coef, renorm, valid, o, seed, with_gates=True, with_loss=True):
+    rows, experts = x.shape
+    dgates = draw((rows, k), seed, 0.5).to(DEV) if with_gates else None
+    dloss = torch.tensor([1.7], device=DEV) if with_loss else None
+    dx = torch.full_like(x, 5.0)
+    route_backward(x, o["idx"], o["counts"], o["n"], dx, dgates=dgates, dloss=dloss, coef=coef, renorm=renorm,
+                   valid=valid)
+    xs = h64(x)
+    v = None if valid is None else valid.cpu().numpy()
+    idx, counts, n = o["idx"].cpu().numpy(), o["counts"].cpu().numpy(), int(o["n"])
+    dg = np.zeros((rows, k)) if dgates is None else h64(dgates)
+    dl = 1.0 if dloss is None else float(np.float32(1.7))
+    want = R.route_backward(xs, idx, counts, n, k, coef, renorm, dg, dl, v)
+    p, live = R.softmax_rows(xs, v)
+    # magnitudes: the balance part less its mean, and the gates' part, |dg| / (sum of the chosen p) twice if renormalised
+    bal = abs(dl * coef) * np.abs(experts * counts - counts.sum()) / (k * max(n, 1) ** 2)
+    q = np.where(idx >= 0, np.take_along_axis(p, np.maximum(idx, 0), 1), 0.0)
+    s = np.where(live, q.sum(1), 1.0)[:, None] if renorm else 1.0
+    gat = np.where(idx >= 0, np.abs(dg) + (np.abs(dg * q).sum(1, keepdims=True) / s if renorm else 0.0), 0.0) / s
+    mag = np.broadcast_to(bal, (rows, experts)).copy()
+    for j in range(k):
+        np.add.at(mag, (np.arange(rows), np.maximum(idx[:, j], 0)), gat[:, j])
+    rel = 2 * (K + _spread(xs)) * U
+    within(dx, want, half_step(x.dtype) * np.abs(want) * (1 + 1e-6)
+           + rel * p * (mag + (p * mag).sum(1, keepdims=True)), "dlogits")
+    return dx
+
+
+@pytest.mark.parametrize("with_gates,with_loss", [(True, False), (False, True), (False, False)])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_optional_gradients(with_gates, with_loss, renorm):
+    x = _logits(300, 24, "f32", 11)
+    o = _run(x, 4, 0.01, renorm, None)
+    _check_grad(x, 4, 0.01, renorm, None, o, 12, with_gates, with_loss)
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("experts", [5, 8, 24, 100, 256])
+def test_masks(experts, dt):
+    """Padding tokens that hold anything, experts shut off for some tokens,
+    rows whose experts are all shut off, rows with fewer experts than k."""
+    rows, k = 201, min(experts, 6)
+    x = _logits(rows, experts, dt, 21 + experts)
+    shut = torch.rand(rows, experts, generator=torch.Generator().manual_seed(5)).to(DEV) < 0.4
+    x[shut] = float("-inf")
+    x[10:20] = float("-inf")
+    x[30, :] = float("-inf")
+    x[30, experts - 1] = -3.0
+    valid = (torch.rand(rows, generator=torch.Generator().manual_seed(6)) < 0.7).to(torch.uint8).to(DEV)
+    valid[[12, 30]] = 1
+    clean = x.clone()
+    x[valid == 0] = float("nan")
+    x[int(torch.nonzero(valid == 0)[0])] = float("inf")
+    for v in (valid, valid.bool()):
+        o = _run(x, k, 0.5, True, v)
+        _check(clean, k, 0.5, True, valid, o)
+        dx = _check_grad(clean, k, 0.5, True, valid, o, 31)
+        got = torch.full_like(x, 5.0)
+        dg = draw((rows, k), 31, 0.5).to(DEV)
+        route_backward(x, o["idx"], o["counts"], o["n"], got, dgates=dg, dloss=torch.tensor([1.7], device=DEV),
+                       coef=0.5, renorm=True, valid=v)
+        assert torch.equal(got, dx)
+        assert not got[valid == 0].any() and not got[12].any() and not got[shut].any()
+    assert o["idx"][30].tolist() == [experts - 1] + [-1] * (k - 1) and o["gates"][30, 0] == 1.0
+
+
+def test_ties_go_to_the_lower_expert():
+    x = torch.zeros(5, 40, device=DEV)
+    x[1, ::2] = -0.0             # equal to 0
+    x[2, 7:12] = 1.0
+    x[3] = -1e30
+    o = _run(x, 6, 1.0, False, None)
+    assert o["idx"][0].tolist() == o["idx"][1].tolist() == o["idx"][3].tolist() == [0, 1, 2, 3, 4, 5]
+    assert o["idx"][2].tolist() == [7, 8, 9, 10, 11, 0]
+    _check(x, 6, 1.0, False, None, o)
+    b = torch.randint(-3, 3, (2000, 256), generator=torch.Generator().manual_seed(1)).to(DEV).bfloat16()
+    _check(b, 16, 1.0, True, None, _run(b, 16, 1.0, True, None))
+
+
+def test_extreme_logits():
+    x = torch.zeros(6, 12, device=DEV)
+    x[0, 3] = 3e38
+    x[1] = -3e38
+    x[2] = torch.linspace(-90, 0, 12)
+    x[3] = torch.linspace(0, 3e38, 12)
+    x[4, :] = 1e-40
+    o = _run(x, 3, 1.0, True, None)
+    idx, gates, counts, n, mean, loss = R.route(h64(x), 3, 1.0, True)
+    assert np.array_equal(o["idx"].cpu().numpy(), idx) and np.array_equal(o["counts"].cpu().numpy(), counts)
+    # exp under- or overflows nowhere; denormal results may be flushed
+    within(o["gates"], gates, 2 * (K + 90) * U * gates + 1e-37, "gates")
+    assert torch.isfinite(o["loss"]).all()
+
+
+def test_bad_values_stay_in_bounds():
+    """NaN and +inf of a counted token show in its gates and the loss; choices
+    stay within the experts, and other tokens are as they were."""
+    x = _logits(100, 30, "f32", 41)
+    clean = _run(x, 4, 1.0, False, None)
+    y = x.clone()
+    y[7, 3], y[9, 4] = float("nan"), float("inf")
+    y[11] = float("nan")
+    o = _run(y, 4, 1.0, False, None)
+    i = o["idx"]
+    assert ((i >= -1) & (i < 30)).all()
+    keep = torch.ones(100, dtype=torch.bool, device=DEV)
+    keep[[7, 9, 11]] = False
+    assert torch.equal(i[keep], clean["idx"][keep]) and torch.equal(o["gates"][keep], clean["gates"][keep])
+    assert torch.isnan(o["loss"]).all()
+
+
+def test_foreign_indices_are_no_choice():
+    """Indices outside the experts count as none, an index named twice twice."""
+    x = _logits(4, 10, "f32", 51)
+    o = _run(x, 3, 0.0, False, None)
+    idx = o["idx"].clone()
+    idx[0] = torch.tensor([2, 2, 5], dtype=torch.int32)
+    idx[1] = torch.tensor([-7, 10, 1 << 30], dtype=torch.int32)
+    dg = draw((4, 3), 52).to(DEV)
+    dx = torch.empty_like(x)
+    route_backward(x, idx, o["counts"], o["n"], dx, dgates=dg, coef=0.0, renorm=False)
+    seen = idx.cpu().numpy().copy()
+    seen[1] = -1
+    want = R.route_backward(h64(x), seen, o["counts"].cpu().numpy(), 4, 3, 0.0, False, h64(dg), 1.0)
+    within(dx, want, 4 * K * U * np.abs(h64(dg)).sum(1, keepdims=True) * np.ones_like(want), "dlogits")
+    assert not dx[1].any()
+
+
+def test_gradient_against_differences():
+    rows, experts, k = 13, 9, 3
+    x = _logits(rows, experts, "f32", 61)
+    for renorm in (False, True):
+        o = _run(x, k, 0.8, renorm, None)
+        dg = draw((rows, k), 62).to(DEV)
+        dx = torch.empty_like(x)
+        route_backward(x, o["idx"], o["counts"], o["n"], dx, dgates=dg, dloss=torch.tensor([2.0], device=DEV),
+                       coef=0.8, renorm=renorm)
+        v = h64(draw((rows, experts), 63))
+        f = lambda z: R.route_objective(z, o["idx"].cpu().numpy(), o["counts"].cpu().numpy(), rows, k, 0.8, renorm,
+                                        h64(dg), 2.0)
+        d = (f(h64(x) + 1e-5 * v) - f(h64(x) - 1e-5 * v)) / 2e-5
+        assert abs((h64(dx) * v).sum() - d) <= 1e-8 + 4 * (K + 20) * U * np.abs(v).sum() * np.abs(h64(dg)).max()
+
+
+def test_balanced_counts_have_no_gradient():
+    x = torch.zeros(64, 8, device=DEV)
+    x[torch.arange(64), torch.arange(64) % 8] = 2.0
+    o = _run(x, 1, 0.3, True, None)
+    assert o["counts"].tolist() == [8] * 8
+    within(o["loss"], np.array([0.3]), np.array([1e-6]), "loss")
+    dx = torch.full_like(x, 5.0)
+    route_backward(x, o["idx"], o["counts"], o["n"], dx, coef=0.3, dgates=torch.ones(64, 1, device=DEV))
+    assert not dx.any()  # E c_e - sum c is 0, and a lone renormalised gate is 1
+
+
+def test_no_tokens():
+    o = _run(torch.empty(0, 6, device=DEV), 2, 1.0, True, None)
+    assert not o["counts"].any() and int(o["n"]) == 0 and not o["mean"].any() and float(o["loss"]) == 0
+    x = _logits(40, 6, "f32", 71)
+    o = _run(x, 2, 1.0, True, torch.zeros(40, dtype=torch.uint8, device=DEV))
+    assert not o["counts"].any() and int(o["n"]) == 0 and not o["mean"].any() and float(o["loss"]) == 0
+    assert (o["idx"] == -1).all() and not o["gates"].any()
+    dx = torch.full_like(x, 5.0)
+    route_backward(x, o["idx"], o["counts"], o["n"], dx, coef=1.0, dgates=torch.ones(40, 2, device=DEV))
+    assert not dx.any()
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,experts,k", [(30000, 8, 2), (20011, 64, 6), (9001, 256, 8)])
+def test_many_tokens_strided_and_repeated(rows, experts, k, dt):
+    x = _logits(rows, experts, dt, 81)
+    o = _run(x, k, 0.01, True, None)
+    _check(x, k, 0.01, True, None, o)
+    dx = _check_grad(x, k, 0.01, True, None, o, 82)
+    buf = torch.full((rows * (experts + 5) + 1,), 3.0, dtype=DTYPES[dt], device=DEV)
+    v = buf[1:].view(rows, experts + 5)[:, :experts]
+    v.copy_(x)
+    ws = torch.full((1 << 22,), 0xFF, dtype=torch.uint8, device=DEV)
+    for kw in (dict(), dict(workspace=ws), dict(workspace=ws)):
+        o2 = _run(v, k, 0.01, True, None, **kw)
+        assert all(torch.equal(o[n], o2[n]) for n in o)
+    dg = draw((rows, k), 82, 0.5).to(DEV)
+    route_backward(x, o["idx"], o["counts"], o["n"], v, dgates=dg, dloss=torch.tensor([1.7], device=DEV), coef=0.01)
+    assert torch.equal(v, dx)
+    v.fill_(3.0)
+    assert (buf == 3.0).all()
+    with pytest.raises(MuonError) as e:
+        _run(x, k, 0.01, True, None, workspace=ws[:16])
+    assert e.value.status == 5
+
+
+def test_graph_replays_and_streams():
+    rows, experts, k = 5000, 24, 3
+    xs = [_logits(rows, experts, "bf16", 91 + i) for i in range(3)]
+    x = xs[0].clone()
+    rec, dg = _outputs(rows, experts, k), draw((rows, k), 95).to(DEV)
+    dx = torch.zeros_like(x)
+
+    def step(src, o, d, stream=None):
+        route(src, o["idx"], o["gates"], o["counts"], o["n"], o["loss"], coef=0.1, prob_mean=o["mean"], stream=stream)
+        route_backward(src, o["idx"], o["counts"], o["n"], d, dgates=dg, coef=0.1, stream=stream)
+
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        step(x, rec, dx)
+    side = torch.cuda.Stream()
+    for src in xs + xs:
+        x.copy_(src)
+        graph.replay()
+        torch.cuda.synchronize()
+        o, d = _outputs(rows, experts, k), torch.empty_like(x)
+        torch.cuda.synchronize()
+        step(src, o, d, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(d, dx) and all(torch.equal(o[n], rec[n]) for n in o)
