@@ -11,6 +11,7 @@ dimensions lie one row stride apart (a column slice of a wider buffer, a
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -21,13 +22,17 @@ from .binding import MuonError, _check, _dtype_code, load_library
 def _matrix(t: torch.Tensor, what: str) -> Tuple[int, int, int]:
     """(rows, cols, row stride) of a matrix argument."""
     shape, stride = t.shape, t.stride()
+    if len(shape) == 2:
+        rows, cols = shape
+        ld, step = stride
+        if step != 1 and cols > 1:
+            raise MuonError(1, f"{what}: the last dimension is not contiguous")
+        return rows, cols, ld if rows > 1 else cols
     if not shape:
         raise MuonError(2, f"{what} needs at least one dimension")
     cols = shape[-1]
     if stride[-1] != 1 and cols > 1:
         raise MuonError(1, f"{what}: the last dimension is not contiguous")
-    if len(shape) == 2 and shape[0] > 1:
-        return shape[0], cols, stride[0]
     rows, ld = 1, None
     for n, s in zip(reversed(shape[:-1]), reversed(stride[:-1])):
         if n == 0:
@@ -44,7 +49,7 @@ def _matrix(t: torch.Tensor, what: str) -> Tuple[int, int, int]:
 
 def _same(t: torch.Tensor, like: torch.Tensor, what: str) -> int:
     """Row stride of a matrix that has to match `like`."""
-    if t.dtype != like.dtype:
+    if t.dtype is not like.dtype:
         raise MuonError(3, f"{what} has dtype {t.dtype}, expected {like.dtype}")
     if t.shape != like.shape:
         raise MuonError(2, f"{what} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
@@ -67,55 +72,53 @@ def _flat(t: Optional[torch.Tensor], n: int, dtypes, what: str) -> Optional[int]
 _F32, _I32, _MASK, _WORD = (torch.float32,), (torch.int32,), (torch.uint8, torch.bool), (torch.int64,)
 
 
-class _On:
-    """The device of a call's tensors, made current for its time, and the
-    stream to run on."""
-
-    def __init__(self, stream, *tensors):
-        dev = None
-        for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
+def _device(stream, *tensors) -> Tuple[int, int]:
+    """(device index, stream handle) of a call: that of its tensors, which must
+    share one, and their device's current stream unless one is given.  The
+    handle is read without making a Stream object, which would cost as much
+    as the launch (2.7 us of 9.7 for a one-row layer_norm)."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        d = t.get_device()
+        if d != dev:
+            if d < 0:
                 raise MuonError(1, "every tensor must be a device tensor")
-            if dev is None:
-                dev = t.device
-            elif t.device != dev:
-                raise MuonError(1, f"tensors on {dev} and {t.device}")
-        if stream is not None and stream.device != dev:
-            raise MuonError(1, f"a stream of {stream.device} for tensors on {dev}")
-        self.dev = dev
-        self.given = stream
-        self._guard = None
+            if dev is not None:
+                raise MuonError(1, f"tensors on devices {dev} and {d}")
+            dev = d
+    if stream is None:
+        return dev, torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise MuonError(1, f"a stream of {stream.device} for tensors on device {dev}")
+    return dev, stream.cuda_stream
 
-    def __enter__(self):
-        if torch.cuda.current_device() != self.dev.index:
-            self._guard = torch.cuda.device(self.dev)
-            self._guard.__enter__()
-        self.stream = self.given if self.given is not None else torch.cuda.current_stream()
-        self.handle = self.stream.cuda_stream
-        return self
 
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
-        return False
+def _call(dev: int, f, *args) -> None:
+    """The C call with the tensors' device current."""
+    if torch._C._cuda_getDevice() == dev:
+        _check(f(*args))
+    else:
+        with torch.cuda.device(dev):
+            _check(f(*args))
 
-    def workspace(self, given: Optional[torch.Tensor], need: int):
-        """(tensor, pointer, bytes): the caller's workspace, or one from
-        torch's allocator that belongs to the call's stream."""
-        if given is not None:
-            if not given.is_contiguous():
-                raise MuonError(5, "workspace is not contiguous")
-            return given, given.data_ptr(), given.numel() * given.element_size()
-        if need == 0:
-            return None, None, 0
-        if self.given is None:
-            t = torch.empty(need, dtype=torch.uint8, device=self.dev)
-        else:
-            with torch.cuda.stream(self.given):
-                t = torch.empty(need, dtype=torch.uint8, device=self.dev)
-        return t, t.data_ptr(), need
+
+def _workspace(given: Optional[torch.Tensor], need: int, stream, dev: int):
+    """(tensor, pointer, bytes): the caller's workspace, or one from torch's
+    allocator that belongs to the call's stream."""
+    if given is not None:
+        if not given.is_contiguous():
+            raise MuonError(5, "workspace is not contiguous")
+        return given, given.data_ptr(), given.numel() * given.element_size()
+    if need == 0:
+        return None, None, 0
+    if stream is None:
+        t = torch.empty(need, dtype=torch.uint8, device=dev)
+    else:
+        with torch.cuda.stream(stream):
+            t = torch.empty(need, dtype=torch.uint8, device=dev)
+    return t, t.data_ptr(), need
 
 
 def _param_code(gamma, beta, x) -> int:
@@ -145,15 +148,13 @@ def layer_norm(x, gamma, beta, y, *, mean=None, rstd=None, eps: float = 1e-5, st
     g = _param(gamma, None, cols, "gamma")
     b = _param(beta, gamma, cols, "beta")
     m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
-    with _On(stream, x, y, gamma, beta, mean, rstd) as on:
-        _check(load_library().muon_layer_norm_fwd(x.data_ptr(), ld, _dtype_code(x.dtype), g, b,
-                                                  _param_code(gamma, beta, x), rows, cols, eps, y.data_ptr(), ld_y, m,
-                                                  r, on.handle))
+    dev, st = _device(stream, x, y, gamma, beta, mean, rstd)
+    _call(dev, load_library().muon_layer_norm_fwd, x.data_ptr(), ld, _dtype_code(x.dtype), g, b,
+          _param_code(gamma, beta, x), rows, cols, eps, y.data_ptr(), ld_y, m, r, st)
 
 
-def _norm_workspace(rows: int, cols: int, wanted: bool) -> int:
-    if not wanted:
-        return 0
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(rows: int, cols: int) -> int:
     n = ctypes.c_size_t()
     _check(load_library().muon_layer_norm_workspace_bytes(rows, cols, ctypes.byref(n)))
     return n.value
@@ -173,12 +174,10 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, dx, *, dgamma=None, dbeta=None
     ld_dy, ld_dx = _same(dy, x, "dy"), _same(dx, x, "dx")
     code, (g, dg, db) = _grad_params(gamma, dgamma, dbeta, x, cols)
     m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
-    with _On(stream, x, dy, dx, gamma, mean, rstd, dgamma, dbeta, workspace) as on:
-        need = _norm_workspace(rows, cols, dg is not None or db is not None)
-        keep, ws, ws_bytes = on.workspace(workspace, need)
-        _check(load_library().muon_layer_norm_bwd(dy.data_ptr(), ld_dy, x.data_ptr(), ld, _dtype_code(x.dtype), g,
-                                                  code, m, r, rows, cols, dx.data_ptr(), ld_dx, dg, db, ws, ws_bytes,
-                                                  on.handle))
+    dev, st = _device(stream, x, dy, dx, gamma, mean, rstd, dgamma, dbeta, workspace)
+    keep, ws, ws_bytes = _workspace(workspace, _norm_workspace(rows, cols) if dg or db else 0, stream, dev)
+    _call(dev, load_library().muon_layer_norm_bwd, dy.data_ptr(), ld_dy, x.data_ptr(), ld, _dtype_code(x.dtype), g,
+          code, m, r, rows, cols, dx.data_ptr(), ld_dx, dg, db, ws, ws_bytes, st)
 
 
 def dropout(x, out, *, p: float, seed: int, offset: int = 0, offset_dev: Optional[torch.Tensor] = None,
@@ -191,10 +190,10 @@ def dropout(x, out, *, p: float, seed: int, offset: int = 0, offset_dev: Optiona
     ld_out = _same(out, x, "out")
     ld_res = 0 if residual is None else _same(residual, x, "residual")
     od = _flat(offset_dev, 1, _WORD, "offset_dev")
-    with _On(stream, x, out, residual, offset_dev) as on:
-        _check(load_library().muon_dropout(x.data_ptr(), ld, None if residual is None else residual.data_ptr(),
-                                           ld_res, _dtype_code(x.dtype), rows, cols, p, _u64(seed, "seed"),
-                                           _u64(offset, "offset"), od, out.data_ptr(), ld_out, on.handle))
+    dev, st = _device(stream, x, out, residual, offset_dev)
+    _call(dev, load_library().muon_dropout, x.data_ptr(), ld, None if residual is None else residual.data_ptr(), ld_res,
+          _dtype_code(x.dtype), rows, cols, p, _u64(seed, "seed"), _u64(offset, "offset"), od, out.data_ptr(), ld_out,
+          st)
 
 
 def dropout_add_layer_norm(x, residual, gamma, beta, h, y, *, p: float, seed: int, offset: int = 0,
@@ -209,11 +208,10 @@ def dropout_add_layer_norm(x, residual, gamma, beta, h, y, *, p: float, seed: in
     b = _param(beta, gamma, cols, "beta")
     m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
     od = _flat(offset_dev, 1, _WORD, "offset_dev")
-    with _On(stream, x, residual, gamma, beta, h, y, mean, rstd, offset_dev) as on:
-        _check(load_library().muon_dropout_add_layer_norm_fwd(
-            x.data_ptr(), ld, residual.data_ptr(), ld_res, _dtype_code(x.dtype), g, b, _param_code(gamma, beta, x),
-            rows, cols, eps, p, _u64(seed, "seed"), _u64(offset, "offset"), od, h.data_ptr(), ld_h, y.data_ptr(),
-            ld_y, m, r, on.handle))
+    dev, st = _device(stream, x, residual, gamma, beta, h, y, mean, rstd, offset_dev)
+    _call(dev, load_library().muon_dropout_add_layer_norm_fwd, x.data_ptr(), ld, residual.data_ptr(), ld_res,
+          _dtype_code(x.dtype), g, b, _param_code(gamma, beta, x), rows, cols, eps, p, _u64(seed, "seed"),
+          _u64(offset, "offset"), od, h.data_ptr(), ld_h, y.data_ptr(), ld_y, m, r, st)
 
 
 def dropout_add_layer_norm_backward(dy, h, gamma, mean, rstd, dx, dresidual, *, p: float, seed: int, offset: int = 0,
@@ -228,13 +226,12 @@ def dropout_add_layer_norm_backward(dy, h, gamma, mean, rstd, dx, dresidual, *, 
     code, (g, dg, db) = _grad_params(gamma, dgamma, dbeta, h, cols)
     m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
     od = _flat(offset_dev, 1, _WORD, "offset_dev")
-    with _On(stream, h, dy, dx, dresidual, dh, gamma, mean, rstd, dgamma, dbeta, offset_dev, workspace) as on:
-        need = _norm_workspace(rows, cols, dg is not None or db is not None)
-        keep, ws, ws_bytes = on.workspace(workspace, need)
-        _check(load_library().muon_dropout_add_layer_norm_bwd(
-            dy.data_ptr(), ld_dy, None if dh is None else dh.data_ptr(), ld_dh, h.data_ptr(), ld,
-            _dtype_code(h.dtype), g, code, m, r, rows, cols, p, _u64(seed, "seed"), _u64(offset, "offset"), od,
-            dx.data_ptr(), ld_dx, dresidual.data_ptr(), ld_dres, dg, db, ws, ws_bytes, on.handle))
+    dev, st = _device(stream, h, dy, dx, dresidual, dh, gamma, mean, rstd, dgamma, dbeta, offset_dev, workspace)
+    keep, ws, ws_bytes = _workspace(workspace, _norm_workspace(rows, cols) if dg or db else 0, stream, dev)
+    _call(dev, load_library().muon_dropout_add_layer_norm_bwd, dy.data_ptr(), ld_dy,
+          None if dh is None else dh.data_ptr(), ld_dh, h.data_ptr(), ld, _dtype_code(h.dtype), g, code, m, r, rows,
+          cols, p, _u64(seed, "seed"), _u64(offset, "offset"), od, dx.data_ptr(), ld_dx, dresidual.data_ptr(), ld_dres,
+          dg, db, ws, ws_bytes, st)
 
 
 def _choices(t: torch.Tensor, rows: int, dtypes, what: str, k: Optional[int] = None) -> int:
@@ -244,6 +241,13 @@ def _choices(t: torch.Tensor, rows: int, dtypes, what: str, k: Optional[int] = N
         raise MuonError(2, f"{what} has shape {tuple(t.shape)}, expected [{rows}, {'k' if k is None else k}]")
     _flat(t, rows * n, dtypes, what)
     return n
+
+
+@functools.lru_cache(maxsize=256)
+def _route_workspace(rows: int, experts: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().muon_route_workspace_bytes(rows, experts, ctypes.byref(n)))
+    return n.value
 
 
 def route(logits, indices, gates, counts, n_tokens, loss, *, coef: float = 1.0, renorm: bool = True, valid=None,
@@ -257,14 +261,10 @@ def route(logits, indices, gates, counts, n_tokens, loss, *, coef: float = 1.0, 
     c, n = _flat(counts, experts, _I32, "counts"), _flat(n_tokens, 1, _I32, "n_tokens")
     lo, pm = _flat(loss, 1, _F32, "loss"), _flat(prob_mean, experts, _F32, "prob_mean")
     v = _flat(valid, rows, _MASK, "valid")
-    with _On(stream, logits, indices, gates, counts, n_tokens, loss, valid, prob_mean, workspace) as on:
-        lib = load_library()
-        need = ctypes.c_size_t()
-        _check(lib.muon_route_workspace_bytes(rows, experts, ctypes.byref(need)))
-        keep, ws, ws_bytes = on.workspace(workspace, need.value)
-        _check(lib.muon_route_fwd(logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, experts, k, v,
-                                  int(bool(renorm)), coef, indices.data_ptr(), gates.data_ptr(), c, n, pm, lo, ws,
-                                  ws_bytes, on.handle))
+    dev, st = _device(stream, logits, indices, gates, counts, n_tokens, loss, valid, prob_mean, workspace)
+    keep, ws, ws_bytes = _workspace(workspace, _route_workspace(rows, experts), stream, dev)
+    _call(dev, load_library().muon_route_fwd, logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, experts, k, v,
+          1 if renorm else 0, coef, indices.data_ptr(), gates.data_ptr(), c, n, pm, lo, ws, ws_bytes, st)
 
 
 def route_backward(logits, indices, counts, n_tokens, dlogits, *, dgates=None, dloss=None, coef: float = 1.0,
@@ -279,8 +279,7 @@ def route_backward(logits, indices, counts, n_tokens, dlogits, *, dgates=None, d
         _choices(dgates, rows, _F32, "dgates", k)
     c, n = _flat(counts, experts, _I32, "counts"), _flat(n_tokens, 1, _I32, "n_tokens")
     dl, v = _flat(dloss, 1, _F32, "dloss"), _flat(valid, rows, _MASK, "valid")
-    with _On(stream, logits, indices, counts, n_tokens, dlogits, dgates, dloss, valid) as on:
-        _check(load_library().muon_route_bwd(logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, experts, k, v,
-                                             int(bool(renorm)), coef, indices.data_ptr(), c, n,
-                                             None if dgates is None else dgates.data_ptr(), dl, dlogits.data_ptr(),
-                                             ld_d, on.handle))
+    dev, st = _device(stream, logits, indices, counts, n_tokens, dlogits, dgates, dloss, valid)
+    _call(dev, load_library().muon_route_bwd, logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, experts, k, v,
+          1 if renorm else 0, coef, indices.data_ptr(), c, n, None if dgates is None else dgates.data_ptr(), dl,
+          dlogits.data_ptr(), ld_d, st)
