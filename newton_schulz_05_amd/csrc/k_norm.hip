@@ -230,23 +230,31 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
 }
 
 // Sums the workgroups' partial dgamma (blockIdx.y == 0) and dbeta over
-// `parts`, 64 columns a workgroup, 16 slices of the parts joined in order.
+// `parts` <= 512: 32 columns a workgroup, 32 slices of the parts, whose at
+// most 16 loads are all in flight at once; the slices are joined in order.
+constexpr int kGradCols = 32, kGradSlices = 32;
 template <typename W>
-__global__ __launch_bounds__(1024) void norm_grad_kernel(const float* __restrict__ part, int parts, int cols, W* dgamma,
-                                                         W* dbeta) {
-  __shared__ float sums[16][64];
+__global__ __launch_bounds__(kGradCols* kGradSlices) void norm_grad_kernel(const float* part, int parts, int cols,
+                                                                           W* dgamma, W* dbeta) {
+  __shared__ float sums[kGradSlices][kGradCols];
   W* out = blockIdx.y ? dbeta : dgamma;
   if (!out) return;
-  const int lane = threadIdx.x & 63, slice = threadIdx.x >> 6;
-  const int c = int(blockIdx.x) * 64 + lane;
-  float s = 0.0f;
-  if (c < cols)
-    for (int p = slice; p < parts; p += 16) s += part[(int64_t(p) * 2 + blockIdx.y) * cols + c];
+  const int lane = threadIdx.x % kGradCols, slice = threadIdx.x / kGradCols;
+  const int c = int(blockIdx.x) * kGradCols + lane;
+  float v[kNormMaxParts / kGradSlices];
+#pragma unroll
+  for (int i = 0; i < kNormMaxParts / kGradSlices; ++i) {
+    const int p = slice + kGradSlices * i;
+    v[i] = c < cols && p < parts ? part[(int64_t(p) * 2 + blockIdx.y) * cols + c] : 0.0f;
+  }
+  float s = v[0];
+#pragma unroll
+  for (int i = 1; i < kNormMaxParts / kGradSlices; ++i) s += v[i];
   sums[slice][lane] = s;
   __syncthreads();
   if (slice == 0 && c < cols) {
 #pragma unroll
-    for (int i = 1; i < 16; ++i) s += sums[i][lane];
+    for (int i = 1; i < kGradSlices; ++i) s += sums[i][lane];
     Elem<W>::store(out + c, s);
   }
 }
@@ -264,8 +272,8 @@ template <typename T, typename W, bool FUSED> struct NormLaunch {
     const int64_t parts = norm_bwd_parts(a.rows, a.cols);
     hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, WG, FUSED>), dim3(unsigned(parts)), dim3(WG), 0, st, a);
     if (parts > 1 && (a.dgamma || a.dbeta))
-      hipLaunchKernelGGL((norm_grad_kernel<W>), dim3(unsigned((a.cols + 63) / 64), 2), dim3(1024), 0, st, a.part,
-                         int(parts), a.cols, (W*)a.dgamma, (W*)a.dbeta);
+      hipLaunchKernelGGL((norm_grad_kernel<W>), dim3(unsigned((a.cols + kGradCols - 1) / kGradCols), 2),
+                         dim3(kGradCols * kGradSlices), 0, st, a.part, int(parts), a.cols, (W*)a.dgamma, (W*)a.dbeta);
   }
   static hipError_t fwd(const NormFwdArgs& a, hipStream_t st) {
     switch (norm_row_threads(a.cols)) {

@@ -24,9 +24,10 @@ constexpr int norm_bwd_threads(int64_t cols) { return cols <= 8192 ? 512 : 1024;
 // Workgroups of the backward pass, each of which leaves one partial sum of
 // the gradients of gamma and beta: at most two for each of 256 compute units
 // (a fixed number, so that results do not depend on the device's).
+constexpr int kNormMaxParts = 512;
 inline int64_t norm_bwd_parts(int64_t rows, int64_t cols) {
   const int64_t per = norm_bwd_threads(cols) / norm_row_threads(cols);
-  return std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, 512));
+  return std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, kNormMaxParts));
 }
 
 // Lanes that share one token of the router: each holds `per` experts.
