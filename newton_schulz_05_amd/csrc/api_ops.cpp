@@ -128,6 +128,7 @@ muon_status norm_bwd(const void* dy, int64_t ld_dy, const void* dh, int64_t ld_d
   muon::NormBwdArgs a{};
   a.dy = dy; a.x = x; a.dh = drop ? dh : nullptr; a.gamma = gamma; a.mean = mean; a.rstd = rstd;
   a.dx = dx; a.dres = dres; a.dgamma = dgamma; a.dbeta = dbeta; a.part = (float*)workspace;
+  a.parts = muon::norm_bwd_split(rows, cols).parts;
   a.rows = rows; a.ld_dy = ld_dy; a.ld_x = ld_x; a.ld_dh = ld_dh; a.ld_dx = ld_dx; a.ld_dres = ld_dres;
   a.cols = int(cols);
   if (drop) a.drop = *drop;

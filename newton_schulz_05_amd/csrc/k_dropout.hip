@@ -10,7 +10,6 @@ namespace muon {
 namespace {
 
 constexpr int kDropThreads = 256;
-constexpr int kDropGrid = 2048;  // 8 workgroups of 4 waves on each of 256 CUs
 
 // Thread v of the grid takes vectors v, v + step, ... of 8 elements, counted
 // row by row; the step is split into rows and vectors on the host, so that a
@@ -48,9 +47,9 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(DropoutArgs a, ui
 template <typename T> void launch(const DropoutArgs& a, hipStream_t st) {
   const uint64_t per_row = uint64_t(a.cols + 7) / 8;
   // a lone long row and many short ones alike: enough workgroups for all
-  // vectors, at most kDropGrid
+  // vectors, at most kOpsMaxGrid
   const uint64_t total = per_row * uint64_t(a.rows);
-  const uint64_t grid = std::min<uint64_t>((total + kDropThreads - 1) / kDropThreads, kDropGrid);
+  const uint64_t grid = std::min<uint64_t>((total + kDropThreads - 1) / kDropThreads, uint64_t(kOpsMaxGrid));
   const uint64_t step = grid * kDropThreads;
   const uint32_t sr = uint32_t(step / per_row), sv = uint32_t(step % per_row);
   if (a.res)

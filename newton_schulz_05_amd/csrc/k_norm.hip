@@ -42,43 +42,68 @@ template <int NT> __device__ __forceinline__ float row_sum(float v, float* red) 
   }
 }
 
-template <typename T> __device__ __forceinline__ void load_param(const void* p, int col, int n, float dflt,
-                                                                 float (&v)[8]) {
-  if (p) {
-    unpack8(load8((const T*)p + col, n), v);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = dflt;
-  }
+// Which of the workgroup's row groups a thread is in: the same for a whole
+// wave from 64 threads a row on, so that row addresses stay in scalar
+// registers (as lane values they spilled above 8192 columns).
+template <int NT> __device__ __forceinline__ int row_group() {
+  const int g = threadIdx.x / NT;
+  return NT >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
 }
 
+// gamma or beta as stored; `dflt` in the place of a null one.
+template <typename W> __device__ __forceinline__ Raw8<W> load_param(const void* p, unsigned col, int n) {
+  return load8((const W*)p + col, p ? n : 0);
+}
+template <typename W>
+__device__ __forceinline__ void unpack_param(const Raw8<W>& r, const void* p, float dflt, float (&v)[8]) {
+  unpack8(r, v);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = p ? v[i] : dflt;
+}
+
+// Bound by memory: x is read and y written once (16384 x 4096 bf16: 5 TB/s,
+// the rate of a large copy).  gamma and beta come from the cache, their loads
+// behind those of x; four vectors a thread (above 16384 columns) leave no
+// registers for them during the reductions.
 template <typename T, typename W, int NT, int NV, int WG, bool FUSED>
 __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdArgs a) {
   constexpr int RPB = WG / NT;
+  constexpr bool EARLY = NV <= 2;
   __shared__ float red[2][WG / 64];
-  const int t = threadIdx.x % NT, sub = threadIdx.x / NT;
+  const int t = threadIdx.x % NT, sub = row_group<NT>();
   const int cols = a.cols;
-  float gam[NV][8], bet[NV][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int col = 8 * (i * NT + t);
-    load_param<W>(a.gamma, col, cols - col, 1.0f, gam[i]);
-    load_param<W>(a.beta, col, cols - col, 0.0f, bet[i]);
-  }
   const uint64_t off = FUSED ? drop_offset(a.drop) : 0;
   for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < a.rows; row0 += int64_t(gridDim.x) * RPB) {
     const int64_t row = row0 + sub;
     const bool live = row < a.rows;
+    Raw8<T> xr[NV], rr[NV];
+    Raw8<W> gr[NV], br[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const unsigned col = 8 * (i * NT + t);
+      const int n = live ? cols - int(col) : 0;
+      xr[i] = load8((const T*)a.x + row * a.ld_x + col, n);
+      if constexpr (FUSED) rr[i] = load8((const T*)a.res + row * a.ld_res + col, n);
+    }
+    if constexpr (EARLY) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const unsigned col = 8 * (i * NT + t);
+        gr[i] = load_param<W>(a.gamma, col, cols - int(col));
+        br[i] = load_param<W>(a.beta, col, cols - int(col));
+      }
+    }
     float v[NV][8];
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = 8 * (i * NT + t), n = live ? cols - col : 0;
-      unpack8(load8((const T*)a.x + row * a.ld_x + col, n), v[i]);
+      const unsigned col = 8 * (i * NT + t);
+      const int n = live ? cols - int(col) : 0;
+      unpack8(xr[i], v[i]);
       if constexpr (FUSED) {
         float rv[8];
-        unpack8(load8((const T*)a.res + row * a.ld_res + col, n), rv);
-        const u32x4 w = drop_draws(a.drop, off, uint32_t(row), uint32_t(col / 8));
+        unpack8(rr[i], rv);
+        const u32x4 w = drop_draws(a.drop, off, uint32_t(row), col / 8);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
           v[i][j] = drop_keeps(w, j, a.drop.thresh) ? fmaf(v[i][j], a.drop.scale, rv[j]) : rv[j];
@@ -105,9 +130,17 @@ __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdArgs a) {
     const float rstd = 1.0f / sqrtf(row_sum<NT>(q, red[1]) / float(cols) + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = 8 * (i * NT + t), n = live ? cols - col : 0;
+      const unsigned col = 8 * (i * NT + t);
+      const int n = live ? cols - int(col) : 0;
+      if constexpr (!EARLY) {
+        gr[i] = load_param<W>(a.gamma, col, n);
+        br[i] = load_param<W>(a.beta, col, n);
+      }
+      float gv[8], bv[8];
+      unpack_param(gr[i], a.gamma, 1.0f, gv);
+      unpack_param(br[i], a.beta, 0.0f, bv);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * rstd, gam[i][j], bet[i][j]);
+      for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * rstd, gv[j], bv[j]);
       store8((T*)a.y + row * a.ld_y + col, n, pack8(v[i], (const T*)nullptr));
     }
     if (live && t == 0) {
@@ -117,121 +150,233 @@ __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdArgs a) {
   }
 }
 
-// One workgroup takes every gridDim.x-th group of WG / NT rows and keeps the
-// sums of its columns' dgamma and dbeta in registers; its row groups are
-// joined in LDS in a fixed order, and the workgroups' sums by
-// norm_grad_kernel.  A lone workgroup writes the gradients itself.
-template <typename T, typename W, int NT, int NV, int WG, bool FUSED>
-__global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
-  constexpr int RPB = WG / NT;
-  __shared__ float red[2][WG / 64];
-  __shared__ float sums[RPB > 1 ? RPB : 1][RPB > 1 ? 8 * NT * NV : 1];
-  const int t = threadIdx.x % NT, sub = threadIdx.x / NT;
-  const int cols = a.cols;
-  float gam[NV][8], dg[NV][8], db[NV][8];
+// Two sums over the NT threads of a row with one barrier (see row_sum; `red`
+// alternates from row to row).
+template <int NT> __device__ __forceinline__ void row_sum2(float& a, float& b, float (*red)[2]) {
+  if constexpr (NT <= 64) {
+    a = lane_sum<NT>(a);
+    b = lane_sum<NT>(b);
+  } else {
+    constexpr int NW = NT / 64;
+    a = lane_sum<64>(a);
+    b = lane_sum<64>(b);
+    const int wave = threadIdx.x / 64, first = wave / NW * NW;
+    if (threadIdx.x % 64 == 0) {
+      red[wave][0] = a;
+      red[wave][1] = b;
+    }
+    __syncthreads();
+    a = red[first][0];
+    b = red[first][1];
+#pragma unroll
+    for (int i = 1; i < NW; ++i) {
+      a += red[first + i][0];
+      b += red[first + i][1];
+    }
+  }
+}
+
+// One thread's vectors of a row.
+template <typename T, int NV> struct RowPart {
+  Raw8<T> x[NV], dy[NV], dh[NV];
+  float mean, rstd;
+};
+
+template <typename T, int NT, int NV, bool FUSED>
+__device__ __forceinline__ void fetch_row(const NormBwdArgs& a, int64_t row, int t, RowPart<T, NV>& r) {
+  const bool live = row < a.rows;
+  r.mean = live ? a.mean[row] : 0.0f;
+  r.rstd = live ? a.rstd[row] : 0.0f;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
-    const int col = 8 * (i * NT + t);
-    load_param<W>(a.gamma, col, cols - col, 1.0f, gam[i]);
+    const unsigned col = 8 * (i * NT + opaque(t));
+    const int n = live ? a.cols - int(col) : 0;
+    r.x[i] = load8((const T*)a.x + row * a.ld_x + col, n);
+    r.dy[i] = load8((const T*)a.dy + row * a.ld_dy + col, n);
+    if constexpr (FUSED)
+      if (a.dh) r.dh[i] = load8((const T*)a.dh + row * a.ld_dh + col, n);
+  }
+}
+
+// Hides a vector's bits from the optimiser: what was computed from them before
+// a row's reduction is computed again after it, instead of being kept in
+// registers over it (the unpacked row is twice the packed one in bf16).
+__device__ __forceinline__ void hide(Raw8<uint16_t>& v) { asm volatile("" : "+v"(v.w)); }
+__device__ __forceinline__ void hide(Raw8<float>& v) { asm volatile("" : "+v"(v.a), "+v"(v.b)); }
+
+// dx of one vector, and with FUSED dres; returns nothing else.
+template <typename T, typename W, bool FUSED>
+__device__ __forceinline__ void emit_dx(const NormBwdArgs& a, int64_t row, unsigned col, int n, const Raw8<T>& xr,
+                                        const Raw8<T>& dr, const Raw8<T>& hr, const float (&gv)[8], float mean,
+                                        float rstd, float c1, float c2, uint64_t off) {
+  float xv[8], dv[8];
+  unpack8(xr, xv);
+  unpack8(dr, dv);
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float xh = (xv[j] - mean) * rstd, g = dv[j] * gv[j];
+    dv[j] = rstd * fmaf(-xh, c2, g - c1);
+  }
+  if constexpr (FUSED) {
+    if (a.dh) {
+      unpack8(hr, xv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) dv[j] += xv[j];
+    }
+    store8((T*)a.dres + row * a.ld_dres + col, n, pack8(dv, (const T*)nullptr));
+    const u32x4 w = drop_draws(a.drop, off, uint32_t(row), col / 8);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dv[j] = drop_keeps(w, j, a.drop.thresh) ? dv[j] * a.drop.scale : 0.0f;
+  }
+  store8((T*)a.dx + row * a.ld_dx + col, n, pack8(dv, (const T*)nullptr));
+}
+
+// Workgroups of WG threads take every gridDim.x-th group of WG / NT rows and,
+// with SUMS, keep the sums of their columns' dgamma and dbeta in registers; a
+// workgroup's row groups are joined in LDS in a fixed order, and the
+// workgroups' sums by norm_grad_kernel.  A lone workgroup writes the gradients
+// itself.
+//
+// Bound by memory: x and dy are read and dx written once.  For many rows one
+// workgroup of 1024 threads on each of 256 units, one 16-byte vector a thread
+// (16 sums to keep) measured best: at 16384 x 8192 bf16 148.7 us against
+// 159.8 with two workgroups of 512 threads and two vectors, and 163.1 without
+// the next row's loads in flight (AHEAD) over the reduction; at 16384 x 4096
+// 77.4 against 105.6.  The fused pass has a third stream in flight and gains
+// nothing from AHEAD (125.1 without, 127.6 with); with two vectors (8193 to
+// 16384 columns) AHEAD has no registers left.  Wider rows have none for the
+// sums: see norm_cols_kernel.
+template <typename T, typename W, int NT, int NV, int WG, bool FUSED, bool SUMS>
+__global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
+  constexpr int RPB = WG / NT;
+  constexpr bool AHEAD = SUMS && !FUSED && (NV == 1 || (NV == 2 && sizeof(T) == 2));
+  __shared__ float red[2][WG / 64][2];
+  __shared__ float sums[SUMS && RPB > 1 ? RPB : 1][SUMS && RPB > 1 ? 8 * NT * NV : 1];
+  const int t = threadIdx.x % NT, sub = row_group<NT>();
+  const int cols = a.cols;
+  Raw8<W> gr[NV];
+  float dg[NV][8], db[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const unsigned col = 8 * (i * NT + opaque(t));
+    gr[i] = load_param<W>(a.gamma, col, cols - int(col));
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.0f;
   }
   const uint64_t off = FUSED ? drop_offset(a.drop) : 0;
   const float inv = 1.0f / float(cols);
-  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < a.rows; row0 += int64_t(gridDim.x) * RPB) {
+  const int64_t step = int64_t(gridDim.x) * RPB;
+  RowPart<T, NV> r;
+  if constexpr (AHEAD) fetch_row<T, NT, NV, FUSED>(a, int64_t(blockIdx.x) * RPB + sub, t, r);
+  int side = 0;
+  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < a.rows; row0 += step) {
     const int64_t row = row0 + sub;
     const bool live = row < a.rows;
-    const float mean = live ? a.mean[row] : 0.0f, rstd = live ? a.rstd[row] : 0.0f;
-    Raw8<T> xr[NV], dr[NV];
+    RowPart<T, NV> next;
+    if constexpr (AHEAD) fetch_row<T, NT, NV, FUSED>(a, row + step, t, next);
+    else fetch_row<T, NT, NV, FUSED>(a, row, t, r);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = 8 * (i * NT + t), n = live ? cols - col : 0;
-      xr[i] = load8((const T*)a.x + row * a.ld_x + col, n);
-      dr[i] = load8((const T*)a.dy + row * a.ld_dy + col, n);
-    }
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      float xv[8], dv[8];
-      unpack8(xr[i], xv);
-      unpack8(dr[i], dv);
+      float xv[8], dv[8], gv[8];
+      unpack8(r.x[i], xv);
+      unpack8(r.dy[i], dv);
+      unpack_param(gr[i], a.gamma, 1.0f, gv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
         // dy is 0 in the elements behind the row's end
-        const float xh = (xv[j] - mean) * rstd, g = dv[j] * gam[i][j];
+        const float xh = (xv[j] - r.mean) * r.rstd, g = dv[j] * gv[j];
         s1 += g;
         s2 = fmaf(g, xh, s2);
-        dg[i][j] = fmaf(dv[j], xh, dg[i][j]);
-        db[i][j] += dv[j];
+        if constexpr (SUMS) {
+          dg[i][j] = fmaf(dv[j], xh, dg[i][j]);
+          db[i][j] += dv[j];
+        }
       }
     }
-    const float c1 = row_sum<NT>(s1, red[0]) * inv, c2 = row_sum<NT>(s2, red[1]) * inv;
+    row_sum2<NT>(s1, s2, red[side]);
+    side ^= 1;
+    const float c1 = s1 * inv, c2 = s2 * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-      const int col = 8 * (i * NT + t), n = live ? cols - col : 0;
-      float xv[8], dv[8];
-      unpack8(xr[i], xv);
-      unpack8(dr[i], dv);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float xh = (xv[j] - mean) * rstd, g = dv[j] * gam[i][j];
-        dv[j] = rstd * fmaf(-xh, c2, g - c1);
+      const unsigned col = 8 * (i * NT + opaque(t));
+      if constexpr (NV > 1) {
+        hide(r.x[i]);
+        hide(r.dy[i]);
+        hide(gr[i]);
       }
-      if constexpr (FUSED) {
-        if (a.dh) {
-          unpack8(load8((const T*)a.dh + row * a.ld_dh + col, n), xv);
-#pragma unroll
-          for (int j = 0; j < 8; ++j) dv[j] += xv[j];
-        }
-        store8((T*)a.dres + row * a.ld_dres + col, n, pack8(dv, (const T*)nullptr));
-        const u32x4 w = drop_draws(a.drop, off, uint32_t(row), uint32_t(col / 8));
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dv[j] = drop_keeps(w, j, a.drop.thresh) ? dv[j] * a.drop.scale : 0.0f;
-      }
-      store8((T*)a.dx + row * a.ld_dx + col, n, pack8(dv, (const T*)nullptr));
+      float gv[8];
+      unpack_param(gr[i], a.gamma, 1.0f, gv);
+      emit_dx<T, W, FUSED>(a, row, col, live ? cols - int(col) : 0, r.x[i], r.dy[i], r.dh[i], gv, r.mean, r.rstd, c1,
+                           c2, off);
     }
+    if constexpr (AHEAD) r = next;
   }
-  if (!a.dgamma && !a.dbeta) return;
-  const bool alone = gridDim.x == 1;
+  if constexpr (SUMS) {
+    if (!a.dgamma && !a.dbeta) return;
+    const bool alone = gridDim.x == 1;
 #pragma unroll
-  for (int part = 0; part < 2; ++part) {
-    float(&acc)[NV][8] = part ? db : dg;
-    if constexpr (RPB > 1) {
-      __syncthreads();
+    for (int part = 0; part < 2; ++part) {
+      float(&acc)[NV][8] = part ? db : dg;
+      void* own = part ? a.dbeta : a.dgamma;
+      float* to = a.part + (int64_t(blockIdx.x) * 2 + part) * cols;
+      if constexpr (RPB > 1) {
+        __syncthreads();
 #pragma unroll
-      for (int i = 0; i < NV; ++i)
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) sums[sub][8 * (i * NT + t) + j] = acc[i][j];
-      __syncthreads();
-    }
-    void* own = part ? a.dbeta : a.dgamma;
-    float* to = a.part + (int64_t(blockIdx.x) * 2 + part) * cols;
-    if constexpr (RPB > 1) {
-      for (int c = threadIdx.x; c < cols; c += WG) {
-        float s = sums[0][c];
+          for (int j = 0; j < 8; ++j) sums[sub][8 * (i * NT + t) + j] = acc[i][j];
+        __syncthreads();
+        for (int c = threadIdx.x; c < cols; c += WG) {
+          float s = sums[0][c];
 #pragma unroll
-        for (int g = 1; g < RPB; ++g) s += sums[g][c];
-        if (!alone) to[c] = s;
-        else if (own) Elem<W>::store((W*)own + c, s);
-      }
-    } else {
-#pragma unroll
-      for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int c = 8 * (i * NT + t) + j;
-          if (c < cols) {
-            if (!alone) to[c] = acc[i][j];
-            else if (own) Elem<W>::store((W*)own + c, acc[i][j]);
-          }
+          for (int g = 1; g < RPB; ++g) s += sums[g][c];
+          if (!alone) to[c] = s;
+          else if (own) Elem<W>::store((W*)own + c, s);
         }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int c = 8 * (i * NT + t);
+          if (!alone) store8(to + c, cols - c, pack8(acc[i], (const float*)nullptr));
+          else if (own) store8((W*)own + c, cols - c, pack8(acc[i], (const W*)nullptr));
+        }
+      }
     }
   }
 }
 
+// The sums of rows wider than 16384 columns, in a pass of its own over x and
+// dy: blockIdx.x takes 2048 columns, a vector a thread, and blockIdx.y every
+// gridDim.y-th row.  With the sums in norm_bwd_kernel four vectors a thread
+// spilled (2048 x 32768 bf16: 288 us).
+template <typename T>
+__global__ __launch_bounds__(256) void norm_cols_kernel(NormBwdArgs a) {
+  const unsigned col = 8 * (blockIdx.x * 256 + threadIdx.x);
+  const int n = a.cols - int(col);
+  float dg[8], db[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) dg[j] = db[j] = 0.0f;
+#pragma unroll 4
+  for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
+    float xv[8], dv[8];
+    unpack8(load8((const T*)a.x + row * a.ld_x + col, n), xv);
+    unpack8(load8((const T*)a.dy + row * a.ld_dy + col, n), dv);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      dg[j] = fmaf(dv[j], (xv[j] - mean) * rstd, dg[j]);
+      db[j] += dv[j];
+    }
+  }
+  float* to = a.part + int64_t(blockIdx.y) * 2 * a.cols;
+  store8(to + col, n, pack8(dg, (const float*)nullptr));
+  store8(to + a.cols + col, n, pack8(db, (const float*)nullptr));
+}
+
 // Sums the workgroups' partial dgamma (blockIdx.y == 0) and dbeta over
-// `parts` <= 512: 32 columns a workgroup, 32 slices of the parts, whose at
-// most 16 loads are all in flight at once; the slices are joined in order.
+// `parts` <= 256: 32 columns a workgroup, 32 slices of the parts, whose at
+// most 8 loads are all in flight at once; the slices are joined in order.
 constexpr int kGradCols = 32, kGradSlices = 32;
 template <typename W>
 __global__ __launch_bounds__(kGradCols* kGradSlices) void norm_grad_kernel(const float* part, int parts, int cols,
@@ -259,40 +404,62 @@ __global__ __launch_bounds__(kGradCols* kGradSlices) void norm_grad_kernel(const
   }
 }
 
-constexpr int kFwdGrid = 2048;
-
 template <typename T, typename W, bool FUSED> struct NormLaunch {
+  // One group of rows a workgroup: new workgroups keep loads in flight while
+  // others reduce (16384 x 4096 bf16: 48.8 us; 52.6 to 66.3 with the rows
+  // dealt to 512 .. 2048 workgroups that loop).
   template <int NT, int NV> static void fwd(const NormFwdArgs& a, hipStream_t st) {
     constexpr int WG = NT < 256 ? 256 : NT;
     const int64_t need = (a.rows + WG / NT - 1) / (WG / NT);
-    hipLaunchKernelGGL((norm_fwd_kernel<T, W, NT, NV, WG, FUSED>), dim3(unsigned(std::min<int64_t>(need, kFwdGrid))),
+    hipLaunchKernelGGL((norm_fwd_kernel<T, W, NT, NV, WG, FUSED>), dim3(unsigned(std::min(need, kOpsMaxGrid))),
                        dim3(WG), 0, st, a);
   }
   template <int NT, int NV, int WG> static void bwd(const NormBwdArgs& a, hipStream_t st) {
-    const int64_t parts = norm_bwd_parts(a.rows, a.cols);
-    hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, WG, FUSED>), dim3(unsigned(parts)), dim3(WG), 0, st, a);
-    if (parts > 1 && (a.dgamma || a.dbeta))
-      hipLaunchKernelGGL((norm_grad_kernel<W>), dim3(unsigned((a.cols + kGradCols - 1) / kGradCols), 2),
-                         dim3(kGradCols * kGradSlices), 0, st, a.part, int(parts), a.cols, (W*)a.dgamma, (W*)a.dbeta);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, WG, FUSED, true>), dim3(unsigned(a.parts)), dim3(WG), 0, st, a);
+  }
+  // Few rows: as many workgroups as there are row groups of 256 threads (see
+  // norm_bwd_split).
+  template <int NT> static void bwd(const NormBwdArgs& a, int wg, hipStream_t st) {
+    constexpr int FEW = NT < 256 ? 256 : NT;
+    wg == 1024 ? bwd<NT, 1, 1024>(a, st) : bwd<NT, 1, FEW>(a, st);
   }
   static hipError_t fwd(const NormFwdArgs& a, hipStream_t st) {
-    switch (norm_row_threads(a.cols)) {
-      case 16: fwd<16, 1>(a, st); break;
-      case 64: a.cols <= 512 ? fwd<64, 1>(a, st) : fwd<64, 2>(a, st); break;
-      case 256: a.cols <= 2048 ? fwd<256, 1>(a, st) : fwd<256, 2>(a, st); break;
-      case 512: fwd<512, 2>(a, st); break;
-      default: a.cols <= 16384 ? fwd<1024, 2>(a, st) : fwd<1024, 4>(a, st); break;
-    }
+    if (a.cols <= 128) fwd<16, 1>(a, st);
+    else if (a.cols <= 512) fwd<64, 1>(a, st);
+    else if (a.cols <= 1024) fwd<64, 2>(a, st);
+    else if (a.cols <= 2048) fwd<256, 1>(a, st);
+    else if (a.cols <= 4096) fwd<256, 2>(a, st);
+    else if (a.cols <= 8192) fwd<512, 2>(a, st);
+    else if (a.cols <= 16384) fwd<1024, 2>(a, st);
+    else fwd<1024, 4>(a, st);
     return hipGetLastError();
   }
   static hipError_t bwd(const NormBwdArgs& a, hipStream_t st) {
-    switch (norm_row_threads(a.cols)) {
-      case 16: bwd<16, 1, 512>(a, st); break;
-      case 64: a.cols <= 512 ? bwd<64, 1, 512>(a, st) : bwd<64, 2, 512>(a, st); break;
-      case 256: a.cols <= 2048 ? bwd<256, 1, 512>(a, st) : bwd<256, 2, 512>(a, st); break;
-      case 512: bwd<512, 2, 512>(a, st); break;
-      default: a.cols <= 16384 ? bwd<1024, 2, 1024>(a, st) : bwd<1024, 4, 1024>(a, st); break;
+    const NormBwdSplit sp = norm_bwd_split(a.rows, a.cols);
+    const bool grads = a.dgamma || a.dbeta;
+    switch (sp.row_threads) {
+      case 16: bwd<16>(a, sp.threads, st); break;
+      case 64: bwd<64>(a, sp.threads, st); break;
+      case 128: bwd<128>(a, sp.threads, st); break;
+      case 256: bwd<256>(a, sp.threads, st); break;
+      case 512: bwd<512>(a, sp.threads, st); break;
+      default:
+        if (a.cols <= 8192) {
+          bwd<1024, 1, 1024>(a, st);
+        } else if (a.cols <= 16384) {
+          bwd<1024, 2, 1024>(a, st);
+        } else {
+          if (a.rows > 0)
+            hipLaunchKernelGGL((norm_bwd_kernel<T, W, 1024, 4, 1024, FUSED, false>),
+                               dim3(unsigned(std::min(a.rows, kOpsMaxGrid))), dim3(1024), 0, st, a);
+          if (grads)
+            hipLaunchKernelGGL((norm_cols_kernel<T>), dim3(unsigned((a.cols + 2047) / 2048), unsigned(a.parts)), dim3(256),
+                               0, st, a);
+        }
     }
+    if (grads && norm_needs_join(a.rows, a.cols))
+      hipLaunchKernelGGL((norm_grad_kernel<W>), dim3(unsigned((a.cols + kGradCols - 1) / kGradCols), 2),
+                         dim3(kGradCols * kGradSlices), 0, st, a.part, a.parts, a.cols, (W*)a.dgamma, (W*)a.dbeta);
     return hipGetLastError();
   }
 };

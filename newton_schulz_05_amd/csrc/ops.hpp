@@ -46,6 +46,7 @@ struct NormBwdArgs {
   void* dgamma;       // null: not wanted
   void* dbeta;
   float* part;        // [parts][2][cols] partial sums of dgamma and dbeta
+  int parts;
   int64_t rows, ld_dy, ld_x, ld_dh, ld_dx, ld_dres;
   int cols;
   DropArgs drop;

@@ -10,9 +10,15 @@ namespace muon {
 // ---- 8 consecutive elements --------------------------------------------------
 // gfx950 loads and stores 16 bytes at any address in global memory, so rows of
 // odd width or stride take the same 16-byte accesses as aligned ones; only
-// the last elements of a row that do not fill a vector go one by one.
+// the end of a row that does not fill a vector goes in runs of 4, 2 and 1
+// elements (three branches: a ladder of single elements made the compiler
+// keep its masks and spill).
 typedef uint32_t u32x4_u __attribute__((ext_vector_type(4), aligned(2)));
+typedef uint32_t u32x2_u __attribute__((ext_vector_type(2), aligned(2)));
+typedef uint32_t u32_u __attribute__((aligned(2)));
 typedef float f32x4_u __attribute__((ext_vector_type(4), aligned(4)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2_u __attribute__((ext_vector_type(2), aligned(4)));
 
 template <typename T> struct Raw8;
 template <> struct Raw8<uint16_t> { u32x4 w; };
@@ -21,30 +27,36 @@ template <> struct Raw8<float> { f32x4 a, b; };
 // The first n (any n, also <= 0 or > 8) of 8 elements at p; 0 in the others.
 __device__ __forceinline__ Raw8<uint16_t> load8(const uint16_t* p, int n) {
   Raw8<uint16_t> r;
+  r.w = u32x4{0, 0, 0, 0};
   if (n >= 8) {
     r.w = *(const u32x4_u*)p;
-  } else {
-    r.w = u32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) r.w[i >> 1] |= uint32_t(p[i]) << (16 * (i & 1));
+  } else if (n > 0) {
+    u32x2 four{0, 0};
+    uint32_t two = 0, one = 0;
+    if (n & 4) four = *(const u32x2_u*)p;
+    if (n & 2) two = *(const u32_u*)(p + (n & 4));
+    if (n & 1) one = p[n & 6];
+    const uint32_t t0 = (n & 2) ? two : one, t1 = (n & 2) ? one : 0;
+    r.w = (n & 4) ? u32x4{four[0], four[1], t0, t1} : u32x4{t0, t1, 0, 0};
   }
   return r;
 }
 __device__ __forceinline__ Raw8<float> load8(const float* p, int n) {
   Raw8<float> r;
+  r.a = f32x4{0, 0, 0, 0};
+  r.b = f32x4{0, 0, 0, 0};
   if (n >= 8) {
     r.a = *(const f32x4_u*)p;
     r.b = *(const f32x4_u*)(p + 4);
-  } else {
-    r.a = f32x4{0, 0, 0, 0};
-    r.b = f32x4{0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) r.a[i] = p[i];
-#pragma unroll
-    for (int i = 4; i < 7; ++i)
-      if (i < n) r.b[i - 4] = p[i];
+  } else if (n > 0) {
+    f32x2 two{0, 0};
+    float one = 0;
+    if (n & 4) r.a = *(const f32x4_u*)p;
+    if (n & 2) two = *(const f32x2_u*)(p + (n & 4));
+    if (n & 1) one = p[n & 6];
+    const f32x4 t = (n & 2) ? f32x4{two[0], two[1], one, 0} : f32x4{one, 0, 0, 0};
+    if (n & 4) r.b = t;
+    else r.a = t;
   }
   return r;
 }
@@ -84,23 +96,36 @@ __device__ __forceinline__ Raw8<float> pack8(const float (&v)[8], const float*) 
 __device__ __forceinline__ void store8(uint16_t* p, int n, const Raw8<uint16_t>& r) {
   if (n >= 8) {
     *(u32x4_u*)p = r.w;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 7; ++i)
-      if (i < n) p[i] = uint16_t(r.w[i >> 1] >> (16 * (i & 1)));
+  } else if (n > 0) {
+    uint32_t t0 = r.w[0], t1 = r.w[1];
+    if (n & 4) {
+      *(u32x2_u*)p = u32x2{t0, t1};
+      t0 = r.w[2];
+      t1 = r.w[3];
+    }
+    if (n & 2) {
+      *(u32_u*)(p + (n & 4)) = t0;
+      t0 = t1;
+    }
+    if (n & 1) p[n & 6] = uint16_t(t0);
   }
 }
 __device__ __forceinline__ void store8(float* p, int n, const Raw8<float>& r) {
   if (n >= 8) {
     *(f32x4_u*)p = r.a;
     *(f32x4_u*)(p + 4) = r.b;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (i < n) p[i] = r.a[i];
-#pragma unroll
-    for (int i = 4; i < 7; ++i)
-      if (i < n) p[i] = r.b[i - 4];
+  } else if (n > 0) {
+    f32x4 t = r.a;
+    if (n & 4) {
+      *(f32x4_u*)p = t;
+      t = r.b;
+    }
+    float one = t[0];
+    if (n & 2) {
+      *(f32x2_u*)(p + (n & 4)) = f32x2{t[0], t[1]};
+      one = t[2];
+    }
+    if (n & 1) p[n & 6] = one;
   }
 }
 

@@ -50,8 +50,7 @@ muon_status check_op_workspace(const void* workspace, size_t bytes, size_t need,
 
 // Bytes of the backward pass's partial sums (0 when one workgroup does it all).
 inline size_t norm_workspace_bytes(int64_t rows, int64_t cols) {
-  const int64_t parts = norm_bwd_parts(rows, cols);
-  return parts > 1 ? size_t(parts) * 2 * size_t(cols) * 4 : 0;
+  return norm_needs_join(rows, cols) ? size_t(norm_bwd_split(rows, cols).parts) * 2 * size_t(cols) * 4 : 0;
 }
 // Per workgroup: experts floats, experts counts, one count.
 inline size_t route_workspace_bytes(int64_t rows, int64_t experts) {

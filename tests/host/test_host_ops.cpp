@@ -69,10 +69,11 @@ int main() {
   // below a bound that holds for any number of rows
   for (int64_t cols = 1; cols <= kNormMaxCols; cols = cols * 3 / 2 + 1)
     for (int64_t rows : {int64_t(0), int64_t(1), int64_t(511), int64_t(70000), int64_t(1) << 40}) {
-      const int64_t parts = norm_bwd_parts(rows, cols);
-      CHECK(parts >= 1 && parts <= 512);
-      CHECK(norm_workspace_bytes(rows, cols) == (parts > 1 ? size_t(parts * 2 * cols * 4) : 0));
-      CHECK(norm_bwd_threads(cols) % norm_row_threads(cols) == 0);
+      const NormBwdSplit sp = norm_bwd_split(rows, cols);
+      CHECK(sp.parts >= 1 && sp.parts <= kNormMaxParts);
+      CHECK(sp.threads % sp.row_threads == 0 && sp.threads >= 256 && sp.threads <= 1024);
+      CHECK(norm_workspace_bytes(rows, cols) == (norm_needs_join(rows, cols) ? size_t(sp.parts) * 2 * cols * 4 : 0));
+      CHECK(norm_needs_join(rows, cols) || sp.parts == 1);
     }
   for (int64_t e = 1; e <= kRouteMaxExperts; ++e) {
     CHECK(route_workspace_bytes(0, e) == 0);
