@@ -231,11 +231,61 @@ __device__ __forceinline__ void emit_dx(const NormBwdArgs& a, int64_t row, unsig
   store8((T*)a.dx + row * a.ld_dx + col, n, pack8(dv, (const T*)nullptr));
 }
 
-// Workgroups of WG threads take every gridDim.x-th group of WG / NT rows and,
-// with SUMS, keep the sums of their columns' dgamma and dbeta in registers; a
-// workgroup's row groups are joined in LDS in a fixed order, and the
-// workgroups' sums by norm_grad_kernel.  A lone workgroup writes the gradients
-// itself.
+// dgamma and dbeta of 64 columns over all rows, for few rows: 8 threads take the
+// columns' vectors of a row, the others the further rows; a wave's rows are
+// joined across its lanes, the waves in LDS.
+template <typename T, typename W, int WG>
+__device__ __forceinline__ void few_rows_sums(const NormBwdArgs& a, int strip, float (*sums)[2][64]) {
+  const int vec = threadIdx.x & 7, wave = threadIdx.x >> 6;
+  const unsigned col = strip * 64 + vec * 8;
+  const int n = a.cols - int(col);
+  float dg[8], db[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) dg[j] = db[j] = 0.0f;
+  for (int64_t row = threadIdx.x >> 3; row < a.rows; row += WG / 8) {
+    float xv[8], dv[8];
+    unpack8(load8((const T*)a.x + row * a.ld_x + col, n), xv);
+    unpack8(load8((const T*)a.dy + row * a.ld_dy + col, n), dv);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      dg[j] = fmaf(dv[j], (xv[j] - mean) * rstd, dg[j]);
+      db[j] += dv[j];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    dg[j] = across_groups<8>(dg[j]);
+    db[j] = across_groups<8>(db[j]);
+  }
+  if ((threadIdx.x & 63) < 8) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      sums[wave][0][vec * 8 + j] = dg[j];
+      sums[wave][1][vec * 8 + j] = db[j];
+    }
+  }
+  __syncthreads();
+  if (threadIdx.x < 128) {
+    const int part = threadIdx.x >> 6, c = threadIdx.x & 63;
+    float s = sums[0][part][c];
+#pragma unroll
+    for (int w = 1; w < WG / 64; ++w) s += sums[w][part][c];
+    W* out = (W*)(part ? a.dbeta : a.dgamma);
+    if (out && strip * 64 + c < a.cols) Elem<W>::store(out + strip * 64 + c, s);
+  }
+}
+
+// Where the sums over rows of dgamma and dbeta are formed.
+enum NormSums {
+  kSumsHere,   // in registers beside dx, one partial sum a workgroup
+  kSumsApart,  // by another kernel
+  kSumsFew,    // by the launch's last workgroups, a strip of 64 columns each
+};
+
+// Workgroups of WG threads take every gridDim.x-th group of WG / NT rows.  With
+// kSumsHere a workgroup's row groups are joined in LDS in a fixed order, and the
+// workgroups' sums by norm_grad_kernel.
 //
 // Bound by memory: x and dy are read and dx written once.  For many rows one
 // workgroup of 1024 threads on each of 256 units, one 16-byte vector a thread
@@ -244,14 +294,22 @@ __device__ __forceinline__ void emit_dx(const NormBwdArgs& a, int64_t row, unsig
 // the next row's loads in flight (AHEAD) over the reduction; at 16384 x 4096
 // 77.4 against 105.6.  The fused pass has a third stream in flight and gains
 // nothing from AHEAD (125.1 without, 127.6 with); with two vectors (8193 to
-// 16384 columns) AHEAD has no registers left.  Wider rows have none for the
-// sums: see norm_cols_kernel.
-template <typename T, typename W, int NT, int NV, int WG, bool FUSED, bool SUMS>
+// 16384 columns) AHEAD spills (2000 x 9000 bf16: 39.8 without, 44.9 with).
+// Wider rows have no registers for the sums: see norm_cols_kernel.
+template <typename T, typename W, int NT, int NV, int WG, bool FUSED, NormSums WHERE>
 __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
   constexpr int RPB = WG / NT;
-  constexpr bool AHEAD = SUMS && !FUSED && (NV == 1 || (NV == 2 && sizeof(T) == 2));
+  constexpr bool SUMS = WHERE == kSumsHere, AHEAD = SUMS && !FUSED && NV == 1;
   __shared__ float red[2][WG / 64][2];
   __shared__ float sums[SUMS && RPB > 1 ? RPB : 1][SUMS && RPB > 1 ? 8 * NT * NV : 1];
+  if constexpr (WHERE == kSumsFew) {
+    __shared__ float strips[WG / 64][2][64];
+    const int first = int((a.rows + RPB - 1) / RPB);
+    if (int(blockIdx.x) >= first) {
+      few_rows_sums<T, W, WG>(a, int(blockIdx.x) - first, strips);
+      return;
+    }
+  }
   const int t = threadIdx.x % NT, sub = row_group<NT>();
   const int cols = a.cols;
   Raw8<W> gr[NV];
@@ -314,11 +372,9 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
   }
   if constexpr (SUMS) {
     if (!a.dgamma && !a.dbeta) return;
-    const bool alone = gridDim.x == 1;
 #pragma unroll
     for (int part = 0; part < 2; ++part) {
       float(&acc)[NV][8] = part ? db : dg;
-      void* own = part ? a.dbeta : a.dgamma;
       float* to = a.part + (int64_t(blockIdx.x) * 2 + part) * cols;
       if constexpr (RPB > 1) {
         __syncthreads();
@@ -331,15 +387,13 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
           float s = sums[0][c];
 #pragma unroll
           for (int g = 1; g < RPB; ++g) s += sums[g][c];
-          if (!alone) to[c] = s;
-          else if (own) Elem<W>::store((W*)own + c, s);
+          to[c] = s;
         }
       } else {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
           const int c = 8 * (i * NT + t);
-          if (!alone) store8(to + c, cols - c, pack8(acc[i], (const float*)nullptr));
-          else if (own) store8((W*)own + c, cols - c, pack8(acc[i], (const W*)nullptr));
+          store8(to + c, cols - c, pack8(acc[i], (const float*)nullptr));
         }
       }
     }
@@ -415,13 +469,21 @@ template <typename T, typename W, bool FUSED> struct NormLaunch {
                        dim3(WG), 0, st, a);
   }
   template <int NT, int NV, int WG> static void bwd(const NormBwdArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, WG, FUSED, true>), dim3(unsigned(a.parts)), dim3(WG), 0, st, a);
+    hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, WG, FUSED, kSumsHere>), dim3(unsigned(a.parts)), dim3(WG), 0, st,
+                       a);
   }
-  // Few rows: as many workgroups as there are row groups of 256 threads (see
-  // norm_bwd_split).
   template <int NT> static void bwd(const NormBwdArgs& a, int wg, hipStream_t st) {
-    constexpr int FEW = NT < 256 ? 256 : NT;
-    wg == 1024 ? bwd<NT, 1, 1024>(a, st) : bwd<NT, 1, FEW>(a, st);
+    if constexpr (NT <= 128) {
+      if (wg == 256) return bwd<NT, 1, 256>(a, st);
+    }
+    bwd<NT, 1, 1024>(a, st);
+  }
+  template <int NT, int NV> static void bwd_few(const NormBwdArgs& a, hipStream_t st) {
+    constexpr int WG = NT < 256 ? 256 : NT;
+    const int64_t groups = (a.rows + WG / NT - 1) / (WG / NT), strips = (a.dgamma || a.dbeta) ? (a.cols + 63) / 64 : 0;
+    if (groups + strips > 0)
+      hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, WG, FUSED, kSumsFew>), dim3(unsigned(groups + strips)), dim3(WG),
+                         0, st, a);
   }
   static hipError_t fwd(const NormFwdArgs& a, hipStream_t st) {
     if (a.cols <= 128) fwd<16, 1>(a, st);
@@ -437,6 +499,18 @@ template <typename T, typename W, bool FUSED> struct NormLaunch {
   static hipError_t bwd(const NormBwdArgs& a, hipStream_t st) {
     const NormBwdSplit sp = norm_bwd_split(a.rows, a.cols);
     const bool grads = a.dgamma || a.dbeta;
+    if (sp.parts == 0) {
+      switch (sp.row_threads) {
+        case 16: bwd_few<16, 1>(a, st); break;
+        case 64: bwd_few<64, 1>(a, st); break;
+        case 128: bwd_few<128, 1>(a, st); break;
+        case 256: bwd_few<256, 1>(a, st); break;
+        case 512: bwd_few<512, 1>(a, st); break;
+        default:
+          a.cols <= 8192 ? bwd_few<1024, 1>(a, st) : a.cols <= 16384 ? bwd_few<1024, 2>(a, st) : bwd_few<1024, 4>(a, st);
+      }
+      return hipGetLastError();
+    }
     switch (sp.row_threads) {
       case 16: bwd<16>(a, sp.threads, st); break;
       case 64: bwd<64>(a, sp.threads, st); break;
@@ -445,19 +519,18 @@ template <typename T, typename W, bool FUSED> struct NormLaunch {
       case 512: bwd<512>(a, sp.threads, st); break;
       default:
         if (a.cols <= 8192) {
-          bwd<1024, 1, 1024>(a, st);
+          bwd<1024>(a, sp.threads, st);
         } else if (a.cols <= 16384) {
           bwd<1024, 2, 1024>(a, st);
         } else {
-          if (a.rows > 0)
-            hipLaunchKernelGGL((norm_bwd_kernel<T, W, 1024, 4, 1024, FUSED, false>),
-                               dim3(unsigned(std::min(a.rows, kOpsMaxGrid))), dim3(1024), 0, st, a);
+          hipLaunchKernelGGL((norm_bwd_kernel<T, W, 1024, 4, 1024, FUSED, kSumsApart>),
+                             dim3(unsigned(std::min(a.rows, kOpsMaxGrid))), dim3(1024), 0, st, a);
           if (grads)
             hipLaunchKernelGGL((norm_cols_kernel<T>), dim3(unsigned((a.cols + 2047) / 2048), unsigned(a.parts)), dim3(256),
                                0, st, a);
         }
     }
-    if (grads && norm_needs_join(a.rows, a.cols))
+    if (grads)
       hipLaunchKernelGGL((norm_grad_kernel<W>), dim3(unsigned((a.cols + kGradCols - 1) / kGradCols), 2),
                          dim3(kGradCols * kGradSlices), 0, st, a.part, a.parts, a.cols, (W*)a.dgamma, (W*)a.dbeta);
     return hipGetLastError();

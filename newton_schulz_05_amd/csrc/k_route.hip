@@ -18,15 +18,34 @@ namespace {
 
 constexpr int WG = kRouteThreads;
 
-// Order-preserving bits of a float: larger value, larger word; 0 for -inf
-// (an expert that is shut off), which is never chosen.  -0 counts as 0.
+// Order-preserving bits of a float: larger value, larger word; -0 counts as 0.
+// Words up to kNone (-inf, an expert that is shut off, and 0, one that is taken)
+// are never chosen.
+constexpr uint32_t kNone = 0x007fffffu;
 __device__ __forceinline__ uint32_t order_key(float v) {
   const uint32_t u = __float_as_uint(v + 0.0f);
-  return v == -INFINITY ? 0u : u ^ ((u >> 31) ? 0xffffffffu : 0x80000000u);
+  return u ^ (uint32_t(int32_t(u) >> 31) | 0x80000000u);
 }
-__device__ __forceinline__ float key_value(uint32_t k) {
-  return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
-}
+
+// What the choices are made by.  bf16: the 16 bits of the value with the
+// expert's complement below them, so that one maximum finds the largest logit
+// and the lowest expert that has it.  fp32 has no room for the expert: the
+// maximum of the value, then the lowest expert that has it.
+template <typename T> struct Choice;
+template <> struct Choice<uint16_t> {
+  static __device__ __forceinline__ uint32_t key(float v, int expert) {
+    return (order_key(v) & 0xffff0000u) | (0xffffu - uint32_t(expert));
+  }
+  static __device__ __forceinline__ float value(uint32_t k) {
+    return __uint_as_float((k >> 31) ? (k & 0xffff0000u) ^ 0x80000000u : ~(k | 0xffffu));
+  }
+};
+template <> struct Choice<float> {
+  static __device__ __forceinline__ uint32_t key(float v, int) { return order_key(v); }
+  static __device__ __forceinline__ float value(uint32_t k) {
+    return __uint_as_float(k ^ ((k >> 31) ? 0x80000000u : 0xffffffffu));
+  }
+};
 
 template <int N> __device__ __forceinline__ uint32_t lane_max(uint32_t v) {
   return lane_reduce<N>(v, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
@@ -35,7 +54,55 @@ template <int N> __device__ __forceinline__ uint32_t lane_min(uint32_t v) {
   return lane_reduce<N>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
 
-// The PER logits of experts base .. base + PER - 1 (-inf behind the last one).
+// Takes the largest key left among the group's lanes out of `key`; returns it
+// and its expert (a key up to kNone once none is left).
+template <typename T, int LANES, int PER>
+__device__ __forceinline__ uint32_t take_largest(uint32_t (&key)[PER], int base, int& expert) {
+  if constexpr (sizeof(T) == 2) {
+    uint32_t best = key[0];
+#pragma unroll
+    for (int i = 1; i < PER; ++i) best = key[i] > best ? key[i] : best;
+    best = lane_max<LANES>(best);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = key[i] == best ? 0u : key[i];
+    expert = 0xffff - int(best & 0xffffu);
+    return best;
+  } else {
+    uint32_t best = key[0], at = 0;
+#pragma unroll
+    for (int i = 1; i < PER; ++i) {
+      at = key[i] > best ? i : at;
+      best = key[i] > best ? key[i] : best;
+    }
+    const uint32_t m = lane_max<LANES>(best);
+    expert = int(lane_min<LANES>(best == m ? base + at : 0xffffu));
+    const int mine = expert - base;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) key[i] = mine == i ? 0u : key[i];
+    return m;
+  }
+}
+
+// exp(x) for x <= 0 (NaN stays NaN) from the hardware's 2^t: x log2(e) is split
+// into its rounded product t and the rest r, and 2^(t + r) = 2^t (1 + r ln 2),
+// which keeps the relative error at a few 2^-24 however large |x| is.
+__device__ __forceinline__ float exp_neg(float x) {
+  x = x < -150.0f ? -150.0f : x;  // 2^-216: 0 in fp32
+  const float t = x * 1.44269502f;
+  const float r = fmaf(x, 1.92596299e-8f, fmaf(x, 1.44269502f, -t));
+  const float e = __builtin_amdgcn_exp2f(t);
+  return fmaf(e, r * 0.693147181f, e);
+}
+
+// Lane J of every group, in all of the group's lanes.
+template <int LANES, int J> __device__ __forceinline__ uint32_t lane_of_group(uint32_t v) {
+  const uint32_t lo = dpp<0x150 + J>(v);  // lane J of each 16
+  if constexpr (LANES == 16) return lo;
+  const uint32_t hi = dpp<0x150 + 8 + J % 8>(v);
+  return (threadIdx.x & 8) ? hi : lo;
+}
+
+// The n of PER logits at p that exist (-inf in the others).
 template <typename T, int PER>
 __device__ __forceinline__ void load_logits(const T* p, int n, float (&v)[PER]) {
   if constexpr (PER >= 8) {
@@ -44,7 +111,11 @@ __device__ __forceinline__ void load_logits(const T* p, int n, float (&v)[PER]) 
       float w[8];
       unpack8(load8(p + i, n - i), w);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i + j] = i + j < n ? w[j] : -INFINITY;
+      for (int j = 0; j < 8; ++j) v[i + j] = w[j];
+    }
+    if (__ballot(n < PER)) {  // padding tokens, experts that are no multiple of the lanes' share
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = i < n ? v[i] : -INFINITY;
     }
   } else {
 #pragma unroll
@@ -52,16 +123,22 @@ __device__ __forceinline__ void load_logits(const T* p, int n, float (&v)[PER]) 
   }
 }
 
+// A workgroup takes every gridDim.x-th run of WG / LANES tokens; a lane keeps the
+// sums of its experts' probabilities over its tokens, the choices are counted
+// in LDS, and both leave one partial sum a workgroup.
 template <typename T, int LANES, int PER>
 __global__ __launch_bounds__(WG) void route_fwd_kernel(RouteArgs a) {
-  constexpr int TOK = WG / LANES;
+  constexpr int TOK = WG / LANES, WAVES = WG / 64;
   __shared__ int32_t hist[LANES * PER];
-  __shared__ float sums[WG / 64][LANES * PER];
+  __shared__ float sums[WAVES][LANES * PER];
   __shared__ int32_t ntok;
   const int t = threadIdx.x % LANES, sub = threadIdx.x / LANES;
   const int base = t * PER, mine = a.experts - base;
   for (int e = threadIdx.x; e < LANES * PER; e += WG) hist[e] = 0;
-  if (threadIdx.x == 0) ntok = 0;
+  if (threadIdx.x == 0) {
+    ntok = 0;
+    if (blockIdx.x == 0) *a.ticket = 0;
+  }
   __syncthreads();
   float psum[PER];
 #pragma unroll
@@ -75,44 +152,35 @@ __global__ __launch_bounds__(WG) void route_fwd_kernel(RouteArgs a) {
     load_logits<T, PER>((const T*)a.logits + row * a.ld + base, live ? mine : 0, v);
     uint32_t key[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = order_key(v[i]);
-    uint32_t top = 0, won = 0;
-    int idx = -1;
-    for (int j = 0; j < a.k; ++j) {
-      uint32_t best = key[0], at = 0;
-#pragma unroll
-      for (int i = 1; i < PER; ++i) {
-        at = key[i] > best ? i : at;
-        best = key[i] > best ? key[i] : best;
-      }
-      const uint32_t m = lane_max<LANES>(best);
-      if (j == 0) top = m;
-      const uint32_t e = lane_min<LANES>(best == m ? base + at : 0xffffu);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) key[i] = base + i == int(e) ? 0u : key[i];
-      if (t == j) {
-        won = m;
-        idx = m ? int(e) : -1;
-      }
+    for (int i = 0; i < PER; ++i) key[i] = Choice<T>::key(v[i], base + i);
+    int expert;
+    const uint32_t top = take_largest<T, LANES, PER>(key, base, expert);
+    uint32_t won = t == 0 ? top : 0u;
+    int idx = expert;
+    for (int j = 1; j < a.k; ++j) {
+      const uint32_t m = take_largest<T, LANES, PER>(key, base, expert);
+      won = t == j ? m : won;
+      idx = t == j ? expert : idx;
     }
-    const bool some = top != 0;
-    const float mx = some ? key_value(top) : 0.0f;
+    const bool some = top > kNone, chosen = won > kNone;
+    if (!chosen) idx = -1;
+    const float mx = some ? Choice<T>::value(top) : 0.0f;
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      v[i] = expf(v[i] - mx);
+      v[i] = exp_neg(v[i] - mx);
       s += v[i];
     }
     const float total = lane_sum<LANES>(s);
     const float inv = some ? 1.0f / total : 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) psum[i] = fmaf(v[i], inv, psum[i]);
-    float gate = idx >= 0 ? expf(key_value(won) - mx) * inv : 0.0f;
+    float gate = chosen ? exp_neg(Choice<T>::value(won) - mx) * inv : 0.0f;
     if (a.renorm) {
       const float all = lane_sum<LANES>(gate);
       gate = some ? gate / all : 0.0f;
     }
-    if (idx >= 0) atomicAdd(&hist[idx], 1);
+    if (chosen) atomicAdd(&hist[idx], 1);
     n += some && t == 0;
     if (in && t < a.k) {
       a.idx[row * a.k + t] = idx;
@@ -123,89 +191,142 @@ __global__ __launch_bounds__(WG) void route_fwd_kernel(RouteArgs a) {
   // the token groups of a wave, then the waves, in a fixed order
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-#pragma unroll
-    for (int d = LANES; d < 64; d *= 2) psum[i] += __shfl_xor(psum[i], d, 64);
-    if ((threadIdx.x & 63) < LANES) sums[threadIdx.x / 64][base + i] = psum[i];
+    const float s = across_groups<LANES>(psum[i]);
+    if ((threadIdx.x & 63) < LANES) sums[threadIdx.x / 64][base + i] = s;
   }
   __syncthreads();
   for (int e = threadIdx.x; e < a.experts; e += WG) {
-    a.part_p[int64_t(blockIdx.x) * a.experts + e] = (sums[0][e] + sums[1][e]) + (sums[2][e] + sums[3][e]);
+    float s = sums[0][e];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) s += sums[w][e];
+    a.part_p[int64_t(blockIdx.x) * a.experts + e] = s;
     a.part_c[int64_t(blockIdx.x) * a.experts + e] = hist[e];
   }
   if (threadIdx.x == 0) a.part_n[blockIdx.x] = ntok;
 }
 
-// Joins the workgroups' sums (one workgroup; thread (slice, e) takes every
-// S-th partial sum of expert e, the slices are joined in order).
-__global__ __launch_bounds__(1024) void route_join_kernel(RouteArgs a, int width) {
-  __shared__ float sp[1024];
-  __shared__ int32_t sc[1024];
-  __shared__ double term[16];
-  __shared__ int32_t ntok;
-  const int e = threadIdx.x & (width - 1), slice = threadIdx.x / width, slices = 1024 / width;
-  if (threadIdx.x == 0) ntok = 0;
+// Joins the workgroups' sums: 16 experts a workgroup, 64 slices of the at most
+// 512 parts, whose at most 8 loads are in flight at once.  The last workgroup
+// to finish adds the terms of the loss, in the order of the experts whichever
+// it is.
+__global__ __launch_bounds__(1024) void route_join_kernel(RouteArgs a) {
+  constexpr int SLICES = 64, EACH = kRouteMaxParts / SLICES;
+  __shared__ float sp[16][16];
+  __shared__ int32_t sc[16][16], sn[16];
+  __shared__ int32_t last;
+  const int lane = threadIdx.x & 15, slice = threadIdx.x >> 4, wave = threadIdx.x >> 6;
+  const int e = int(blockIdx.x) * 16 + lane;
+  float vp[EACH];
+  int32_t vc[EACH];
+#pragma unroll
+  for (int i = 0; i < EACH; ++i) {
+    const int g = slice + SLICES * i;
+    const bool have = e < a.experts && g < a.parts;
+    vp[i] = have ? a.part_p[int64_t(g) * a.experts + e] : 0.0f;
+    vc[i] = have ? a.part_c[int64_t(g) * a.experts + e] : 0;
+  }
+  int32_t n = int(threadIdx.x) < a.parts ? a.part_n[threadIdx.x] : 0;
+  float p = vp[0];
+  int32_t c = vc[0];
+#pragma unroll
+  for (int i = 1; i < EACH; ++i) {
+    p += vp[i];
+    c += vc[i];
+  }
+  p = across_groups<16>(p);
+  c += __shfl_xor(c, 16, 64);
+  c += __shfl_xor(c, 32, 64);
+  for (int d = 32; d >= 1; d >>= 1) n += __shfl_xor(n, d, 64);
+  if ((threadIdx.x & 63) < 16) {
+    sp[wave][lane] = p;
+    sc[wave][lane] = c;
+  }
+  if ((threadIdx.x & 63) == 0) sn[wave] = n;
   __syncthreads();
-  int n = 0;
-  for (int g = threadIdx.x; g < a.parts; g += 1024) n += a.part_n[g];
-  if (n) atomicAdd(&ntok, n);
-  float p = 0.0f;
-  int32_t c = 0;
-  if (e < a.experts)
-    for (int g = slice; g < a.parts; g += slices) {
-      p += a.part_p[int64_t(g) * a.experts + e];
-      c += a.part_c[int64_t(g) * a.experts + e];
-    }
-  sp[threadIdx.x] = p;
-  sc[threadIdx.x] = c;
-  __syncthreads();
-  const double tokens = ntok > 0 ? double(ntok) : 1.0;
+  if (threadIdx.x >= 64) return;
+  n = sn[0];
+#pragma unroll
+  for (int w = 1; w < 16; ++w) n += sn[w];
+  const double tokens = n > 0 ? double(n) : 1.0;
   double x = 0.0;
-  if (slice == 0 && e < a.experts) {
-    for (int i = 1; i < slices; ++i) {
-      p += sp[i * width + e];
-      c += sc[i * width + e];
+  if (threadIdx.x < 16 && e < a.experts) {
+    p = sp[0][lane];
+    c = sc[0][lane];
+#pragma unroll
+    for (int w = 1; w < 16; ++w) {
+      p += sp[w][lane];
+      c += sc[w][lane];
     }
     a.counts[e] = c;
     if (a.prob_mean) a.prob_mean[e] = float(double(p) / tokens);
     x = double(c) * double(p);
   }
-  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
-  if ((threadIdx.x & 63) == 0) term[threadIdx.x >> 6] = x;
-  __syncthreads();
+  for (int d = 8; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
+  if (gridDim.x > 1) {
+    if (threadIdx.x == 0) {
+      __hip_atomic_store(a.terms + blockIdx.x, x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      last = __hip_atomic_fetch_add(a.ticket, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+    }
+    if (!__shfl(threadIdx.x == 0 ? last : 0, 0, 64)) return;
+    x = threadIdx.x < gridDim.x ? __hip_atomic_load(a.terms + threadIdx.x, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT)
+                                : 0.0;
+    for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
+  }
   if (threadIdx.x == 0) {
-    for (int i = 1; i < 16; ++i) x += term[i];
     a.loss[0] = float(double(a.coef) * a.experts * x / (double(a.k) * tokens * tokens));
-    a.n_tokens[0] = ntok;
+    a.n_tokens[0] = n;
+  }
+}
+
+// dp += the gradient dg of choice J and of the following ones.
+template <int LANES, int PER, int J>
+__device__ __forceinline__ void add_choices(float (&dp)[PER], int idx, float dg, int base, int k) {
+  if (J < k) {
+    const int e = int(lane_of_group<LANES, J>(uint32_t(idx))) - base;
+    const float x = __uint_as_float(lane_of_group<LANES, J>(__float_as_uint(dg)));
+#pragma unroll
+    for (int i = 0; i < PER; ++i) dp[i] += e == i ? x : 0.0f;
+    if constexpr (J + 1 < LANES) add_choices<LANES, PER, J + 1>(dp, idx, dg, base, k);
   }
 }
 
 template <typename T, int LANES, int PER>
-__global__ __launch_bounds__(WG) void route_bwd_kernel(RouteBwdArgs a) {
-  constexpr int TOK = WG / LANES;
+__global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArgs a) {
+  constexpr int TOK = kRouteBwdThreads / LANES;
   const int t = threadIdx.x % LANES, sub = threadIdx.x / LANES;
   const int base = t * PER, mine = a.experts - base;
   // A constant added to every dp of a token changes nothing (sum p = 1), so
-  // the counts enter as E c_e - sum c, formed exactly in integers: near
-  // balance the differences are what matters.
-  int64_t c[PER], all = 0;
+  // the counts enter as E c_e - sum c, exact in fp64: near balance the
+  // differences are what matters.
+  int32_t c[PER], own = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     c[i] = i < mine ? a.counts[base + i] : 0;
-    all += c[i];
+    own += c[i];
   }
-#pragma unroll
-  for (int d = 1; d < LANES; d *= 2) all += __shfl_xor(all, d, 64);
+  const int32_t all = lane_reduce<LANES>(own, [](int32_t x, int32_t y) { return x + y; });
   const int ntok = a.n_tokens[0];
   const double up = ntok > 0 ? double(a.coef) * (a.dloss ? double(a.dloss[0]) : 1.0) / (double(a.k) * ntok * ntok) : 0.0;
   float bal[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) bal[i] = float(up * double(c[i] * a.experts - all));
+  for (int i = 0; i < PER; ++i) bal[i] = float(up * (double(c[i]) * a.experts - double(all)));
   for (int64_t row0 = int64_t(blockIdx.x) * TOK; row0 < a.rows; row0 += int64_t(gridDim.x) * TOK) {
     const int64_t row = row0 + sub;
     const bool in = row < a.rows;
     const bool live = in && (!a.valid || a.valid[row] != 0);
     float v[PER];
     load_logits<T, PER>((const T*)a.logits + row * a.ld + base, live ? mine : 0, v);
+    // lane t holds the token's choice t
+    int idx = -1;
+    float dg = 0.0f;
+    if (live && a.dgates && t < a.k) {
+      idx = a.idx[row * a.k + t];
+      dg = a.dgates[row * a.k + t];
+      if (idx < 0 || idx >= a.experts) {
+        idx = -1;
+        dg = 0.0f;
+      }
+    }
     float mx = v[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) mx = fmaxf(mx, v[i]);
@@ -215,21 +336,13 @@ __global__ __launch_bounds__(WG) void route_bwd_kernel(RouteBwdArgs a) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      v[i] = expf(v[i] - mx);
+      v[i] = exp_neg(v[i] - mx);
       s += v[i];
     }
     const float total = lane_sum<LANES>(s);
     const float inv = some ? 1.0f / total : 0.0f;
-    // lane t holds the token's choice t
-    int idx = -1;
-    float dg = 0.0f;
-    if (live && a.dgates && t < a.k) {
-      idx = a.idx[row * a.k + t];
-      if (idx < 0 || idx >= a.experts) idx = -1;
-      else dg = a.dgates[row * a.k + t];
-    }
     if (a.dgates && a.renorm) {
-      const float q = idx >= 0 ? expf(Elem<T>::load((const T*)a.logits + row * a.ld + idx) - mx) * inv : 0.0f;
+      const float q = idx >= 0 ? exp_neg(Elem<T>::load((const T*)a.logits + row * a.ld + idx) - mx) * inv : 0.0f;
       const float sum = lane_sum<LANES>(q);
       const float share = sum > 0.0f ? q / sum : 0.0f;  // exactly 1 for a lone choice, which has no gradient
       const float mid = lane_sum<LANES>(dg * share);
@@ -238,14 +351,7 @@ __global__ __launch_bounds__(WG) void route_bwd_kernel(RouteBwdArgs a) {
     float dp[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) dp[i] = bal[i];
-    if (a.dgates) {
-      for (int j = 0; j < a.k; ++j) {
-        const int e = __shfl(idx, j, LANES) - base;
-        const float x = __shfl(dg, j, LANES);
-#pragma unroll
-        for (int i = 0; i < PER; ++i) dp[i] += e == i ? x : 0.0f;
-      }
-    }
+    if (a.dgates) add_choices<LANES, PER, 0>(dp, idx, dg, base, a.k);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
@@ -290,25 +396,22 @@ template <typename F> void by_experts(int experts, F f) {
 }  // namespace
 
 hipError_t run_route_fwd(const RouteArgs& a, bool bf16, hipStream_t st) {
-  if (a.parts > 0)
-    by_experts(a.experts, [&](auto lanes, auto per) {
-      constexpr int L = decltype(lanes)::value, P = decltype(per)::value;
-      if (bf16) hipLaunchKernelGGL((route_fwd_kernel<uint16_t, L, P>), dim3(unsigned(a.parts)), dim3(WG), 0, st, a);
-      else hipLaunchKernelGGL((route_fwd_kernel<float, L, P>), dim3(unsigned(a.parts)), dim3(WG), 0, st, a);
-    });
-  int width = 1;
-  while (width < a.experts) width *= 2;
-  hipLaunchKernelGGL(route_join_kernel, dim3(1), dim3(1024), 0, st, a, width);
+  by_experts(a.experts, [&](auto lanes, auto per) {
+    constexpr int L = decltype(lanes)::value, P = decltype(per)::value;
+    if (bf16) hipLaunchKernelGGL((route_fwd_kernel<uint16_t, L, P>), dim3(unsigned(a.parts)), dim3(WG), 0, st, a);
+    else hipLaunchKernelGGL((route_fwd_kernel<float, L, P>), dim3(unsigned(a.parts)), dim3(WG), 0, st, a);
+  });
+  hipLaunchKernelGGL(route_join_kernel, dim3(unsigned((a.experts + 15) / 16)), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 
 hipError_t run_route_bwd(const RouteBwdArgs& a, bool bf16, hipStream_t st) {
   by_experts(a.experts, [&](auto lanes, auto per) {
     constexpr int L = decltype(lanes)::value, P = decltype(per)::value;
-    const int64_t need = (a.rows + WG / L - 1) / (WG / L);
-    const dim3 grid(unsigned(std::min<int64_t>(need, 2048)));
-    if (bf16) hipLaunchKernelGGL((route_bwd_kernel<uint16_t, L, P>), grid, dim3(WG), 0, st, a);
-    else hipLaunchKernelGGL((route_bwd_kernel<float, L, P>), grid, dim3(WG), 0, st, a);
+    const int64_t need = (a.rows + kRouteBwdThreads / L - 1) / (kRouteBwdThreads / L);
+    const dim3 grid(unsigned(std::min<int64_t>(need, 1024)));
+    if (bf16) hipLaunchKernelGGL((route_bwd_kernel<uint16_t, L, P>), grid, dim3(kRouteBwdThreads), 0, st, a);
+    else hipLaunchKernelGGL((route_bwd_kernel<float, L, P>), grid, dim3(kRouteBwdThreads), 0, st, a);
   });
   return hipGetLastError();
 }

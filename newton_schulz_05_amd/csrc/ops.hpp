@@ -77,6 +77,8 @@ struct RouteArgs {
   int32_t* part_c;   // [parts][experts]
   int32_t* part_n;   // [parts]
   int parts;
+  double* terms;     // the loss's, one for each 16 experts
+  uint32_t* ticket;  // workgroups that have added theirs
 };
 
 struct RouteBwdArgs {

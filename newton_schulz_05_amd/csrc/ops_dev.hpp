@@ -158,6 +158,18 @@ template <int N> __device__ __forceinline__ float lane_sum(float v) {
   return lane_reduce<N>(v, [](float a, float b) { return a + b; });
 }
 
+// Sum over the lanes that stand at the same place of their group of
+// LANES.
+template <int LANES> __device__ __forceinline__ float across_groups(float v) {
+  if constexpr (LANES == 8) v += __uint_as_float(dpp<0x128>(__float_as_uint(v)));  // 8 lanes on within 16
+  const uint32_t x = __float_as_uint(v);
+  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const uint32_t y = __float_as_uint(v);
+  const auto b = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
 // ---- dropout's generator -------------------------------------------------------
 // Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
 // easy as 1, 2, 3", 2011): ten rounds of two 32 x 32 -> 64 bit products, keyed

@@ -17,40 +17,41 @@ constexpr int64_t kOpsMaxGrid = 1 << 20;  // workgroups of a launch; a kernel lo
 
 // Split of a norm's backward pass: threads that share a row (one vector of 8
 // elements each up to 8192 columns, then two and, beyond 16384 columns, four),
-// threads of a workgroup, and the number of workgroups, each of which leaves
-// one partial sum of the gradients of gamma and beta.  Many rows: 1024 threads
-// on each of 256 compute units (a fixed number, so that results do not depend
-// on the device's).  Rows that 256 workgroups of 256 threads (or of one row)
-// take at once: such workgroups, for a shorter reduction and join (64 x 1536
-// bf16: 5.3 us against 8.2).  Beyond 16384 columns the sums have a kernel of
-// their own, with up to 64 partial sums of 16 or fewer column strips.
+// threads of a workgroup, and the number of partial sums of the gradients of
+// gamma and beta, which a second launch joins.
+//   up to 256 rows: no partial sums; one launch, whose last workgroups sum 64
+//     columns each over all rows (they read x and dy again, out of the cache:
+//     64 x 1536 bf16 takes one launch instead of two);
+//   many rows: one partial sum a workgroup, 1024 threads on each of 256 compute
+//     units (a fixed number, so that results do not depend on the device's),
+//     or, for narrow rows, 256 threads as long as 256 such workgroups take all
+//     rows at once;
+//   beyond 16384 columns the sums have a kernel of their own, with 64 partial
+//     sums of each strip of 2048 columns.
 struct NormBwdSplit {
   int row_threads, threads, parts;
 };
 constexpr int kNormMaxParts = 256;
+constexpr int64_t kNormFewRows = 256;
 inline NormBwdSplit norm_bwd_split(int64_t rows, int64_t cols) {
   NormBwdSplit s;
   s.row_threads = cols <= 128 ? 16 : cols <= 512 ? 64 : cols <= 1024 ? 128 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
-  const int few = std::max(256, s.row_threads);
-  s.threads = rows <= int64_t(few / s.row_threads) * kNormMaxParts ? few : 1024;
+  s.threads = s.row_threads <= 128 && rows <= int64_t(256 / s.row_threads) * kNormMaxParts ? 256 : 1024;
   const int64_t per = s.threads / s.row_threads, most = cols <= 16384 ? kNormMaxParts : 64;
-  s.parts = int(std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, most)));
+  s.parts = rows <= kNormFewRows ? 0 : int(std::min<int64_t>((rows + per - 1) / per, most));
   return s;
-}
-// Whether the partial sums are joined by a launch of their own (else a lone
-// workgroup writes the gradients itself).
-inline bool norm_needs_join(int64_t rows, int64_t cols) {
-  return cols > 16384 || norm_bwd_split(rows, cols).parts > 1;
 }
 
 // Lanes that share one token of the router: each holds `per` experts.
 constexpr int route_lanes(int64_t experts) { return experts <= 8 ? 8 : 16; }
-constexpr int kRouteThreads = 256;
+constexpr int kRouteThreads = 512, kRouteBwdThreads = 256;
 
-// Workgroups of the router's forward pass (one partial sum each).
+// Workgroups of the router's forward pass (one partial sum each): two for each
+// of 256 compute units, a fixed number like the norm's.
+constexpr int kRouteMaxParts = 512;
 inline int64_t route_parts(int64_t rows, int64_t experts) {
   const int64_t per = kRouteThreads / route_lanes(experts);
-  return std::min<int64_t>((rows + per - 1) / per, 256);
+  return std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, kRouteMaxParts));
 }
 
 }  // namespace muon

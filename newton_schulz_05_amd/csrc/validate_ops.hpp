@@ -48,13 +48,15 @@ muon_status check_dropout(float p, int64_t rows, const uint64_t* offset_dev, std
 
 muon_status check_op_workspace(const void* workspace, size_t bytes, size_t need, std::string* detail);
 
-// Bytes of the backward pass's partial sums (0 when one workgroup does it all).
+// Bytes of the backward pass's partial sums (none for few rows).
 inline size_t norm_workspace_bytes(int64_t rows, int64_t cols) {
-  return norm_needs_join(rows, cols) ? size_t(norm_bwd_split(rows, cols).parts) * 2 * size_t(cols) * 4 : 0;
+  return size_t(norm_bwd_split(rows, cols).parts) * 2 * size_t(cols) * 4;
 }
-// Per workgroup: experts floats, experts counts, one count.
+// The loss's terms (a double for each 16 experts), a counter of 16 bytes, and
+// per workgroup: experts floats, experts counts, one count.
+constexpr int64_t kRouteTerms = kRouteMaxExperts / 16;
 inline size_t route_workspace_bytes(int64_t rows, int64_t experts) {
-  return size_t(route_parts(rows, experts)) * (size_t(experts) * 8 + 4);
+  return size_t(kRouteTerms) * 8 + 16 + size_t(route_parts(rows, experts)) * (size_t(experts) * 8 + 4);
 }
 
 // Sizes of a router call.

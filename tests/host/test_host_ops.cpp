@@ -70,13 +70,13 @@ int main() {
   for (int64_t cols = 1; cols <= kNormMaxCols; cols = cols * 3 / 2 + 1)
     for (int64_t rows : {int64_t(0), int64_t(1), int64_t(511), int64_t(70000), int64_t(1) << 40}) {
       const NormBwdSplit sp = norm_bwd_split(rows, cols);
-      CHECK(sp.parts >= 1 && sp.parts <= kNormMaxParts);
+      CHECK(sp.parts >= 0 && sp.parts <= kNormMaxParts && (sp.parts == 0) == (rows <= kNormFewRows));
       CHECK(sp.threads % sp.row_threads == 0 && sp.threads >= 256 && sp.threads <= 1024);
-      CHECK(norm_workspace_bytes(rows, cols) == (norm_needs_join(rows, cols) ? size_t(sp.parts) * 2 * cols * 4 : 0));
-      CHECK(norm_needs_join(rows, cols) || sp.parts == 1);
+      CHECK(norm_workspace_bytes(rows, cols) == size_t(sp.parts) * 2 * cols * 4);
     }
   for (int64_t e = 1; e <= kRouteMaxExperts; ++e) {
-    CHECK(route_workspace_bytes(0, e) == 0);
+    CHECK(route_workspace_bytes(0, e) == route_workspace_bytes(1, e));
+    CHECK((e + 15) / 16 <= kRouteTerms && route_parts(int64_t(1) << 31, e) <= kRouteMaxParts);
     CHECK(route_parts(1, e) == 1 && route_parts(int64_t(1) << 31, e) >= 1);
   }
   if (g_fail) return 1;

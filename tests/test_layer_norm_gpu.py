@@ -83,7 +83,8 @@ def test_forward_and_backward_match_the_oracle(cols, dt, wdt):
 
 
 @pytest.mark.parametrize("dt,wdt", KINDS[:3])
-@pytest.mark.parametrize("rows,cols", [(5000, 24), (4099, 640), (1031, 1536), (1025, 4096), (530, 8192)])
+@pytest.mark.parametrize("rows,cols", [(5000, 24), (4099, 640), (1031, 1536), (1025, 4096), (530, 8192), (257, 40),
+                                       (300, 400), (700, 1000), (400, 9000), (300, 17001)])
 def test_many_rows(rows, cols, dt, wdt):
     """More rows than workgroups: each keeps several, and the partial sums of
     dgamma and dbeta are joined by the second kernel."""
@@ -288,7 +289,7 @@ def test_fused_forward_is_the_two_calls(cols, dt, wdt):
 
 @pytest.mark.parametrize("dt,wdt", KINDS)
 @pytest.mark.parametrize("rows,cols", [(1, 8), (19, 1), (19, 121), (700, 129), (45, 1543), (600, 4096), (33, 8193),
-                                       (9, 16390), (7, 32768)])
+                                       (9, 16390), (7, 32768), (260, 100), (400, 9000), (300, 17001)])
 @pytest.mark.parametrize("with_dh", [True, False])
 def test_fused_backward(rows, cols, dt, wdt, with_dh):
     h, gamma, _ = _inputs(rows, cols, dt, wdt, 400 + cols)

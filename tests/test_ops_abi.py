@@ -186,7 +186,7 @@ def test_route_refusals():
     assert lib.muon_route_workspace_bytes(100, 8, None) == INVALID
     n = ctypes.c_size_t()
     assert lib.muon_route_workspace_bytes(100, 1025, ctypes.byref(n)) == SHAPE
-    assert lib.muon_route_workspace_bytes(0, 8, ctypes.byref(n)) == 0 and n.value == 0
+    assert lib.muon_route_workspace_bytes(0, 8, ctypes.byref(n)) == 0 and n.value > 0
 
 
 # ---- the binding -------------------------------------------------------------------
