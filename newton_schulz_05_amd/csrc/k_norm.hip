@@ -63,8 +63,8 @@ __device__ __forceinline__ void unpack_param(const Raw8<W>& r, const void* p, fl
 
 // Bound by memory: x is read and y written once (16384 x 4096 bf16: 5 TB/s,
 // the rate of a large copy).  gamma and beta come from the cache, their loads
-// behind those of x; four vectors a thread (above 16384 columns) leave no
-// registers for them during the reductions.
+// behind those of x; with three and more vectors a thread they are read after
+// the reductions, over which they would take registers.
 template <typename T, typename W, int NT, int NV, int WG, bool FUSED>
 __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdArgs a) {
   constexpr int RPB = WG / NT;
@@ -293,15 +293,16 @@ enum NormSums {
 // 159.8 with two workgroups of 512 threads and two vectors, and 163.1 without
 // the next row's loads in flight (AHEAD) over the reduction; at 16384 x 4096
 // 77.4 against 105.6.  The fused pass has a third stream in flight and gains
-// nothing from AHEAD (125.1 without, 127.6 with); with two vectors (8193 to
-// 16384 columns) AHEAD spills (2000 x 9000 bf16: 39.8 without, 44.9 with).
-// Wider rows have no registers for the sums: see norm_cols_kernel.
+// nothing from AHEAD (125.1 without, 127.6 with); with more vectors AHEAD spills
+// or gains nothing (2000 x 9000 bf16, two vectors: 39.8 without, 44.9 with).
+// Rows above 20480 columns have no registers for the sums: see
+// norm_cols_kernel.
 template <typename T, typename W, int NT, int NV, int WG, bool FUSED, NormSums WHERE>
 __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
-  constexpr int RPB = WG / NT;
+  constexpr int RPB = WG / NT, JOIN = NT < 64 ? WG / 64 : RPB;
   constexpr bool SUMS = WHERE == kSumsHere, AHEAD = SUMS && !FUSED && NV == 1;
   __shared__ float red[2][WG / 64][2];
-  __shared__ float sums[SUMS && RPB > 1 ? RPB : 1][SUMS && RPB > 1 ? 8 * NT * NV : 1];
+  __shared__ float sums[SUMS && JOIN > 1 ? JOIN : 1][SUMS && JOIN > 1 ? 8 * NT * NV : 1];
   if constexpr (WHERE == kSumsFew) {
     __shared__ float strips[WG / 64][2][64];
     const int first = int((a.rows + RPB - 1) / RPB);
@@ -376,17 +377,26 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
     for (int part = 0; part < 2; ++part) {
       float(&acc)[NV][8] = part ? db : dg;
       float* to = a.part + (int64_t(blockIdx.x) * 2 + part) * cols;
-      if constexpr (RPB > 1) {
+      if constexpr (JOIN > 1) {
+        // the row groups of a wave across its lanes, then the waves or groups in order
+        if constexpr (NT < 64) {
+#pragma unroll
+          for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][j] = across_groups<NT>(acc[i][j]);
+        }
         __syncthreads();
+        if (NT >= 64 || (threadIdx.x & 63) < NT) {
 #pragma unroll
-        for (int i = 0; i < NV; ++i)
+          for (int i = 0; i < NV; ++i)
 #pragma unroll
-          for (int j = 0; j < 8; ++j) sums[sub][8 * (i * NT + t) + j] = acc[i][j];
+            for (int j = 0; j < 8; ++j) sums[NT < 64 ? threadIdx.x / 64 : sub][8 * (i * NT + t) + j] = acc[i][j];
+        }
         __syncthreads();
         for (int c = threadIdx.x; c < cols; c += WG) {
           float s = sums[0][c];
 #pragma unroll
-          for (int g = 1; g < RPB; ++g) s += sums[g][c];
+          for (int g = 1; g < JOIN; ++g) s += sums[g][c];
           to[c] = s;
         }
       } else {
@@ -400,7 +410,7 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
   }
 }
 
-// The sums of rows wider than 16384 columns, in a pass of its own over x and
+// The sums of rows wider than 20480 columns, in a pass of its own over x and
 // dy: blockIdx.x takes 2048 columns, a vector a thread, and blockIdx.y every
 // gridDim.y-th row.  With the sums in norm_bwd_kernel four vectors a thread
 // spilled (2048 x 32768 bf16: 288 us).
@@ -473,10 +483,14 @@ template <typename T, typename W, bool FUSED> struct NormLaunch {
                        a);
   }
   template <int NT> static void bwd(const NormBwdArgs& a, int wg, hipStream_t st) {
-    if constexpr (NT <= 128) {
-      if (wg == 256) return bwd<NT, 1, 256>(a, st);
-    }
-    bwd<NT, 1, 1024>(a, st);
+    wg == 256 ? bwd<NT, 1, 256>(a, st) : bwd<NT, 1, 1024>(a, st);
+  }
+  template <int NT, int NV> static void bwd_apart(const NormBwdArgs& a, bool grads, hipStream_t st) {
+    hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, NT, FUSED, kSumsApart>),
+                       dim3(unsigned(std::min(a.rows, kOpsMaxGrid))), dim3(NT), 0, st, a);
+    if (grads)
+      hipLaunchKernelGGL((norm_cols_kernel<T>), dim3(unsigned((a.cols + 2047) / 2048), unsigned(a.parts)), dim3(256), 0,
+                         st, a);
   }
   template <int NT, int NV> static void bwd_few(const NormBwdArgs& a, hipStream_t st) {
     constexpr int WG = NT < 256 ? 256 : NT;
@@ -486,13 +500,24 @@ template <typename T, typename W, bool FUSED> struct NormLaunch {
                          0, st, a);
   }
   static hipError_t fwd(const NormFwdArgs& a, hipStream_t st) {
-    if (a.cols <= 128) fwd<16, 1>(a, st);
-    else if (a.cols <= 512) fwd<64, 1>(a, st);
-    else if (a.cols <= 1024) fwd<64, 2>(a, st);
-    else if (a.cols <= 2048) fwd<256, 1>(a, st);
-    else if (a.cols <= 4096) fwd<256, 2>(a, st);
-    else if (a.cols <= 8192) fwd<512, 2>(a, st);
-    else if (a.cols <= 16384) fwd<1024, 2>(a, st);
+    // The narrowest fit that keeps several workgroups on a compute unit: three
+    // to five vectors a thread rather than 512 or 1024 threads a row (8192
+    // columns bf16: 51.6 us with 256 threads, 66.6 with 512; 20000 columns: 61
+    // with 512, 105 with 1024; 200 columns, 65536 rows: 64 threads 29.9 us).
+    const int vecs = (a.cols + 7) / 8;
+    if (vecs <= 8) fwd<8, 1>(a, st);
+    else if (vecs <= 16) fwd<16, 1>(a, st);
+    else if (vecs <= 32) fwd<32, 1>(a, st);
+    else if (vecs <= 64) fwd<64, 1>(a, st);
+    else if (vecs <= 128) fwd<64, 2>(a, st);
+    else if (vecs <= 256) fwd<256, 1>(a, st);
+    else if (vecs <= 512) fwd<256, 2>(a, st);
+    else if (vecs <= 768) fwd<256, 3>(a, st);
+    else if (vecs <= 1024) fwd<256, 4>(a, st);
+    else if (vecs <= 1280) fwd<256, 5>(a, st);
+    else if (vecs <= 1536) fwd<512, 3>(a, st);
+    else if (vecs <= 2048) fwd<512, 4>(a, st);
+    else if (vecs <= 2560) fwd<512, 5>(a, st);
     else fwd<1024, 4>(a, st);
     return hipGetLastError();
   }
@@ -501,7 +526,9 @@ template <typename T, typename W, bool FUSED> struct NormLaunch {
     const bool grads = a.dgamma || a.dbeta;
     if (sp.parts == 0) {
       switch (sp.row_threads) {
+        case 8: bwd_few<8, 1>(a, st); break;
         case 16: bwd_few<16, 1>(a, st); break;
+        case 32: bwd_few<32, 1>(a, st); break;
         case 64: bwd_few<64, 1>(a, st); break;
         case 128: bwd_few<128, 1>(a, st); break;
         case 256: bwd_few<256, 1>(a, st); break;
@@ -511,24 +538,22 @@ template <typename T, typename W, bool FUSED> struct NormLaunch {
       }
       return hipGetLastError();
     }
+    const int vecs = (a.cols + 7) / 8;
     switch (sp.row_threads) {
+      case 8: bwd<8>(a, sp.threads, st); break;
       case 16: bwd<16>(a, sp.threads, st); break;
+      case 32: bwd<32>(a, sp.threads, st); break;
       case 64: bwd<64>(a, sp.threads, st); break;
       case 128: bwd<128>(a, sp.threads, st); break;
-      case 256: bwd<256>(a, sp.threads, st); break;
-      case 512: bwd<512>(a, sp.threads, st); break;
+      case 256: bwd<256, 1, 1024>(a, st); break;
+      case 512: bwd<512, 1, 1024>(a, st); break;
       default:
-        if (a.cols <= 8192) {
-          bwd<1024>(a, sp.threads, st);
-        } else if (a.cols <= 16384) {
-          bwd<1024, 2, 1024>(a, st);
-        } else {
-          hipLaunchKernelGGL((norm_bwd_kernel<T, W, 1024, 4, 1024, FUSED, kSumsApart>),
-                             dim3(unsigned(std::min(a.rows, kOpsMaxGrid))), dim3(1024), 0, st, a);
-          if (grads)
-            hipLaunchKernelGGL((norm_cols_kernel<T>), dim3(unsigned((a.cols + 2047) / 2048), unsigned(a.parts)), dim3(256),
-                               0, st, a);
-        }
+        if (vecs <= 1024) bwd<1024, 1, 1024>(a, st);
+        else if (vecs <= 1536) bwd<512, 3, 512>(a, st);
+        else if (vecs <= 2048) bwd<1024, 2, 1024>(a, st);
+        else if (vecs <= 2560) bwd<512, 5, 512>(a, st);
+        else if (vecs <= 3072) bwd_apart<1024, 3>(a, grads, st);
+        else bwd_apart<1024, 4>(a, grads, st);
     }
     if (grads)
       hipLaunchKernelGGL((norm_grad_kernel<W>), dim3(unsigned((a.cols + kGradCols - 1) / kGradCols), 2),

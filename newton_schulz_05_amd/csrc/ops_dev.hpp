@@ -139,16 +139,18 @@ template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t x) {
 }
 
 template <int N, typename V, typename F> __device__ __forceinline__ V lane_reduce(V v, F f) {
-  static_assert(sizeof(V) == 4 && (N == 8 || N == 16 || N == 64));
+  static_assert(sizeof(V) == 4 && (N == 8 || N == 16 || N == 32 || N == 64));
   auto bits = [](V x) { return __builtin_bit_cast(uint32_t, x); };
   auto val = [](uint32_t x) { return __builtin_bit_cast(V, x); };
   v = f(v, val(dpp<0xB1>(bits(v))));   // quad_perm [1,0,3,2]
   v = f(v, val(dpp<0x4E>(bits(v))));   // quad_perm [2,3,0,1]
   v = f(v, val(dpp<0x141>(bits(v))));  // mirror of 8 lanes
   if constexpr (N >= 16) v = f(v, val(dpp<0x140>(bits(v))));  // mirror of 16 lanes
-  if constexpr (N == 64) {
+  if constexpr (N >= 32) {
     const auto a = __builtin_amdgcn_permlane16_swap(bits(v), bits(v), false, false);
     v = f(val(a[0]), val(a[1]));
+  }
+  if constexpr (N == 64) {
     const auto b = __builtin_amdgcn_permlane32_swap(bits(v), bits(v), false, false);
     v = f(val(b[0]), val(b[1]));
   }
@@ -162,12 +164,17 @@ template <int N> __device__ __forceinline__ float lane_sum(float v) {
 // LANES.
 template <int LANES> __device__ __forceinline__ float across_groups(float v) {
   if constexpr (LANES == 8) v += __uint_as_float(dpp<0x128>(__float_as_uint(v)));  // 8 lanes on within 16
-  const uint32_t x = __float_as_uint(v);
-  const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
-  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-  const uint32_t y = __float_as_uint(v);
-  const auto b = __builtin_amdgcn_permlane32_swap(y, y, false, false);
-  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  if constexpr (LANES <= 16) {
+    const uint32_t x = __float_as_uint(v);
+    const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  }
+  if constexpr (LANES <= 32) {
+    const uint32_t y = __float_as_uint(v);
+    const auto b = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+    v = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+  }
+  return v;
 }
 
 // ---- dropout's generator -------------------------------------------------------

@@ -15,29 +15,35 @@ constexpr int32_t kRouteMaxK = 16;       // a 16-lane group keeps one choice per
 
 constexpr int64_t kOpsMaxGrid = 1 << 20;  // workgroups of a launch; a kernel loops over what is left
 
-// Split of a norm's backward pass: threads that share a row (one vector of 8
-// elements each up to 8192 columns, then two and, beyond 16384 columns, four),
-// threads of a workgroup, and the number of partial sums of the gradients of
-// gamma and beta, which a second launch joins.
+// Split of a norm's backward pass: threads that share a row, threads of a
+// workgroup, and the number of partial sums of the gradients of gamma and beta,
+// which a second launch joins.
 //   up to 256 rows: no partial sums; one launch, whose last workgroups sum 64
 //     columns each over all rows (they read x and dy again, out of the cache:
-//     64 x 1536 bf16 takes one launch instead of two);
+//     64 x 1536 bf16 fused 12.0 us a call against 16.2 with two launches);
 //   many rows: one partial sum a workgroup, 1024 threads on each of 256 compute
 //     units (a fixed number, so that results do not depend on the device's),
 //     or, for narrow rows, 256 threads as long as 256 such workgroups take all
 //     rows at once;
-//   beyond 16384 columns the sums have a kernel of their own, with 64 partial
+//   beyond 20480 columns the sums have a kernel of their own, with 64 partial
 //     sums of each strip of 2048 columns.
+// A thread holds one vector of 8 elements of its row up to 8192 columns; then
+// 512 threads three (up to 12288), 1024 two (16384), 512 five (20480), 1024
+// three or four: what measured best in each range (bf16 9000 columns: 95 us
+// with 512 x 3, 98 with 1024 x 2, and fused 144 and 153; 16384 columns: 85
+// with 1024 x 2, 89 with 512 x 4; 20000 columns: 96 with 512 x 5, 130 with the
+// sums apart).
 struct NormBwdSplit {
   int row_threads, threads, parts;
 };
 constexpr int kNormMaxParts = 256;
-constexpr int64_t kNormFewRows = 256;
+constexpr int64_t kNormFewRows = 256, kNormSumsHereCols = 20480;
 inline NormBwdSplit norm_bwd_split(int64_t rows, int64_t cols) {
   NormBwdSplit s;
-  s.row_threads = cols <= 128 ? 16 : cols <= 512 ? 64 : cols <= 1024 ? 128 : cols <= 2048 ? 256 : cols <= 4096 ? 512 : 1024;
+  s.row_threads = 8;
+  while (s.row_threads < 1024 && s.row_threads * 8 < cols) s.row_threads *= 2;
   s.threads = s.row_threads <= 128 && rows <= int64_t(256 / s.row_threads) * kNormMaxParts ? 256 : 1024;
-  const int64_t per = s.threads / s.row_threads, most = cols <= 16384 ? kNormMaxParts : 64;
+  const int64_t per = s.threads / s.row_threads, most = cols <= kNormSumsHereCols ? kNormMaxParts : 64;
   s.parts = rows <= kNormFewRows ? 0 : int(std::min<int64_t>((rows + per - 1) / per, most));
   return s;
 }

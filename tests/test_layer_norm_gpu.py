@@ -16,8 +16,8 @@ from tests.ops_helpers import DEV, DTYPES, K, U, draw, h64, half_step, norm_boun
 pytestmark = pytest.mark.gpu
 EPS = 1e-5
 # around each change of the number of threads or vectors a row takes
-WIDTHS = [1, 2, 7, 8, 9, 127, 128, 129, 511, 513, 1023, 1024, 1025, 2047, 2049, 4096, 4097, 8191, 8193, 16384, 16385,
-          32761, 32768]
+WIDTHS = [1, 2, 7, 8, 9, 63, 65, 127, 128, 129, 255, 257, 511, 513, 1023, 1024, 1025, 2047, 2049, 4096, 4097, 6145, 8191,
+          8193, 10241, 12289, 16384, 16385, 20481, 32761, 32768]
 KINDS = [("bf16", "bf16"), ("bf16", "f32"), ("f32", "f32"), ("f32", "bf16")]
 
 
@@ -84,7 +84,8 @@ def test_forward_and_backward_match_the_oracle(cols, dt, wdt):
 
 @pytest.mark.parametrize("dt,wdt", KINDS[:3])
 @pytest.mark.parametrize("rows,cols", [(5000, 24), (4099, 640), (1031, 1536), (1025, 4096), (530, 8192), (257, 40),
-                                       (300, 400), (700, 1000), (400, 9000), (300, 17001)])
+                                       (300, 400), (700, 1000), (400, 9000), (300, 12300), (300, 17001), (300, 21000),
+                                       (270, 30000), (9000, 200), (3000, 250)])
 def test_many_rows(rows, cols, dt, wdt):
     """More rows than workgroups: each keeps several, and the partial sums of
     dgamma and dbeta are joined by the second kernel."""
@@ -289,7 +290,8 @@ def test_fused_forward_is_the_two_calls(cols, dt, wdt):
 
 @pytest.mark.parametrize("dt,wdt", KINDS)
 @pytest.mark.parametrize("rows,cols", [(1, 8), (19, 1), (19, 121), (700, 129), (45, 1543), (600, 4096), (33, 8193),
-                                       (9, 16390), (7, 32768), (260, 100), (400, 9000), (300, 17001)])
+                                       (9, 16390), (7, 32768), (260, 100), (400, 9000), (300, 12300),
+                                       (300, 17001), (270, 21000), (270, 30000), (9000, 200)])
 @pytest.mark.parametrize("with_dh", [True, False])
 def test_fused_backward(rows, cols, dt, wdt, with_dh):
     h, gamma, _ = _inputs(rows, cols, dt, wdt, 400 + cols)
