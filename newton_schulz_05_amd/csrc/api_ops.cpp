@@ -249,18 +249,20 @@ muon_status muon_route_fwd(const void* logits, int64_t ld, muon_dtype dt, int64_
                                    vec("n_tokens", n_tokens, 1, 4, true),
                                    vec("prob_mean", prob_mean, experts, 4, true, true),
                                    vec("loss", loss, 1, 4, true),
-                                   vec("workspace", workspace, int64_t(need / 4), 4, true)};
+                                   vec("workspace", need ? workspace : nullptr, int64_t(need / 4), 4, true, true)};
     MUON_TRY(muon::check_operands(ops, d));
     muon::RouteArgs a{};
     a.logits = logits; a.valid = valid; a.rows = tokens; a.ld = ld; a.experts = experts; a.k = k;
     a.renorm = renorm; a.coef = coef; a.idx = indices; a.gates = gates; a.counts = counts; a.n_tokens = n_tokens;
     a.prob_mean = prob_mean; a.loss = loss;
     a.parts = int(muon::route_parts(tokens, experts));
-    a.terms = (double*)workspace;
-    a.ticket = (uint32_t*)(a.terms + muon::kRouteTerms);
-    a.part_p = (float*)(a.ticket + 4);
-    a.part_c = (int32_t*)a.part_p + int64_t(a.parts) * experts;
-    a.part_n = a.part_c + int64_t(a.parts) * experts;
+    if (a.parts > 1) {
+      a.terms = (double*)workspace;
+      a.ticket = (uint32_t*)(a.terms + muon::kRouteTerms);
+      a.part_p = (float*)(a.ticket + 4);
+      a.part_c = (int32_t*)a.part_p + int64_t(a.parts) * experts;
+      a.part_n = a.part_c + int64_t(a.parts) * experts;
+    }
     return launched(muon::run_route_fwd(a, dt == MUON_BF16, (hipStream_t)stream));
   });
 }

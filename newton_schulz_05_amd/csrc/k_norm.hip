@@ -503,14 +503,15 @@ template <typename T, typename W, bool FUSED> struct NormLaunch {
     // The narrowest fit that keeps several workgroups on a compute unit: three
     // to five vectors a thread rather than 512 or 1024 threads a row (8192
     // columns bf16: 51.6 us with 256 threads, 66.6 with 512; 20000 columns: 61
-    // with 512, 105 with 1024; 200 columns, 65536 rows: 64 threads 29.9 us).
+    // with 512, 105 with 1024; 2048 columns: 48.6 with 128, 59.6 with 256; 200
+    // columns, 65536 rows: 17.9 with 32, 29.9 with 64).
     const int vecs = (a.cols + 7) / 8;
     if (vecs <= 8) fwd<8, 1>(a, st);
     else if (vecs <= 16) fwd<16, 1>(a, st);
     else if (vecs <= 32) fwd<32, 1>(a, st);
     else if (vecs <= 64) fwd<64, 1>(a, st);
     else if (vecs <= 128) fwd<64, 2>(a, st);
-    else if (vecs <= 256) fwd<256, 1>(a, st);
+    else if (vecs <= 256) fwd<128, 2>(a, st);
     else if (vecs <= 512) fwd<256, 2>(a, st);
     else if (vecs <= 768) fwd<256, 3>(a, st);
     else if (vecs <= 1024) fwd<256, 4>(a, st);

@@ -123,9 +123,23 @@ __device__ __forceinline__ void load_logits(const T* p, int n, float (&v)[PER]) 
   }
 }
 
+// The loss from x = sum_e c_e (sum_t p_te) over n tokens.
+__device__ __forceinline__ void put_loss(const RouteArgs& a, double x, int32_t n) {
+  const double tokens = n > 0 ? double(n) : 1.0;
+  a.loss[0] = float(double(a.coef) * a.experts * x / (double(a.k) * tokens * tokens));
+  a.n_tokens[0] = n;
+}
+// Counts and mean probability of one expert; returns its c_e (sum_t p_te).
+__device__ __forceinline__ double put_expert(const RouteArgs& a, int e, int32_t c, float p, int32_t n) {
+  a.counts[e] = c;
+  if (a.prob_mean) a.prob_mean[e] = n > 0 ? float(double(p) / n) : 0.0f;
+  return double(c) * double(p);
+}
+
 // A workgroup takes every gridDim.x-th run of WG / LANES tokens; a lane keeps the
 // sums of its experts' probabilities over its tokens, the choices are counted
-// in LDS, and both leave one partial sum a workgroup.
+// in LDS, and both leave one partial sum a workgroup.  A lone workgroup (few
+// tokens, see route_parts) finishes the call itself.
 template <typename T, int LANES, int PER>
 __global__ __launch_bounds__(WG) void route_fwd_kernel(RouteArgs a) {
   constexpr int TOK = WG / LANES, WAVES = WG / 64;
@@ -137,7 +151,7 @@ __global__ __launch_bounds__(WG) void route_fwd_kernel(RouteArgs a) {
   for (int e = threadIdx.x; e < LANES * PER; e += WG) hist[e] = 0;
   if (threadIdx.x == 0) {
     ntok = 0;
-    if (blockIdx.x == 0) *a.ticket = 0;
+    if (blockIdx.x == 0 && gridDim.x > 1) *a.ticket = 0;
   }
   __syncthreads();
   float psum[PER];
@@ -195,14 +209,32 @@ __global__ __launch_bounds__(WG) void route_fwd_kernel(RouteArgs a) {
     if ((threadIdx.x & 63) < LANES) sums[threadIdx.x / 64][base + i] = s;
   }
   __syncthreads();
+  const bool lone = gridDim.x == 1;
+  double x = 0.0;
   for (int e = threadIdx.x; e < a.experts; e += WG) {
     float s = sums[0][e];
 #pragma unroll
     for (int w = 1; w < WAVES; ++w) s += sums[w][e];
-    a.part_p[int64_t(blockIdx.x) * a.experts + e] = s;
-    a.part_c[int64_t(blockIdx.x) * a.experts + e] = hist[e];
+    if (lone) {
+      x += put_expert(a, e, hist[e], s, ntok);
+    } else {
+      a.part_p[int64_t(blockIdx.x) * a.experts + e] = s;
+      a.part_c[int64_t(blockIdx.x) * a.experts + e] = hist[e];
+    }
   }
-  if (threadIdx.x == 0) a.part_n[blockIdx.x] = ntok;
+  if (!lone) {
+    if (threadIdx.x == 0) a.part_n[blockIdx.x] = ntok;
+    return;
+  }
+  __shared__ double terms[WAVES];
+  for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
+  if ((threadIdx.x & 63) == 0) terms[threadIdx.x / 64] = x;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) x += terms[w];
+    put_loss(a, x, ntok);
+  }
 }
 
 // Joins the workgroups' sums: 16 experts a workgroup, 64 slices of the at most
@@ -247,7 +279,6 @@ __global__ __launch_bounds__(1024) void route_join_kernel(RouteArgs a) {
   n = sn[0];
 #pragma unroll
   for (int w = 1; w < 16; ++w) n += sn[w];
-  const double tokens = n > 0 ? double(n) : 1.0;
   double x = 0.0;
   if (threadIdx.x < 16 && e < a.experts) {
     p = sp[0][lane];
@@ -257,9 +288,7 @@ __global__ __launch_bounds__(1024) void route_join_kernel(RouteArgs a) {
       p += sp[w][lane];
       c += sc[w][lane];
     }
-    a.counts[e] = c;
-    if (a.prob_mean) a.prob_mean[e] = float(double(p) / tokens);
-    x = double(c) * double(p);
+    x = put_expert(a, e, c, p, n);
   }
   for (int d = 8; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
   if (gridDim.x > 1) {
@@ -272,10 +301,7 @@ __global__ __launch_bounds__(1024) void route_join_kernel(RouteArgs a) {
                                 : 0.0;
     for (int d = 32; d >= 1; d >>= 1) x += __shfl_xor(x, d, 64);
   }
-  if (threadIdx.x == 0) {
-    a.loss[0] = float(double(a.coef) * a.experts * x / (double(a.k) * tokens * tokens));
-    a.n_tokens[0] = n;
-  }
+  if (threadIdx.x == 0) put_loss(a, x, n);
 }
 
 // dp += the gradient dg of choice J and of the following ones.
@@ -401,7 +427,8 @@ hipError_t run_route_fwd(const RouteArgs& a, bool bf16, hipStream_t st) {
     if (bf16) hipLaunchKernelGGL((route_fwd_kernel<uint16_t, L, P>), dim3(unsigned(a.parts)), dim3(WG), 0, st, a);
     else hipLaunchKernelGGL((route_fwd_kernel<float, L, P>), dim3(unsigned(a.parts)), dim3(WG), 0, st, a);
   });
-  hipLaunchKernelGGL(route_join_kernel, dim3(unsigned((a.experts + 15) / 16)), dim3(1024), 0, st, a);
+  if (a.parts > 1)
+    hipLaunchKernelGGL(route_join_kernel, dim3(unsigned((a.experts + 15) / 16)), dim3(1024), 0, st, a);
   return hipGetLastError();
 }
 

@@ -53,11 +53,12 @@ constexpr int route_lanes(int64_t experts) { return experts <= 8 ? 8 : 16; }
 constexpr int kRouteThreads = 512, kRouteBwdThreads = 256;
 
 // Workgroups of the router's forward pass (one partial sum each): two for each
-// of 256 compute units, a fixed number like the norm's.
+// of 256 compute units, a fixed number like the norm's; one, and no second
+// launch, for tokens that it takes in two rounds.
 constexpr int kRouteMaxParts = 512;
 inline int64_t route_parts(int64_t rows, int64_t experts) {
   const int64_t per = kRouteThreads / route_lanes(experts);
-  return std::max<int64_t>(1, std::min<int64_t>((rows + per - 1) / per, kRouteMaxParts));
+  return rows <= 2 * per ? 1 : std::min<int64_t>((rows + per - 1) / per, kRouteMaxParts);
 }
 
 }  // namespace muon

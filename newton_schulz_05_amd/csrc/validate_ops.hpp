@@ -53,10 +53,12 @@ inline size_t norm_workspace_bytes(int64_t rows, int64_t cols) {
   return size_t(norm_bwd_split(rows, cols).parts) * 2 * size_t(cols) * 4;
 }
 // The loss's terms (a double for each 16 experts), a counter of 16 bytes, and
-// per workgroup: experts floats, experts counts, one count.
+// per workgroup: experts floats, experts counts, one count.  None for a lone
+// workgroup.
 constexpr int64_t kRouteTerms = kRouteMaxExperts / 16;
 inline size_t route_workspace_bytes(int64_t rows, int64_t experts) {
-  return size_t(kRouteTerms) * 8 + 16 + size_t(route_parts(rows, experts)) * (size_t(experts) * 8 + 4);
+  const int64_t parts = route_parts(rows, experts);
+  return parts > 1 ? size_t(kRouteTerms) * 8 + 16 + size_t(parts) * (size_t(experts) * 8 + 4) : 0;
 }
 
 // Sizes of a router call.

@@ -60,14 +60,14 @@ RAT = {n: (i + 1) * STEP for i, n in enumerate(
     ("logits", "valid", "idx", "gates", "counts", "n", "mean", "loss", "ws", "dgates", "dloss", "dlogits"))}
 
 
-def route(ld=8, dt=F32, tokens=100, experts=8, k=2, renorm=1, coef=1.0, ws_bytes=1 << 20, **at):
+def route(ld=8, dt=F32, tokens=1000, experts=8, k=2, renorm=1, coef=1.0, ws_bytes=1 << 20, **at):
     a = {**RAT, **at}
     return B.load_library().muon_route_fwd(a["logits"], ld, dt, tokens, experts, k, a["valid"], renorm, coef,
                                            a["idx"], a["gates"], a["counts"], a["n"], a["mean"], a["loss"], a["ws"],
                                            ws_bytes, None)
 
 
-def route_bwd(ld=8, dt=F32, tokens=100, experts=8, k=2, renorm=1, coef=1.0, ld_d=8, **at):
+def route_bwd(ld=8, dt=F32, tokens=1000, experts=8, k=2, renorm=1, coef=1.0, ld_d=8, **at):
     a = {**RAT, **at}
     return B.load_library().muon_route_bwd(a["logits"], ld, dt, tokens, experts, k, a["valid"], renorm, coef,
                                            a["idx"], a["counts"], a["n"], a["dgates"], a["dloss"], a["dlogits"], ld_d,
@@ -186,7 +186,7 @@ def test_route_refusals():
     assert lib.muon_route_workspace_bytes(100, 8, None) == INVALID
     n = ctypes.c_size_t()
     assert lib.muon_route_workspace_bytes(100, 1025, ctypes.byref(n)) == SHAPE
-    assert lib.muon_route_workspace_bytes(0, 8, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.muon_route_workspace_bytes(0, 8, ctypes.byref(n)) == 0 and n.value == 0
 
 
 # ---- the binding -------------------------------------------------------------------
