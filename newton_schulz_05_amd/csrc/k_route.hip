@@ -304,21 +304,34 @@ __global__ __launch_bounds__(1024) void route_join_kernel(RouteArgs a) {
   if (threadIdx.x == 0) put_loss(a, x, n);
 }
 
-// dp += the gradient dg of choice J and of the following ones.
+// A group's lanes are in one wave, whose LDS accesses take place in order; this
+// keeps the compiler from moving them.
+__device__ __forceinline__ void wave_lds_order() { __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront"); }
+
+// Lane J's choice of every group in turn: dp += its gradient dg at its expert.
+// Up to two experts a lane compare; with more, the gradients go through the
+// group's own run of LDS, one lane of each group at a time, so that an index
+// named more than once is added in the order of the slots (65536 x 128
+// bf16, k = 8: 208 instructions a token group by comparison).
 template <int LANES, int PER, int J>
-__device__ __forceinline__ void add_choices(float (&dp)[PER], int idx, float dg, int base, int k) {
+__device__ __forceinline__ void add_choices(float (&dp)[PER], float* mem, int t, int idx, float dg, int base, int k) {
   if (J < k) {
-    const int e = int(lane_of_group<LANES, J>(uint32_t(idx))) - base;
-    const float x = __uint_as_float(lane_of_group<LANES, J>(__float_as_uint(dg)));
+    if constexpr (PER <= 2) {
+      const int e = int(lane_of_group<LANES, J>(uint32_t(idx))) - base;
+      const float x = __uint_as_float(lane_of_group<LANES, J>(__float_as_uint(dg)));
 #pragma unroll
-    for (int i = 0; i < PER; ++i) dp[i] += e == i ? x : 0.0f;
-    if constexpr (J + 1 < LANES) add_choices<LANES, PER, J + 1>(dp, idx, dg, base, k);
+      for (int i = 0; i < PER; ++i) dp[i] += e == i ? x : 0.0f;
+    } else {
+      if (t == J && idx >= 0) atomicAdd(mem + idx, dg);
+    }
+    if constexpr (J + 1 < LANES) add_choices<LANES, PER, J + 1>(dp, mem, t, idx, dg, base, k);
   }
 }
 
 template <typename T, int LANES, int PER>
 __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArgs a) {
   constexpr int TOK = kRouteBwdThreads / LANES;
+  __shared__ __attribute__((aligned(16))) float slots[TOK][PER > 2 ? LANES * PER : 1];
   const int t = threadIdx.x % LANES, sub = threadIdx.x / LANES;
   const int base = t * PER, mine = a.experts - base;
   // A constant added to every dp of a token changes nothing (sum p = 1), so
@@ -377,7 +390,21 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
     float dp[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) dp[i] = bal[i];
-    if (a.dgates) add_choices<LANES, PER, 0>(dp, idx, dg, base, a.k);
+    if (a.dgates) {
+      float* mem = slots[sub];
+      if constexpr (PER > 2) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i) mem[base + i] = dp[i];
+        wave_lds_order();
+      }
+      add_choices<LANES, PER, 0>(dp, mem, t, idx, dg, base, a.k);
+      if constexpr (PER > 2) {
+        wave_lds_order();
+#pragma unroll
+        for (int i = 0; i < PER; ++i) dp[i] = mem[base + i];
+        wave_lds_order();
+      }
+    }
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
