@@ -148,6 +148,56 @@ def bench_adamw(steps, warmup, elems):
                          "launches_per_step": (len(sizes) + 31) // 32}}
 
 
+def bench_block(steps, warmup):
+    """The training operators beside the step, as one block of the 32-layer
+    transformer set runs them on 16384 tokens: dropout + residual add + layer
+    norm of [16384, 4096] bf16 forward (x, residual, h, y: 8 B per element) and
+    backward (dy, dh, h, dx, dresidual: 10 B), and the router of 8 experts, two
+    a token, forward (logits, choices, gates) and backward (logits, choices,
+    their gradients).  Each is also timed alone."""
+    import torch
+    import newton_schulz_05_amd as muon
+    t, c, e, k = 16384, 4096, 8, 2
+    dev, bf = "cuda", torch.bfloat16
+    mat = [torch.randn(t, c, device=dev).to(bf) for _ in range(4)]  # x, residual, dy, dh
+    h, y, dx, dres = (torch.empty(t, c, dtype=bf, device=dev) for _ in range(4))
+    gamma, beta = torch.ones(c, dtype=bf, device=dev), torch.zeros(c, dtype=bf, device=dev)
+    dgamma, dbeta = torch.empty_like(gamma), torch.empty_like(beta)
+    mean, rstd = torch.empty(t, device=dev), torch.empty(t, device=dev)
+    logits = torch.randn(t, e, device=dev)
+    idx, gates = torch.empty(t, k, dtype=torch.int32, device=dev), torch.empty(t, k, device=dev)
+    counts, n = torch.empty(e, dtype=torch.int32, device=dev), torch.empty(1, dtype=torch.int32, device=dev)
+    loss, dgates, dlogits = torch.empty(1, device=dev), torch.randn(t, k, device=dev), torch.empty_like(logits)
+    st = torch.cuda.current_stream()
+    rng = dict(p=0.1, seed=1, offset=2)
+    parts = {
+        "dropout_add_layer_norm": (8.0 * t * c, lambda: muon.dropout_add_layer_norm(
+            mat[0], mat[1], gamma, beta, h, y, mean=mean, rstd=rstd, stream=st, **rng)),
+        "route": (t * (4.0 * e + 8 * k), lambda: muon.route(logits, idx, gates, counts, n, loss, coef=0.01, stream=st)),
+        "route_backward": (t * (8.0 * e + 8 * k), lambda: muon.route_backward(
+            logits, idx, counts, n, dlogits, dgates=dgates, coef=0.01, stream=st)),
+        "dropout_add_layer_norm_backward": (10.0 * t * c, lambda: muon.dropout_add_layer_norm_backward(
+            mat[2], h, gamma, mean, rstd, dx, dres, dh=mat[3], dgamma=dgamma, dbeta=dbeta, stream=st, **rng)),
+    }
+
+    def fn():
+        for _, f in parts.values():
+            f()
+    ms = _events_time(fn, steps, warmup, st)
+    byt = sum(b for b, _ in parts.values())
+    alone = {name: {"ms": round(m, 5), "gb_s": round(b / (m * 1e-3) / 1e9, 1)}
+             for name, (b, f) in parts.items() for m in [_events_time(f, steps, warmup, st)]}
+    gbs = byt / (ms * 1e-3) / 1e9
+    return {"metric": "training operators of one block (ms, GB/s)", "value": round(gbs, 1), "unit": "GB/s", "n_gpus": 1,
+            "steps": steps, "warmup": warmup, "ms_per_step": round(ms, 5), "higher_is_better": True,
+            "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+            "config": {"workload": "block_operators_16384x4096_8_experts", "tokens": t, "cols": c, "experts": e, "k": k},
+            "alone": alone,
+            "roofline": {"bound": "hbm", "achieved": round(gbs, 1), "peak": HBM_PEAK_GBS, "unit": "GB/s",
+                         "frac": round(gbs / HBM_PEAK_GBS, 4), "traffic": None, "kernel": "norm_bwd_kernel",
+                         "launches_per_step": 6}}
+
+
 def time_groups(wl, steps, warmup, dev):
     """Each shape group of a multi-group workload timed alone (its own plan
     over the parameters of that group), with the fraction of its own bound:
@@ -446,9 +496,10 @@ def main() -> int:
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-extra", action="store_true",
                     help="skip the other workloads' whole-step figures reported beside the headline")
-    ap.add_argument("--op", default="step", choices=["step", "ns", "shard_update", "adamw"],
+    ap.add_argument("--op", default="step", choices=["step", "ns", "shard_update", "adamw", "block"],
                     help="step: the Muon step (default); ns: muon_ns alone on the workload; "
-                         "shard_update / adamw: the companion kernels")
+                         "shard_update / adamw: the companion kernels; "
+                         "block: the training operators beside the step")
     ap.add_argument("--adamw-elems", type=int, default=0,
                     help="adamw: total elements of a 64-tensor stress set instead of the model's gains")
     ap.add_argument("--copy-probe", type=int, default=0, metavar="BYTES",
@@ -473,6 +524,10 @@ def main() -> int:
         return 0
     if args.op == "adamw":
         print(json.dumps(bench_adamw(args.steps or 100, args.warmup or 10, args.adamw_elems)), flush=True)
+        return 0
+
+    if args.op == "block":
+        print(json.dumps(bench_block(args.steps or 100, args.warmup or 10)), flush=True)
         return 0
 
     import torch

@@ -51,7 +51,8 @@
  *   - Pointer arguments named `*_ptrs` are HOST arrays of DEVICE pointers,
  *     one per parameter, in plan order.
  *   - Every tensor is dense row-major [batch, rows, cols], 16-byte aligned,
- *     and no two tensors overlap.
+ *     and no two tensors overlap (the 1-D, shard and training operators
+ *     further down state their own layouts).
  *   - Arguments are validated before anything is enqueued.  A non-OK status
  *     from validation leaves every buffer untouched.  MUON_ERR_HIP means a
  *     launch failed after work may have been enqueued: buffer contents are
@@ -277,9 +278,10 @@ muon_status muon_adamw_step(void* const* params, const void* const* grads, float
  *     are written as 0.
  *   - An output may not overlap another argument, except where said; column
  *     slices of one buffer with the same ld do not overlap.
- *   - Every sum, mean and softmax is formed in fp32 or wider; each output is
- *     rounded once, to nearest even.  Results are the same from run to run
- *     (no order depends on timing) and do not depend on ld or alignment.
+ *   - Every sum, mean and softmax is formed in fp32 or wider (a norm's squares
+ *     overflow beyond about 1e18); each output is rounded once, to nearest
+ *     even.  Results are the same from run to run (no order depends on
+ *     timing) and do not depend on ld or alignment.
  *   - Nothing is kept between calls; every call enqueues kernels only and may
  *     be recorded into a HIP graph.  A workspace needs no clearing and may be
  *     shared by calls that are ordered on one stream. */
@@ -383,7 +385,8 @@ muon_status muon_route_fwd(const void* logits, int64_t ld, muon_dtype dt, int64_
                            size_t workspace_bytes, void* stream);
 
 /* Gradient of the gates and the loss by the logits (counts, choices and n
- * are constants):
+ * are constants; counts and n summed over ranks give the gradient of the
+ * loss over all their tokens):
  *   dp_e = dloss * coef * experts * counts_e / (k n^2) + (chosen: its gate's),
  *   dlogit = p (dp - sum_e p dp), 0 for tokens without a choice.
  *   indices, counts, n_tokens : as the forward pass wrote them (an index

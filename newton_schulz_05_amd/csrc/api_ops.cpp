@@ -4,7 +4,6 @@
 #include <hip/hip_runtime.h>
 
 #include <cmath>
-#include <exception>
 #include <string>
 #include <vector>
 
@@ -51,7 +50,7 @@ template <typename F> muon_status guarded(F f) {
     std::string d;
     const muon_status s = f(&d);
     return s == MUON_OK || d.empty() ? s : muon::api_fail(s, d);
-  } catch (const std::exception&) {
+  } catch (...) {
     return MUON_ERR_INVALID_ARG;
   }
 }

@@ -16,7 +16,17 @@ from typing import Optional, Tuple
 
 import torch
 
-from .binding import MuonError, _check, _dtype_code, load_library
+from .binding import MUON_BF16, MUON_F32, MuonError, _check, load_library
+
+
+_CODES = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
+
+
+def _dtype_code(dt: torch.dtype) -> int:
+    code = _CODES.get(dt)
+    if code is None:
+        raise MuonError(3, f"unsupported dtype {dt}")
+    return code
 
 
 def _matrix(t: torch.Tensor, what: str) -> Tuple[int, int, int]:
@@ -104,7 +114,7 @@ def _call(dev: int, f, *args) -> None:
             _check(f(*args))
 
 
-def _workspace(given: Optional[torch.Tensor], need: int, stream, dev: int):
+def _workspace(given: Optional[torch.Tensor], need: int, stream, dev: int, handle: int):
     """(tensor, pointer, bytes): the caller's workspace, or one from torch's
     allocator that belongs to the call's stream."""
     if given is not None:
@@ -113,7 +123,7 @@ def _workspace(given: Optional[torch.Tensor], need: int, stream, dev: int):
         return given, given.data_ptr(), given.numel() * given.element_size()
     if need == 0:
         return None, None, 0
-    if stream is None:
+    if stream is None or handle == torch._C._cuda_getCurrentRawStream(dev):
         t = torch.empty(need, dtype=torch.uint8, device=dev)
     else:
         with torch.cuda.stream(stream):
@@ -175,7 +185,7 @@ def layer_norm_backward(dy, x, gamma, mean, rstd, dx, *, dgamma=None, dbeta=None
     code, (g, dg, db) = _grad_params(gamma, dgamma, dbeta, x, cols)
     m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
     dev, st = _device(stream, x, dy, dx, gamma, mean, rstd, dgamma, dbeta, workspace)
-    keep, ws, ws_bytes = _workspace(workspace, _norm_workspace(rows, cols) if dg or db else 0, stream, dev)
+    keep, ws, ws_bytes = _workspace(workspace, _norm_workspace(rows, cols) if dg or db else 0, stream, dev, st)
     _call(dev, load_library().muon_layer_norm_bwd, dy.data_ptr(), ld_dy, x.data_ptr(), ld, _dtype_code(x.dtype), g,
           code, m, r, rows, cols, dx.data_ptr(), ld_dx, dg, db, ws, ws_bytes, st)
 
@@ -227,7 +237,7 @@ def dropout_add_layer_norm_backward(dy, h, gamma, mean, rstd, dx, dresidual, *, 
     m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
     od = _flat(offset_dev, 1, _WORD, "offset_dev")
     dev, st = _device(stream, h, dy, dx, dresidual, dh, gamma, mean, rstd, dgamma, dbeta, offset_dev, workspace)
-    keep, ws, ws_bytes = _workspace(workspace, _norm_workspace(rows, cols) if dg or db else 0, stream, dev)
+    keep, ws, ws_bytes = _workspace(workspace, _norm_workspace(rows, cols) if dg or db else 0, stream, dev, st)
     _call(dev, load_library().muon_dropout_add_layer_norm_bwd, dy.data_ptr(), ld_dy,
           None if dh is None else dh.data_ptr(), ld_dh, h.data_ptr(), ld, _dtype_code(h.dtype), g, code, m, r, rows,
           cols, p, _u64(seed, "seed"), _u64(offset, "offset"), od, dx.data_ptr(), ld_dx, dresidual.data_ptr(), ld_dres,
@@ -262,7 +272,7 @@ def route(logits, indices, gates, counts, n_tokens, loss, *, coef: float = 1.0, 
     lo, pm = _flat(loss, 1, _F32, "loss"), _flat(prob_mean, experts, _F32, "prob_mean")
     v = _flat(valid, rows, _MASK, "valid")
     dev, st = _device(stream, logits, indices, gates, counts, n_tokens, loss, valid, prob_mean, workspace)
-    keep, ws, ws_bytes = _workspace(workspace, _route_workspace(rows, experts), stream, dev)
+    keep, ws, ws_bytes = _workspace(workspace, _route_workspace(rows, experts), stream, dev, st)
     _call(dev, load_library().muon_route_fwd, logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, experts, k, v,
           1 if renorm else 0, coef, indices.data_ptr(), gates.data_ptr(), c, n, pm, lo, ws, ws_bytes, st)
 
