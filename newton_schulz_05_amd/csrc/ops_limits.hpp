@@ -52,13 +52,15 @@ inline NormBwdSplit norm_bwd_split(int64_t rows, int64_t cols) {
 constexpr int route_lanes(int64_t experts) { return experts <= 8 ? 8 : 16; }
 constexpr int kRouteThreads = 512, kRouteBwdThreads = 256;
 
-// Workgroups of the router's forward pass (one partial sum each): two for each
-// of 256 compute units, a fixed number like the norm's; one, and no second
-// launch, for tokens that it takes in two rounds.
+// Workgroups of the router's forward pass (one partial sum each), a fixed number
+// like the norm's: two for each of 256 compute units, one beyond 128 experts,
+// where a partial sum costs more than the second workgroup hides (bf16, with
+// 512 and 256: 65536 x 128 22.1 and 23.8 us, 16384 x 256 15.5 and 14.1).  One,
+// and no second launch, for tokens that it takes in two rounds.
 constexpr int kRouteMaxParts = 512;
 inline int64_t route_parts(int64_t rows, int64_t experts) {
-  const int64_t per = kRouteThreads / route_lanes(experts);
-  return rows <= 2 * per ? 1 : std::min<int64_t>((rows + per - 1) / per, kRouteMaxParts);
+  const int64_t per = kRouteThreads / route_lanes(experts), most = experts <= 128 ? kRouteMaxParts : kRouteMaxParts / 2;
+  return rows <= 2 * per ? 1 : std::min<int64_t>((rows + per - 1) / per, most);
 }
 
 }  // namespace muon
