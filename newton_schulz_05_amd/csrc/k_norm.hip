@@ -553,7 +553,7 @@ template <typename T, typename W, bool FUSED> struct NormLaunch {
         else if (vecs <= 1536) bwd<512, 3, 512>(a, st);
         else if (vecs <= 2048) bwd<1024, 2, 1024>(a, st);
         else if (vecs <= 2560) bwd<512, 5, 512>(a, st);
-        else if (vecs <= 3072) bwd_apart<1024, 3>(a, grads, st);
+        else if (a.cols <= 24576) bwd_apart<1024, 3>(a, grads, st);
         else bwd_apart<1024, 4>(a, grads, st);
     }
     if (grads)

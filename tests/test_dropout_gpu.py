@@ -81,6 +81,11 @@ def test_in_place_strides_and_gaps(dt):
     r2 = res.clone()
     dropout(x, r2, p=0.3, seed=4, offset=9, residual=r2)
     assert torch.equal(r2, wres)
+    x2 = x.clone()   # all three the same tensor
+    dropout(x2, x2, p=0.3, seed=4, offset=9, residual=x2)
+    self_res = torch.empty_like(x)
+    dropout(x, self_res, p=0.3, seed=4, offset=9, residual=x)
+    assert torch.equal(x2, self_res)
     x3 = x.view(61, 7, 29)   # rows are what precedes the last dimension
     o3 = torch.empty_like(x3)
     dropout(x3, o3, p=0.3, seed=4, offset=9)

@@ -199,6 +199,41 @@ def test_offsets_past_32_bits():
     assert torch.equal(dx, want)
 
 
+@pytest.mark.parametrize("rows,cols", [((1 << 25) + 77, 5), ((1 << 21) + 3, 1030)])
+def test_more_rows_than_a_launch_has_workgroups(rows, cols):
+    """The forward launch is capped and loops: the last rows come out as they
+    do alone."""
+    x = torch.empty(rows, cols, dtype=torch.bfloat16, device=DEV).fill_(1.0)
+    tail = 700
+    x[-tail:] = draw((tail, cols), 63, 1.0, 0.2, torch.bfloat16).to(DEV)
+    gamma = draw((cols,), 64, 0.2, 1.0).to(DEV)
+    y, mean, rstd = _forward(x, gamma, None)
+    want = _forward(x[-tail:].clone(), gamma, None)
+    for a, b in zip((y, mean, rstd), want):
+        assert torch.equal(a[-tail:], b)
+    assert not y[:-tail].any() and (mean[:-tail] == 1.0).all()
+
+
+def test_parameters_at_odd_addresses():
+    """gamma, beta and their gradients as slices of a flat parameter buffer."""
+    for rows in (9, 400):
+        x, gamma, beta = _inputs(rows, 77, "bf16", "bf16", 65)
+        dy = draw((rows, 77), 66, 0.1, 0.0, torch.bfloat16).to(DEV)
+        flat = torch.zeros(2 * 77 + 3, dtype=torch.bfloat16, device=DEV)
+        gv, bv = flat[1:78], flat[79:156]
+        gv.copy_(gamma)
+        bv.copy_(beta)
+        y, mean, rstd = _forward(x, gamma, beta)
+        y2, _, _ = _forward(x, gv, bv)
+        assert torch.equal(y, y2)
+        grads = torch.full_like(flat, 3.0)
+        dx, dg, db = torch.empty_like(x), torch.empty_like(gamma), torch.empty_like(gamma)
+        layer_norm_backward(dy, x, gamma, mean, rstd, dx, dgamma=dg, dbeta=db)
+        layer_norm_backward(dy, x, gv, mean, rstd, dx, dgamma=grads[1:78], dbeta=grads[79:156])
+        assert torch.equal(grads[1:78], dg) and torch.equal(grads[79:156], db)
+        assert (grads[[0, 78, 156]] == 3.0).all()
+
+
 def test_leading_dimensions():
     x, gamma, beta = _inputs(24, 96, "bf16", "bf16", 71)
     y, mean, rstd = _forward(x, gamma, beta)
