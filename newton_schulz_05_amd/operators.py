@@ -59,10 +59,14 @@ def _matrix(t: torch.Tensor, what: str) -> Tuple[int, int, int]:
 
 def _same(t: torch.Tensor, like: torch.Tensor, what: str) -> int:
     """Row stride of a matrix that has to match `like`."""
+    shape = t.shape
+    if shape != like.shape:
+        raise MuonError(2, f"{what} has shape {tuple(shape)}, expected {tuple(like.shape)}")
     if t.dtype is not like.dtype:
         raise MuonError(3, f"{what} has dtype {t.dtype}, expected {like.dtype}")
-    if t.shape != like.shape:
-        raise MuonError(2, f"{what} has shape {tuple(t.shape)}, expected {tuple(like.shape)}")
+    stride = t.stride()
+    if len(shape) == 2 and stride[1] == 1:
+        return stride[0] if shape[0] > 1 else shape[1]
     return _matrix(t, what)[2]
 
 
@@ -131,19 +135,30 @@ def _workspace(given: Optional[torch.Tensor], need: int, stream, dev: int, handl
     return t, t.data_ptr(), need
 
 
-def _param_code(gamma, beta, x) -> int:
-    p = gamma if gamma is not None else beta
-    return _dtype_code(x.dtype if p is None else p.dtype)
-
-
-def _param(t: Optional[torch.Tensor], first: Optional[torch.Tensor], cols: int, what: str) -> Optional[int]:
+def _param(t: Optional[torch.Tensor], dt: torch.dtype, cols: int, what: str) -> Optional[int]:
+    """Pointer of a 1-D parameter or its gradient, or None."""
     if t is None:
         return None
-    return _flat(t, cols, (t.dtype,) if first is None else (first.dtype,), what)
+    if t.dtype is not dt:
+        raise MuonError(3, f"{what} has dtype {t.dtype}, expected {dt}")
+    if t.numel() != cols:
+        raise MuonError(2, f"{what} has {t.numel()} elements, expected {cols}")
+    if not t.is_contiguous():
+        raise MuonError(1, f"{what} is not contiguous")
+    return t.data_ptr()
+
+
+def _param_dtype(x: torch.Tensor, *params) -> torch.dtype:
+    """The parameters' common dtype: that of the first one given."""
+    for t in params:
+        if t is not None:
+            return t.dtype
+    return x.dtype
 
 
 def _u64(v: int, what: str) -> int:
-    v = int(v)
+    if type(v) is not int:
+        v = int(v)
     if not 0 <= v < 1 << 64:
         raise MuonError(1, f"{what} must be an unsigned 64-bit integer")
     return v
@@ -155,12 +170,12 @@ def layer_norm(x, gamma, beta, y, *, mean=None, rstd=None, eps: float = 1e-5, st
     what layer_norm_backward needs."""
     rows, cols, ld = _matrix(x, "x")
     ld_y = _same(y, x, "y")
-    g = _param(gamma, None, cols, "gamma")
-    b = _param(beta, gamma, cols, "beta")
+    wdt = _param_dtype(x, gamma, beta)
+    g, b = _param(gamma, wdt, cols, "gamma"), _param(beta, wdt, cols, "beta")
     m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
     dev, st = _device(stream, x, y, gamma, beta, mean, rstd)
     _call(dev, load_library().muon_layer_norm_fwd, x.data_ptr(), ld, _dtype_code(x.dtype), g, b,
-          _param_code(gamma, beta, x), rows, cols, eps, y.data_ptr(), ld_y, m, r, st)
+          _dtype_code(wdt), rows, cols, eps, y.data_ptr(), ld_y, m, r, st)
 
 
 @functools.lru_cache(maxsize=256)
@@ -170,24 +185,20 @@ def _norm_workspace(rows: int, cols: int) -> int:
     return n.value
 
 
-def _grad_params(gamma, dgamma, dbeta, x, cols: int):
-    first = next((t for t in (gamma, dgamma, dbeta) if t is not None), None)
-    ptrs = [_param(t, first, cols, w) for t, w in ((gamma, "gamma"), (dgamma, "dgamma"), (dbeta, "dbeta"))]
-    return _dtype_code(x.dtype if first is None else first.dtype), ptrs
-
-
 def layer_norm_backward(dy, x, gamma, mean, rstd, dx, *, dgamma=None, dbeta=None,
                         workspace: Optional[torch.Tensor] = None, stream=None) -> None:
     """Gradients of layer_norm (muon_layer_norm_bwd): dx, and dgamma and dbeta
     where given, in gamma's dtype (the `grads` of adamw_step)."""
     rows, cols, ld = _matrix(x, "x")
     ld_dy, ld_dx = _same(dy, x, "dy"), _same(dx, x, "dx")
-    code, (g, dg, db) = _grad_params(gamma, dgamma, dbeta, x, cols)
+    wdt = _param_dtype(x, gamma, dgamma, dbeta)
+    g = _param(gamma, wdt, cols, "gamma")
+    dg, db = _param(dgamma, wdt, cols, "dgamma"), _param(dbeta, wdt, cols, "dbeta")
     m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
     dev, st = _device(stream, x, dy, dx, gamma, mean, rstd, dgamma, dbeta, workspace)
     keep, ws, ws_bytes = _workspace(workspace, _norm_workspace(rows, cols) if dg or db else 0, stream, dev, st)
     _call(dev, load_library().muon_layer_norm_bwd, dy.data_ptr(), ld_dy, x.data_ptr(), ld, _dtype_code(x.dtype), g,
-          code, m, r, rows, cols, dx.data_ptr(), ld_dx, dg, db, ws, ws_bytes, st)
+          _dtype_code(wdt), m, r, rows, cols, dx.data_ptr(), ld_dx, dg, db, ws, ws_bytes, st)
 
 
 def dropout(x, out, *, p: float, seed: int, offset: int = 0, offset_dev: Optional[torch.Tensor] = None,
@@ -214,13 +225,13 @@ def dropout_add_layer_norm(x, residual, gamma, beta, h, y, *, p: float, seed: in
     by layer_norm.  h may be the residual itself."""
     rows, cols, ld = _matrix(x, "x")
     ld_res, ld_h, ld_y = _same(residual, x, "residual"), _same(h, x, "h"), _same(y, x, "y")
-    g = _param(gamma, None, cols, "gamma")
-    b = _param(beta, gamma, cols, "beta")
+    wdt = _param_dtype(x, gamma, beta)
+    g, b = _param(gamma, wdt, cols, "gamma"), _param(beta, wdt, cols, "beta")
     m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
     od = _flat(offset_dev, 1, _WORD, "offset_dev")
     dev, st = _device(stream, x, residual, gamma, beta, h, y, mean, rstd, offset_dev)
     _call(dev, load_library().muon_dropout_add_layer_norm_fwd, x.data_ptr(), ld, residual.data_ptr(), ld_res,
-          _dtype_code(x.dtype), g, b, _param_code(gamma, beta, x), rows, cols, eps, p, _u64(seed, "seed"),
+          _dtype_code(x.dtype), g, b, _dtype_code(wdt), rows, cols, eps, p, _u64(seed, "seed"),
           _u64(offset, "offset"), od, h.data_ptr(), ld_h, y.data_ptr(), ld_y, m, r, st)
 
 
@@ -233,14 +244,16 @@ def dropout_add_layer_norm_backward(dy, h, gamma, mean, rstd, dx, dresidual, *, 
     rows, cols, ld = _matrix(h, "h")
     ld_dy, ld_dx, ld_dres = _same(dy, h, "dy"), _same(dx, h, "dx"), _same(dresidual, h, "dresidual")
     ld_dh = 0 if dh is None else _same(dh, h, "dh")
-    code, (g, dg, db) = _grad_params(gamma, dgamma, dbeta, h, cols)
+    wdt = _param_dtype(h, gamma, dgamma, dbeta)
+    g = _param(gamma, wdt, cols, "gamma")
+    dg, db = _param(dgamma, wdt, cols, "dgamma"), _param(dbeta, wdt, cols, "dbeta")
     m, r = _flat(mean, rows, _F32, "mean"), _flat(rstd, rows, _F32, "rstd")
     od = _flat(offset_dev, 1, _WORD, "offset_dev")
     dev, st = _device(stream, h, dy, dx, dresidual, dh, gamma, mean, rstd, dgamma, dbeta, offset_dev, workspace)
     keep, ws, ws_bytes = _workspace(workspace, _norm_workspace(rows, cols) if dg or db else 0, stream, dev, st)
     _call(dev, load_library().muon_dropout_add_layer_norm_bwd, dy.data_ptr(), ld_dy,
-          None if dh is None else dh.data_ptr(), ld_dh, h.data_ptr(), ld, _dtype_code(h.dtype), g, code, m, r, rows,
-          cols, p, _u64(seed, "seed"), _u64(offset, "offset"), od, dx.data_ptr(), ld_dx, dresidual.data_ptr(), ld_dres,
+          None if dh is None else dh.data_ptr(), ld_dh, h.data_ptr(), ld, _dtype_code(h.dtype), g, _dtype_code(wdt), m, r,
+          rows, cols, p, _u64(seed, "seed"), _u64(offset, "offset"), od, dx.data_ptr(), ld_dx, dresidual.data_ptr(), ld_dres,
           dg, db, ws, ws_bytes, st)
 
 
