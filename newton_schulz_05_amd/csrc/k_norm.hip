@@ -10,7 +10,7 @@
 //             dh = norm backward + the gradient that reaches h directly,
 //             dresidual = dh, dx = dropout of dh with the same mask
 //
-// A row is read once and held in registers by 16 to 1024 threads, so the mean
+// A row is read once and held in registers by 8 to 1024 threads, so the mean
 // comes before the squared deviations are formed (no cancellation) without a
 // second pass over memory.  All sums are fp32; each output is rounded once.
 #include "ops_dev.hpp"
@@ -204,7 +204,7 @@ __device__ __forceinline__ void fetch_row(const NormBwdArgs& a, int64_t row, int
 __device__ __forceinline__ void hide(Raw8<uint16_t>& v) { asm volatile("" : "+v"(v.w)); }
 __device__ __forceinline__ void hide(Raw8<float>& v) { asm volatile("" : "+v"(v.a), "+v"(v.b)); }
 
-// dx of one vector, and with FUSED dres; returns nothing else.
+// Stores dx of one vector, and with FUSED dres.
 template <typename T, typename W, bool FUSED>
 __device__ __forceinline__ void emit_dx(const NormBwdArgs& a, int64_t row, unsigned col, int n, const Raw8<T>& xr,
                                         const Raw8<T>& dr, const Raw8<T>& hr, const float (&gv)[8], float mean,

@@ -123,7 +123,7 @@ def route_backward(x, idx, counts, n, k, coef, renorm, dgates, dloss, valid=None
     dg = np.where(good, dgates, 0.0)
     if renorm:
         q = np.where(good, np.take_along_axis(p, at, 1), 0.0)
-        s = np.where(live, q.sum(1), 1.0)[:, None]
+        s = np.where(q.sum(1) > 0, q.sum(1), 1.0)[:, None]  # without a choice there is no gradient
         dg = np.where(good, (dg - (dg * q).sum(1, keepdims=True) / s) / s, 0.0)
     for j in range(idx.shape[1]):
         np.add.at(dp, (np.arange(rows), at[:, j]), dg[:, j])

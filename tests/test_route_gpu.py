@@ -179,21 +179,67 @@ def test_bad_values_stay_in_bounds():
     assert torch.isnan(o["loss"]).all()
 
 
-def test_foreign_indices_are_no_choice():
-    """Indices outside the experts count as none, an index named twice twice."""
-    x = _logits(4, 10, "f32", 51)
-    o = _run(x, 3, 0.0, False, None)
+@pytest.mark.parametrize("experts", [10, 100, 700])
+def test_foreign_indices_are_no_choice(experts):
+    """Indices outside the experts count as none, an index named several times
+    counts each time, in the order of the slots."""
+    k = 5
+    x = _logits(6, experts, "f32", 51)
+    o = _run(x, k, 0.0, False, None)
     idx = o["idx"].clone()
-    idx[0] = torch.tensor([2, 2, 5], dtype=torch.int32)
-    idx[1] = torch.tensor([-7, 10, 1 << 30], dtype=torch.int32)
-    dg = draw((4, 3), 52).to(DEV)
-    dx = torch.empty_like(x)
-    route_backward(x, idx, o["counts"], o["n"], dx, dgates=dg, coef=0.0, renorm=False)
+    idx[0] = torch.tensor([2, 2, 5, 2, 2], dtype=torch.int32)
+    idx[1] = torch.tensor([-7, experts, 1 << 30, -(1 << 31), -1], dtype=torch.int32)
+    idx[2] = torch.tensor([experts - 1, -1, 3, experts - 1, 0], dtype=torch.int32)
+    dg = draw((6, k), 52).to(DEV)
     seen = idx.cpu().numpy().copy()
-    seen[1] = -1
-    want = R.route_backward(h64(x), seen, o["counts"].cpu().numpy(), 4, 3, 0.0, False, h64(dg), 1.0)
-    within(dx, want, 4 * K * U * np.abs(h64(dg)).sum(1, keepdims=True) * np.ones_like(want), "dlogits")
-    assert not dx[1].any()
+    seen[(seen < 0) | (seen >= experts)] = -1
+    for renorm in (False, True):
+        dx, again = torch.empty_like(x), torch.empty_like(x)
+        for out in (dx, again):
+            route_backward(x, idx, o["counts"], o["n"], out, dgates=dg, coef=0.0, renorm=renorm)
+        want = R.route_backward(h64(x), seen, o["counts"].cpu().numpy(), 6, k, 0.0, renorm, h64(dg), 1.0)
+        p, _ = R.softmax_rows(h64(x))
+        q = np.where(seen >= 0, np.take_along_axis(p, np.maximum(seen, 0), 1), 0.0)
+        scale = np.abs(h64(dg)).sum(1, keepdims=True) / np.where(renorm & (q.sum(1) > 0), q.sum(1), 1.0)[:, None]
+        within(dx, want, 8 * (K + 20) * U * scale * p, "dlogits")
+        assert not dx[1].any() and torch.equal(dx, again)
+
+
+def test_two_host_threads():
+    """Two host threads on streams of their own, many calls each: no state is
+    shared between calls."""
+    import threading
+    sets = []
+    for i in range(2):
+        x = _logits(3000 + 500 * i, 60, "bf16", 55 + i)
+        sets.append((x, _run(x, 4, 0.1, True, None), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(x, want, stream):
+        try:
+            outs = [_outputs(x.shape[0], 60, 4) for _ in range(20)]
+            torch.cuda.synchronize()
+            for o in outs:
+                route(x, o["idx"], o["gates"], o["counts"], o["n"], o["loss"], coef=0.1, prob_mean=o["mean"],
+                      stream=stream)
+            stream.synchronize()
+            if not all(torch.equal(o[n], want[n]) for o in outs for n in want):
+                bad.append("outputs differ")
+            try:
+                route(x, o["idx"], o["gates"], o["counts"], o["n"], o["loss"], coef=float("inf"), stream=stream)
+            except MuonError as e:
+                if "coef" not in str(e):
+                    bad.append(str(e))
+        except Exception as e:  # noqa: BLE001 - reported by the test
+            bad.append(repr(e))
+
+    ts = [threading.Thread(target=work, args=s) for s in sets]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad, bad
 
 
 def test_gradient_against_differences():
