@@ -102,26 +102,49 @@ template <int LANES, int J> __device__ __forceinline__ uint32_t lane_of_group(ui
   return (threadIdx.x & 8) ? hi : lo;
 }
 
-// The n of PER logits at p that exist (-inf in the others).
-template <typename T, int PER>
-__device__ __forceinline__ void load_logits(const T* p, int n, float (&v)[PER]) {
-  if constexpr (PER >= 8) {
+__device__ __forceinline__ float widen(uint16_t x) { return bf2f(x); }
+__device__ __forceinline__ float widen(float x) { return x; }
+template <typename T> __device__ __forceinline__ T narrow(float x);
+template <> __device__ __forceinline__ uint16_t narrow<uint16_t>(float x) { return f2bf(x); }
+template <> __device__ __forceinline__ float narrow<float>(float x) { return x; }
+
+// A lane's PER logits as stored, by one access where all PER exist (at any
+// alignment of an element, like load8); floats(): -inf where there is none.
+template <typename T, int PER> struct Logits {
+  typedef T V __attribute__((ext_vector_type(PER < 8 ? PER : 1)));
+  typedef T VU __attribute__((ext_vector_type(PER < 8 ? PER : 1), aligned(sizeof(T))));
+  Raw8<T> many[PER < 8 ? 1 : PER / 8];
+  V few;
+  __device__ __forceinline__ void load(const T* p, int n) {
+    if constexpr (PER >= 8) {
 #pragma unroll
-    for (int i = 0; i < PER; i += 8) {
-      float w[8];
-      unpack8(load8(p + i, n - i), w);
+      for (int i = 0; i < PER; i += 8) many[i / 8] = load8(p + i, n - i);
+    } else if (n >= PER) {
+      few = *(const VU*)p;
+    } else {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[i + j] = w[j];
+      for (int i = 0; i < PER; ++i) few[i] = i < n ? p[i] : T(0);
+    }
+  }
+  __device__ __forceinline__ void floats(int n, float (&v)[PER]) const {
+    if constexpr (PER >= 8) {
+#pragma unroll
+      for (int i = 0; i < PER; i += 8) {
+        float w[8];
+        unpack8(many[i / 8], w);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[i + j] = w[j];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = widen(few[i]);
     }
     if (__ballot(n < PER)) {  // padding tokens, experts that are no multiple of the lanes' share
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[i] = i < n ? v[i] : -INFINITY;
     }
-  } else {
-#pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] = i < n ? Elem<T>::load(p + i) : -INFINITY;
   }
-}
+};
 
 // The loss from x = sum_e c_e (sum_t p_te) over n tokens.
 __device__ __forceinline__ void put_loss(const RouteArgs& a, double x, int32_t n) {
@@ -161,9 +184,11 @@ __global__ __launch_bounds__(WG) void route_fwd_kernel(RouteArgs a) {
   for (int64_t row0 = int64_t(blockIdx.x) * TOK; row0 < a.rows; row0 += int64_t(gridDim.x) * TOK) {
     const int64_t row = row0 + sub;
     const bool in = row < a.rows;
-    const bool live = in && (!a.valid || a.valid[row] != 0);
+    const int have = in && (!a.valid || a.valid[row] != 0) ? mine : 0;  // of the lane's logits
+    Logits<T, PER> raw;
+    raw.load((const T*)a.logits + row * a.ld + base, have);
     float v[PER];
-    load_logits<T, PER>((const T*)a.logits + row * a.ld + base, live ? mine : 0, v);
+    raw.floats(have, v);
     uint32_t key[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) key[i] = Choice<T>::key(v[i], base + i);
@@ -353,8 +378,8 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
     const int64_t row = row0 + sub;
     const bool in = row < a.rows;
     const bool live = in && (!a.valid || a.valid[row] != 0);
-    float v[PER];
-    load_logits<T, PER>((const T*)a.logits + row * a.ld + base, live ? mine : 0, v);
+    Logits<T, PER> raw;
+    raw.load((const T*)a.logits + row * a.ld + base, live ? mine : 0);
     // lane t holds the token's choice t
     int idx = -1;
     float dg = 0.0f;
@@ -366,6 +391,8 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
         dg = 0.0f;
       }
     }
+    float v[PER];
+    raw.floats(live ? mine : 0, v);
     float mx = v[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) mx = fmaxf(mx, v[i]);
@@ -424,6 +451,11 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
           for (int j = 0; j < 8; ++j) w[j] = v[i + j];
           store8(out + i, mine - i, pack8(w, (const T*)nullptr));
         }
+      } else if (mine >= PER) {
+        typename Logits<T, PER>::V w;
+#pragma unroll
+        for (int i = 0; i < PER; ++i) w[i] = narrow<T>(v[i]);
+        *(typename Logits<T, PER>::VU*)out = w;
       } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
