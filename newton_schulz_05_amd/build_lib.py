@@ -24,7 +24,7 @@ COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
           "-Wno-unused-function", "-Wno-unused-variable"] + DEVICE_FLAGS
 
 SOURCES = ["plan.cpp", "validate.cpp", "validate_ops.cpp", "api.cpp", "api_ops.cpp", "timer.cpp",
-           "k_large.hip", "k_skinny.hip", "k_elem.hip", "k_norm.hip", "k_dropout.hip", "k_route.hip"]
+           "k_large.hip", "k_skinny.hip", "k_elem.hip", "k_norm_fwd.hip", "k_norm_bwd.hip", "k_dropout.hip", "k_route.hip"]
 
 
 def _compile(src: str) -> str:
@@ -38,7 +38,7 @@ def _compile(src: str) -> str:
 
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=min(7, len(SOURCES))) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         objs = list(ex.map(_compile, SOURCES))
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "-shared", "-fPIC", f"--offload-arch={ARCH}", *objs, "-o", tmp]

@@ -24,9 +24,19 @@ __global__ __launch_bounds__(kDropThreads) void dropout_kernel(DropoutArgs a, ui
   while (row < uint64_t(a.rows)) {
     const int64_t col = int64_t(vec) * 8;
     const int n = a.cols - col >= 8 ? 8 : int(a.cols - col);
+    // the row's end, as load_row8 takes it (columns here may pass 32 bits)
+    const bool whole = a.cols >= 8;
+    const int64_t at = whole ? (n < 8 ? a.cols - 8 : col) : col;
+    const int take = whole ? 8 : n;
     float v[8], rv[8];
-    unpack8(load8((const T*)a.x + row * a.ld_x + col, n), v);
-    if constexpr (RES) unpack8(load8((const T*)a.res + row * a.ld_res + col, n), rv);
+    Raw8<T> xr = load8((const T*)a.x + row * a.ld_x + at, take), rr;
+    if constexpr (RES) rr = load8((const T*)a.res + row * a.ld_res + at, take);
+    settle8(xr, n, take);
+    unpack8(xr, v);
+    if constexpr (RES) {
+      settle8(rr, n, take);
+      unpack8(rr, rv);
+    }
     const u32x4 w = drop_draws(a.drop, off, uint32_t(row), vec);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {

@@ -1,154 +1,9 @@
-// Layer norm over the rows of [rows, cols], forward and backward, alone or
-// fused with the residual add and dropout before it.
-//
-//   forward   mu = mean(x), r = 1 / sqrt(mean((x - mu)^2) + eps),
-//             y = (x - mu) r gamma + beta
-//   backward  xh = (x - mu) r, g = dy gamma,
-//             dx = r (g - mean(g) - xh mean(g xh)),
-//             dgamma = sum over rows of dy xh, dbeta = sum over rows of dy
-//   fused     h = residual + dropout(x), y = norm(h);
-//             dh = norm backward + the gradient that reaches h directly,
-//             dresidual = dh, dx = dropout of dh with the same mask
-//
-// A row is read once and held in registers by 8 to 1024 threads, so the mean
-// comes before the squared deviations are formed (no cancellation) without a
-// second pass over memory.  All sums are fp32; each output is rounded once.
-#include "ops_dev.hpp"
-
-// Products and sums are joined only where fmaf says so, so that every variant
-// of a kernel (fused or not, any row split) rounds alike.
-#pragma clang fp contract(off)
+// Layer norm, backward (see norm_dev.hpp).
+#include "norm_dev.hpp"
 
 namespace muon {
 
 namespace {
-
-// Sum over the NT threads of a row; `red` holds one word per wave and row.
-// The caller alternates two `red` buffers, so that one barrier per sum is
-// enough.
-template <int NT> __device__ __forceinline__ float row_sum(float v, float* red) {
-  if constexpr (NT <= 64) {
-    return lane_sum<NT>(v);
-  } else {
-    constexpr int NW = NT / 64;
-    v = lane_sum<64>(v);
-    const int wave = threadIdx.x / 64, first = wave / NW * NW;
-    if (threadIdx.x % 64 == 0) red[wave] = v;
-    __syncthreads();
-    float s = red[first];
-#pragma unroll
-    for (int i = 1; i < NW; ++i) s += red[first + i];
-    return s;
-  }
-}
-
-// Which of the workgroup's row groups a thread is in: the same for a whole
-// wave from 64 threads a row on, so that row addresses stay in scalar
-// registers (as lane values they spilled above 8192 columns).
-template <int NT> __device__ __forceinline__ int row_group() {
-  const int g = threadIdx.x / NT;
-  return NT >= 64 ? __builtin_amdgcn_readfirstlane(g) : g;
-}
-
-// gamma or beta as stored; `dflt` in the place of a null one.
-template <typename W> __device__ __forceinline__ Raw8<W> load_param(const void* p, unsigned col, int n) {
-  return load8((const W*)p + col, p ? n : 0);
-}
-template <typename W>
-__device__ __forceinline__ void unpack_param(const Raw8<W>& r, const void* p, float dflt, float (&v)[8]) {
-  unpack8(r, v);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = p ? v[i] : dflt;
-}
-
-// Bound by memory: x is read and y written once (16384 x 4096 bf16: 5 TB/s,
-// the rate of a large copy).  gamma and beta come from the cache, their loads
-// behind those of x; with three and more vectors a thread they are read after
-// the reductions, over which they would take registers.
-template <typename T, typename W, int NT, int NV, int WG, bool FUSED>
-__global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdArgs a) {
-  constexpr int RPB = WG / NT;
-  constexpr bool EARLY = NV <= 2;
-  __shared__ float red[2][WG / 64];
-  const int t = threadIdx.x % NT, sub = row_group<NT>();
-  const int cols = a.cols;
-  const uint64_t off = FUSED ? drop_offset(a.drop) : 0;
-  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < a.rows; row0 += int64_t(gridDim.x) * RPB) {
-    const int64_t row = row0 + sub;
-    const bool live = row < a.rows;
-    Raw8<T> xr[NV], rr[NV];
-    Raw8<W> gr[NV], br[NV];
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const unsigned col = 8 * (i * NT + t);
-      const int n = live ? cols - int(col) : 0;
-      xr[i] = load8((const T*)a.x + row * a.ld_x + col, n);
-      if constexpr (FUSED) rr[i] = load8((const T*)a.res + row * a.ld_res + col, n);
-    }
-    if constexpr (EARLY) {
-#pragma unroll
-      for (int i = 0; i < NV; ++i) {
-        const unsigned col = 8 * (i * NT + t);
-        gr[i] = load_param<W>(a.gamma, col, cols - int(col));
-        br[i] = load_param<W>(a.beta, col, cols - int(col));
-      }
-    }
-    float v[NV][8];
-    float s = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const unsigned col = 8 * (i * NT + t);
-      const int n = live ? cols - int(col) : 0;
-      unpack8(xr[i], v[i]);
-      if constexpr (FUSED) {
-        float rv[8];
-        unpack8(rr[i], rv);
-        const u32x4 w = drop_draws(a.drop, off, uint32_t(row), col / 8);
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          v[i][j] = drop_keeps(w, j, a.drop.thresh) ? fmaf(v[i][j], a.drop.scale, rv[j]) : rv[j];
-        // the norm is that of h as it is stored, so that the backward pass,
-        // which reads h, sees the same values
-        const Raw8<T> hr = pack8(v[i], (const T*)nullptr);
-        store8((T*)a.h + row * a.ld_h + col, n, hr);
-        unpack8(hr, v[i]);
-      }
-#pragma unroll
-      for (int j = 0; j < 8; ++j) s += j < n ? v[i][j] : 0.0f;
-    }
-    const float mean = row_sum<NT>(s, red[0]) / float(cols);
-    float q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int n = cols - 8 * (i * NT + t);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        v[i][j] -= mean;
-        q = j < n ? fmaf(v[i][j], v[i][j], q) : q;
-      }
-    }
-    const float rstd = 1.0f / sqrtf(row_sum<NT>(q, red[1]) / float(cols) + a.eps);
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const unsigned col = 8 * (i * NT + t);
-      const int n = live ? cols - int(col) : 0;
-      if constexpr (!EARLY) {
-        gr[i] = load_param<W>(a.gamma, col, n);
-        br[i] = load_param<W>(a.beta, col, n);
-      }
-      float gv[8], bv[8];
-      unpack_param(gr[i], a.gamma, 1.0f, gv);
-      unpack_param(br[i], a.beta, 0.0f, bv);
-#pragma unroll
-      for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * rstd, gv[j], bv[j]);
-      store8((T*)a.y + row * a.ld_y + col, n, pack8(v[i], (const T*)nullptr));
-    }
-    if (live && t == 0) {
-      if (a.mean) a.mean[row] = mean;
-      if (a.rstd) a.rstd[row] = rstd;
-    }
-  }
-}
 
 // Two sums over the NT threads of a row with one barrier (see row_sum; `red`
 // alternates from row to row).
@@ -182,7 +37,7 @@ template <typename T, int NV> struct RowPart {
   float mean, rstd;
 };
 
-template <typename T, int NT, int NV, bool FUSED>
+template <typename T, int NT, int NV, bool FUSED, bool RAG>
 __device__ __forceinline__ void fetch_row(const NormBwdArgs& a, int64_t row, int t, RowPart<T, NV>& r) {
   const bool live = row < a.rows;
   r.mean = live ? a.mean[row] : 0.0f;
@@ -191,10 +46,22 @@ __device__ __forceinline__ void fetch_row(const NormBwdArgs& a, int64_t row, int
   for (int i = 0; i < NV; ++i) {
     const unsigned col = 8 * (i * NT + opaque(t));
     const int n = live ? a.cols - int(col) : 0;
-    r.x[i] = load8((const T*)a.x + row * a.ld_x + col, n);
-    r.dy[i] = load8((const T*)a.dy + row * a.ld_dy + col, n);
+    r.x[i] = load_vec<RAG>((const T*)a.x + row * a.ld_x, col, n, a.cols);
+    r.dy[i] = load_vec<RAG>((const T*)a.dy + row * a.ld_dy, col, n, a.cols);
     if constexpr (FUSED)
-      if (a.dh) r.dh[i] = load8((const T*)a.dh + row * a.ld_dh + col, n);
+      if (a.dh) r.dh[i] = load_vec<RAG>((const T*)a.dh + row * a.ld_dh, col, n, a.cols);
+  }
+}
+
+template <typename T, int NT, int NV, bool FUSED, bool RAG>
+__device__ __forceinline__ void settle_row(const NormBwdArgs& a, bool live, int t, RowPart<T, NV>& r) {
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int n = live ? a.cols - 8 * (i * NT + opaque(t)) : 0;
+    settle<RAG>(r.x[i], n, a.cols);
+    settle<RAG>(r.dy[i], n, a.cols);
+    if constexpr (FUSED)
+      if (a.dh) settle<RAG>(r.dh[i], n, a.cols);
   }
 }
 
@@ -205,7 +72,7 @@ __device__ __forceinline__ void hide(Raw8<uint16_t>& v) { asm volatile("" : "+v"
 __device__ __forceinline__ void hide(Raw8<float>& v) { asm volatile("" : "+v"(v.a), "+v"(v.b)); }
 
 // Stores dx of one vector, and with FUSED dres.
-template <typename T, typename W, bool FUSED>
+template <typename T, typename W, bool FUSED, bool RAG>
 __device__ __forceinline__ void emit_dx(const NormBwdArgs& a, int64_t row, unsigned col, int n, const Raw8<T>& xr,
                                         const Raw8<T>& dr, const Raw8<T>& hr, const float (&gv)[8], float mean,
                                         float rstd, float c1, float c2, uint64_t off) {
@@ -223,18 +90,18 @@ __device__ __forceinline__ void emit_dx(const NormBwdArgs& a, int64_t row, unsig
 #pragma unroll
       for (int j = 0; j < 8; ++j) dv[j] += xv[j];
     }
-    store8((T*)a.dres + row * a.ld_dres + col, n, pack8(dv, (const T*)nullptr));
+    store_vec<RAG>((T*)a.dres + row * a.ld_dres + col, n, pack8(dv, (const T*)nullptr));
     const u32x4 w = drop_draws(a.drop, off, uint32_t(row), col / 8);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dv[j] = drop_keeps(w, j, a.drop.thresh) ? dv[j] * a.drop.scale : 0.0f;
   }
-  store8((T*)a.dx + row * a.ld_dx + col, n, pack8(dv, (const T*)nullptr));
+  store_vec<RAG>((T*)a.dx + row * a.ld_dx + col, n, pack8(dv, (const T*)nullptr));
 }
 
 // dgamma and dbeta of 64 columns over all rows, for few rows: 8 threads take the
 // columns' vectors of a row, the others the further rows; a wave's rows are
 // joined across its lanes, the waves in LDS.
-template <typename T, typename W, int WG>
+template <typename T, typename W, int WG, bool RAG>
 __device__ __forceinline__ void few_rows_sums(const NormBwdArgs& a, int strip, float (*sums)[2][64]) {
   const int vec = threadIdx.x & 7, wave = threadIdx.x >> 6;
   const unsigned col = strip * 64 + vec * 8;
@@ -244,8 +111,12 @@ __device__ __forceinline__ void few_rows_sums(const NormBwdArgs& a, int strip, f
   for (int j = 0; j < 8; ++j) dg[j] = db[j] = 0.0f;
   for (int64_t row = threadIdx.x >> 3; row < a.rows; row += WG / 8) {
     float xv[8], dv[8];
-    unpack8(load8((const T*)a.x + row * a.ld_x + col, n), xv);
-    unpack8(load8((const T*)a.dy + row * a.ld_dy + col, n), dv);
+    Raw8<T> xr = load_vec<RAG>((const T*)a.x + row * a.ld_x, col, n, a.cols);
+    Raw8<T> dr = load_vec<RAG>((const T*)a.dy + row * a.ld_dy, col, n, a.cols);
+    settle<RAG>(xr, n, a.cols);
+    settle<RAG>(dr, n, a.cols);
+    unpack8(xr, xv);
+    unpack8(dr, dv);
     const float mean = a.mean[row], rstd = a.rstd[row];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -297,7 +168,7 @@ enum NormSums {
 // or gains nothing (2000 x 9000 bf16, two vectors: 39.8 without, 44.9 with).
 // Rows above 20480 columns have no registers for the sums: see
 // norm_cols_kernel.
-template <typename T, typename W, int NT, int NV, int WG, bool FUSED, NormSums WHERE>
+template <typename T, typename W, int NT, int NV, int WG, bool FUSED, bool RAG, NormSums WHERE>
 __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
   constexpr int RPB = WG / NT, JOIN = NT < 64 ? WG / 64 : RPB;
   constexpr bool SUMS = WHERE == kSumsHere, AHEAD = SUMS && !FUSED && NV == 1;
@@ -307,7 +178,7 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
     __shared__ float strips[WG / 64][2][64];
     const int first = int((a.rows + RPB - 1) / RPB);
     if (int(blockIdx.x) >= first) {
-      few_rows_sums<T, W, WG>(a, int(blockIdx.x) - first, strips);
+      few_rows_sums<T, W, WG, RAG>(a, int(blockIdx.x) - first, strips);
       return;
     }
   }
@@ -318,7 +189,8 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     const unsigned col = 8 * (i * NT + opaque(t));
-    gr[i] = load_param<W>(a.gamma, col, cols - int(col));
+    gr[i] = load_param<RAG, W>(a.gamma, col, cols);
+    settle<RAG>(gr[i], cols - int(col), cols);
 #pragma unroll
     for (int j = 0; j < 8; ++j) dg[i][j] = db[i][j] = 0.0f;
   }
@@ -326,14 +198,15 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
   const float inv = 1.0f / float(cols);
   const int64_t step = int64_t(gridDim.x) * RPB;
   RowPart<T, NV> r;
-  if constexpr (AHEAD) fetch_row<T, NT, NV, FUSED>(a, int64_t(blockIdx.x) * RPB + sub, t, r);
+  if constexpr (AHEAD) fetch_row<T, NT, NV, FUSED, RAG>(a, int64_t(blockIdx.x) * RPB + sub, t, r);
   int side = 0;
   for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < a.rows; row0 += step) {
     const int64_t row = row0 + sub;
     const bool live = row < a.rows;
     RowPart<T, NV> next;
-    if constexpr (AHEAD) fetch_row<T, NT, NV, FUSED>(a, row + step, t, next);
-    else fetch_row<T, NT, NV, FUSED>(a, row, t, r);
+    if constexpr (AHEAD) fetch_row<T, NT, NV, FUSED, RAG>(a, row + step, t, next);
+    else fetch_row<T, NT, NV, FUSED, RAG>(a, row, t, r);
+    settle_row<T, NT, NV, FUSED, RAG>(a, live, t, r);
     float s1 = 0.0f, s2 = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -366,7 +239,7 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
       }
       float gv[8];
       unpack_param(gr[i], a.gamma, 1.0f, gv);
-      emit_dx<T, W, FUSED>(a, row, col, live ? cols - int(col) : 0, r.x[i], r.dy[i], r.dh[i], gv, r.mean, r.rstd, c1,
+      emit_dx<T, W, FUSED, RAG>(a, row, col, live ? cols - int(col) : 0, r.x[i], r.dy[i], r.dh[i], gv, r.mean, r.rstd, c1,
                            c2, off);
     }
     if constexpr (AHEAD) r = next;
@@ -414,7 +287,7 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
 // dy: blockIdx.x takes 2048 columns, a vector a thread, and blockIdx.y every
 // gridDim.y-th row.  With the sums in norm_bwd_kernel four vectors a thread
 // spilled (2048 x 32768 bf16: 288 us).
-template <typename T>
+template <typename T, bool RAG>
 __global__ __launch_bounds__(256) void norm_cols_kernel(NormBwdArgs a) {
   const unsigned col = 8 * (blockIdx.x * 256 + threadIdx.x);
   const int n = a.cols - int(col);
@@ -424,8 +297,12 @@ __global__ __launch_bounds__(256) void norm_cols_kernel(NormBwdArgs a) {
 #pragma unroll 4
   for (int64_t row = blockIdx.y; row < a.rows; row += gridDim.y) {
     float xv[8], dv[8];
-    unpack8(load8((const T*)a.x + row * a.ld_x + col, n), xv);
-    unpack8(load8((const T*)a.dy + row * a.ld_dy + col, n), dv);
+    Raw8<T> xr = load_vec<RAG>((const T*)a.x + row * a.ld_x, col, n, a.cols);
+    Raw8<T> dr = load_vec<RAG>((const T*)a.dy + row * a.ld_dy, col, n, a.cols);
+    settle<RAG>(xr, n, a.cols);
+    settle<RAG>(dr, n, a.cols);
+    unpack8(xr, xv);
+    unpack8(dr, dv);
     const float mean = a.mean[row], rstd = a.rstd[row];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -468,59 +345,27 @@ __global__ __launch_bounds__(kGradCols* kGradSlices) void norm_grad_kernel(const
   }
 }
 
-template <typename T, typename W, bool FUSED> struct NormLaunch {
-  // One group of rows a workgroup: new workgroups keep loads in flight while
-  // others reduce (16384 x 4096 bf16: 48.8 us; 52.6 to 66.3 with the rows
-  // dealt to 512 .. 2048 workgroups that loop).
-  template <int NT, int NV> static void fwd(const NormFwdArgs& a, hipStream_t st) {
-    constexpr int WG = NT < 256 ? 256 : NT;
-    const int64_t need = (a.rows + WG / NT - 1) / (WG / NT);
-    hipLaunchKernelGGL((norm_fwd_kernel<T, W, NT, NV, WG, FUSED>), dim3(unsigned(std::min(need, kOpsMaxGrid))),
-                       dim3(WG), 0, st, a);
-  }
+template <typename T, typename W, bool FUSED, bool RAG> struct BwdLaunch {
   template <int NT, int NV, int WG> static void bwd(const NormBwdArgs& a, hipStream_t st) {
-    hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, WG, FUSED, kSumsHere>), dim3(unsigned(a.parts)), dim3(WG), 0, st,
+    hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, WG, FUSED, RAG, kSumsHere>), dim3(unsigned(a.parts)), dim3(WG), 0, st,
                        a);
   }
   template <int NT> static void bwd(const NormBwdArgs& a, int wg, hipStream_t st) {
     wg == 256 ? bwd<NT, 1, 256>(a, st) : bwd<NT, 1, 1024>(a, st);
   }
   template <int NT, int NV> static void bwd_apart(const NormBwdArgs& a, bool grads, hipStream_t st) {
-    hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, NT, FUSED, kSumsApart>),
+    hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, NT, FUSED, RAG, kSumsApart>),
                        dim3(unsigned(std::min(a.rows, kOpsMaxGrid))), dim3(NT), 0, st, a);
     if (grads)
-      hipLaunchKernelGGL((norm_cols_kernel<T>), dim3(unsigned((a.cols + 2047) / 2048), unsigned(a.parts)), dim3(256), 0,
+      hipLaunchKernelGGL((norm_cols_kernel<T, RAG>), dim3(unsigned((a.cols + 2047) / 2048), unsigned(a.parts)), dim3(256), 0,
                          st, a);
   }
   template <int NT, int NV> static void bwd_few(const NormBwdArgs& a, hipStream_t st) {
     constexpr int WG = NT < 256 ? 256 : NT;
     const int64_t groups = (a.rows + WG / NT - 1) / (WG / NT), strips = (a.dgamma || a.dbeta) ? (a.cols + 63) / 64 : 0;
     if (groups + strips > 0)
-      hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, WG, FUSED, kSumsFew>), dim3(unsigned(groups + strips)), dim3(WG),
+      hipLaunchKernelGGL((norm_bwd_kernel<T, W, NT, NV, WG, FUSED, RAG, kSumsFew>), dim3(unsigned(groups + strips)), dim3(WG),
                          0, st, a);
-  }
-  static hipError_t fwd(const NormFwdArgs& a, hipStream_t st) {
-    // The narrowest fit that keeps several workgroups on a compute unit: three
-    // to five vectors a thread rather than 512 or 1024 threads a row (8192
-    // columns bf16: 51.6 us with 256 threads, 66.6 with 512; 20000 columns: 61
-    // with 512, 105 with 1024; 2048 columns: 48.6 with 128, 59.6 with 256; 200
-    // columns, 65536 rows: 17.9 with 32, 29.9 with 64).
-    const int vecs = (a.cols + 7) / 8;
-    if (vecs <= 8) fwd<8, 1>(a, st);
-    else if (vecs <= 16) fwd<16, 1>(a, st);
-    else if (vecs <= 32) fwd<32, 1>(a, st);
-    else if (vecs <= 64) fwd<64, 1>(a, st);
-    else if (vecs <= 128) fwd<64, 2>(a, st);
-    else if (vecs <= 256) fwd<128, 2>(a, st);
-    else if (vecs <= 512) fwd<256, 2>(a, st);
-    else if (vecs <= 768) fwd<256, 3>(a, st);
-    else if (vecs <= 1024) fwd<256, 4>(a, st);
-    else if (vecs <= 1280) fwd<256, 5>(a, st);
-    else if (vecs <= 1536) fwd<512, 3>(a, st);
-    else if (vecs <= 2048) fwd<512, 4>(a, st);
-    else if (vecs <= 2560) fwd<512, 5>(a, st);
-    else fwd<1024, 4>(a, st);
-    return hipGetLastError();
   }
   static hipError_t bwd(const NormBwdArgs& a, hipStream_t st) {
     const NormBwdSplit sp = norm_bwd_split(a.rows, a.cols);
@@ -563,24 +408,10 @@ template <typename T, typename W, bool FUSED> struct NormLaunch {
   }
 };
 
-template <typename A, typename F> hipError_t by_types(const A& a, bool bf16, bool wbf16, bool fused, F f) {
-  auto go = [&](auto t, auto w) {
-    typedef decltype(t) T;
-    typedef decltype(w) W;
-    return fused ? f(NormLaunch<T, W, true>{}) : f(NormLaunch<T, W, false>{});
-  };
-  if (bf16) return wbf16 ? go(uint16_t{}, uint16_t{}) : go(uint16_t{}, float{});
-  return wbf16 ? go(float{}, uint16_t{}) : go(float{}, float{});
-}
-
 }  // namespace
 
-hipError_t run_norm_fwd(const NormFwdArgs& a, bool bf16, bool wbf16, bool fused, hipStream_t st) {
-  return by_types(a, bf16, wbf16, fused, [&](auto l) { return l.fwd(a, st); });
-}
-
 hipError_t run_norm_bwd(const NormBwdArgs& a, bool bf16, bool wbf16, bool fused, hipStream_t st) {
-  return by_types(a, bf16, wbf16, fused, [&](auto l) { return l.bwd(a, st); });
+  return norm_by_types<BwdLaunch>(a.cols, bf16, wbf16, fused, [&](auto l) { return l.bwd(a, st); });
 }
 
 }  // namespace muon

@@ -1,0 +1,143 @@
+// Layer norm, forward (see norm_dev.hpp).
+#include "norm_dev.hpp"
+
+namespace muon {
+
+namespace {
+
+// Bound by memory: x is read and y written once (16384 x 4096 bf16: 5 TB/s,
+// the rate of a large copy).  gamma and beta come from the cache, their loads
+// behind those of x; with three and more vectors a thread they are read after
+// the reductions, over which they would take registers.
+template <typename T, typename W, int NT, int NV, int WG, bool FUSED, bool RAG>
+__global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdArgs a) {
+  constexpr int RPB = WG / NT;
+  constexpr bool EARLY = NV <= 2;
+  __shared__ float red[2][WG / 64];
+  const int t = threadIdx.x % NT, sub = row_group<NT>();
+  const int cols = a.cols;
+  const uint64_t off = FUSED ? drop_offset(a.drop) : 0;
+  for (int64_t row0 = int64_t(blockIdx.x) * RPB; row0 < a.rows; row0 += int64_t(gridDim.x) * RPB) {
+    const int64_t row = row0 + sub;
+    const bool live = row < a.rows;
+    Raw8<T> xr[NV], rr[NV];
+    Raw8<W> gr[NV], br[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const unsigned col = 8 * (i * NT + t);
+      const int n = live ? cols - int(col) : 0;
+      xr[i] = load_vec<RAG>((const T*)a.x + row * a.ld_x, col, n, a.cols);
+      if constexpr (FUSED) rr[i] = load_vec<RAG>((const T*)a.res + row * a.ld_res, col, n, a.cols);
+    }
+    if constexpr (EARLY) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const unsigned col = 8 * (i * NT + t);
+        gr[i] = load_param<RAG, W>(a.gamma, col, cols);
+        br[i] = load_param<RAG, W>(a.beta, col, cols);
+      }
+    }
+    float v[NV][8];
+    float s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const unsigned col = 8 * (i * NT + t);
+      const int n = live ? cols - int(col) : 0;
+      settle<RAG>(xr[i], n, cols);
+      unpack8(xr[i], v[i]);
+      if constexpr (FUSED) {
+        float rv[8];
+        settle<RAG>(rr[i], n, cols);
+        unpack8(rr[i], rv);
+        const u32x4 w = drop_draws(a.drop, off, uint32_t(row), col / 8);
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          v[i][j] = drop_keeps(w, j, a.drop.thresh) ? fmaf(v[i][j], a.drop.scale, rv[j]) : rv[j];
+        // the norm is that of h as it is stored, so that the backward pass,
+        // which reads h, sees the same values
+        const Raw8<T> hr = pack8(v[i], (const T*)nullptr);
+        store_vec<RAG>((T*)a.h + row * a.ld_h + col, n, hr);
+        unpack8(hr, v[i]);
+      }
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s += !RAG || j < n ? v[i][j] : 0.0f;  // 0 in a vector that does not exist
+    }
+    const float mean = row_sum<NT>(s, red[0]) / float(cols);
+    float q = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int n = cols - 8 * (i * NT + t);
+      const float m = RAG || n > 0 ? mean : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        v[i][j] -= m;
+        q = !RAG || j < n ? fmaf(v[i][j], v[i][j], q) : q;
+      }
+    }
+    const float rstd = 1.0f / sqrtf(row_sum<NT>(q, red[1]) / float(cols) + a.eps);
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const unsigned col = 8 * (i * NT + t);
+      const int n = live ? cols - int(col) : 0;
+      if constexpr (!EARLY) {
+        gr[i] = load_param<RAG, W>(a.gamma, col, cols);
+        br[i] = load_param<RAG, W>(a.beta, col, cols);
+      }
+      float gv[8], bv[8];
+      settle<RAG>(gr[i], cols - int(col), cols);
+      settle<RAG>(br[i], cols - int(col), cols);
+      unpack_param(gr[i], a.gamma, 1.0f, gv);
+      unpack_param(br[i], a.beta, 0.0f, bv);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = fmaf(v[i][j] * rstd, gv[j], bv[j]);
+      store_vec<RAG>((T*)a.y + row * a.ld_y + col, n, pack8(v[i], (const T*)nullptr));
+    }
+    if (live && t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+  }
+}
+
+template <typename T, typename W, bool FUSED, bool RAG> struct FwdLaunch {
+  // One group of rows a workgroup: new workgroups keep loads in flight while
+  // others reduce (16384 x 4096 bf16: 48.8 us; 52.6 to 66.3 with the rows
+  // dealt to 512 .. 2048 workgroups that loop).
+  template <int NT, int NV> static void fwd(const NormFwdArgs& a, hipStream_t st) {
+    constexpr int WG = NT < 256 ? 256 : NT;
+    const int64_t need = (a.rows + WG / NT - 1) / (WG / NT);
+    hipLaunchKernelGGL((norm_fwd_kernel<T, W, NT, NV, WG, FUSED, RAG>), dim3(unsigned(std::min(need, kOpsMaxGrid))),
+                       dim3(WG), 0, st, a);
+  }
+  static hipError_t fwd(const NormFwdArgs& a, hipStream_t st) {
+    // The narrowest fit that keeps several workgroups on a compute unit: three
+    // to five vectors a thread rather than 512 or 1024 threads a row (8192
+    // columns bf16: 51.6 us with 256 threads, 66.6 with 512; 20000 columns: 61
+    // with 512, 105 with 1024; 2048 columns: 48.6 with 128, 59.6 with 256; 200
+    // columns, 65536 rows: 17.9 with 32, 29.9 with 64).
+    const int vecs = (a.cols + 7) / 8;
+    if (vecs <= 8) fwd<8, 1>(a, st);
+    else if (vecs <= 16) fwd<16, 1>(a, st);
+    else if (vecs <= 32) fwd<32, 1>(a, st);
+    else if (vecs <= 64) fwd<64, 1>(a, st);
+    else if (vecs <= 128) fwd<64, 2>(a, st);
+    else if (vecs <= 256) fwd<128, 2>(a, st);
+    else if (vecs <= 512) fwd<256, 2>(a, st);
+    else if (vecs <= 768) fwd<256, 3>(a, st);
+    else if (vecs <= 1024) fwd<256, 4>(a, st);
+    else if (vecs <= 1280) fwd<256, 5>(a, st);
+    else if (vecs <= 1536) fwd<512, 3>(a, st);
+    else if (vecs <= 2048) fwd<512, 4>(a, st);
+    else if (vecs <= 2560) fwd<512, 5>(a, st);
+    else fwd<1024, 4>(a, st);
+    return hipGetLastError();
+  }
+};
+
+}  // namespace
+
+hipError_t run_norm_fwd(const NormFwdArgs& a, bool bf16, bool wbf16, bool fused, hipStream_t st) {
+  return norm_by_types<FwdLaunch>(a.cols, bf16, wbf16, fused, [&](auto l) { return l.fwd(a, st); });
+}
+
+}  // namespace muon
