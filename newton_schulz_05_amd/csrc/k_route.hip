@@ -5,8 +5,8 @@
 // gates (the counts c are constants):
 //   dp_te = coef E c_e / (k n^2) dL + [e chosen] (gradient of its gate),
 //   dlogit = p (dp - sum_e p dp).
-// A group of 8 or 16 lanes holds one token's logits in registers, each lane
-// PER consecutive experts, so the maximum, the sums and the choices are
+// A group of 8 or 16 lanes holds one token's logits in registers, each lane PER
+// of them (see expert_of), so the maximum, the sums and the choices are
 // reductions over at most 16 lanes, all of them single DPP steps.
 #include "ops_dev.hpp"
 
@@ -54,10 +54,18 @@ template <int N> __device__ __forceinline__ uint32_t lane_min(uint32_t v) {
   return lane_reduce<N>(v, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
 }
 
+// The i-th expert of lane t: runs of 8 dealt to the lanes in turn, so that a
+// group's 16-byte accesses are adjacent (backward of 32768 x 256 fp32 20.1 us,
+// 23.7 with PER consecutive experts a lane); fewer than 8 a lane are
+// consecutive.  Experts rise with i.
+template <int LANES, int PER> __device__ __forceinline__ int expert_of(int t, int i) {
+  return PER >= 8 ? ((i >> 3) * LANES + t) * 8 + (i & 7) : t * PER + i;
+}
+
 // Takes the largest key left among the group's lanes out of `key`; returns it
 // and its expert (a key up to kNone once none is left).
 template <typename T, int LANES, int PER>
-__device__ __forceinline__ uint32_t take_largest(uint32_t (&key)[PER], int base, int& expert) {
+__device__ __forceinline__ uint32_t take_largest(uint32_t (&key)[PER], int t, int& expert) {
   if constexpr (sizeof(T) == 2) {
     uint32_t best = key[0];
 #pragma unroll
@@ -75,10 +83,9 @@ __device__ __forceinline__ uint32_t take_largest(uint32_t (&key)[PER], int base,
       best = key[i] > best ? key[i] : best;
     }
     const uint32_t m = lane_max<LANES>(best);
-    expert = int(lane_min<LANES>(best == m ? base + at : 0xffffu));
-    const int mine = expert - base;
+    expert = int(lane_min<LANES>(best == m ? uint32_t(expert_of<LANES, PER>(t, at)) : 0xffffu));
 #pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = mine == i ? 0u : key[i];
+    for (int i = 0; i < PER; ++i) key[i] = expert == expert_of<LANES, PER>(t, i) ? 0u : key[i];
     return m;
   }
 }
@@ -108,25 +115,33 @@ template <typename T> __device__ __forceinline__ T narrow(float x);
 template <> __device__ __forceinline__ uint16_t narrow<uint16_t>(float x) { return f2bf(x); }
 template <> __device__ __forceinline__ float narrow<float>(float x) { return x; }
 
-// A lane's PER logits as stored, by one access where all PER exist (at any
-// alignment of an element, like load8); floats(): -inf where there is none.
-template <typename T, int PER> struct Logits {
+// Lane t's PER logits of a token that has `have` of them (0: none are read), as
+// stored, by one access for each run that exists whole (at any alignment of an
+// element, like load8); floats(): -inf where there is none.
+template <typename T, int LANES, int PER> struct Logits {
   typedef T V __attribute__((ext_vector_type(PER < 8 ? PER : 1)));
   typedef T VU __attribute__((ext_vector_type(PER < 8 ? PER : 1), aligned(sizeof(T))));
   Raw8<T> many[PER < 8 ? 1 : PER / 8];
   V few;
-  __device__ __forceinline__ void load(const T* p, int n) {
+  __device__ __forceinline__ void load(const T* row, int t, int have) {
     if constexpr (PER >= 8) {
 #pragma unroll
-      for (int i = 0; i < PER; i += 8) many[i / 8] = load8(p + i, n - i);
-    } else if (n >= PER) {
-      few = *(const VU*)p;
+      for (int i = 0; i < PER; i += 8) {
+        const int e = expert_of<LANES, PER>(t, i);
+        many[i / 8] = load8(row + e, have - e);
+      }
     } else {
+      const T* p = row + t * PER;
+      const int n = have - t * PER;
+      if (n >= PER) {
+        few = *(const VU*)p;
+      } else {
 #pragma unroll
-      for (int i = 0; i < PER; ++i) few[i] = i < n ? p[i] : T(0);
+        for (int i = 0; i < PER; ++i) few[i] = i < n ? p[i] : T(0);
+      }
     }
   }
-  __device__ __forceinline__ void floats(int n, float (&v)[PER]) const {
+  __device__ __forceinline__ void floats(int t, int have, float (&v)[PER]) const {
     if constexpr (PER >= 8) {
 #pragma unroll
       for (int i = 0; i < PER; i += 8) {
@@ -139,9 +154,9 @@ template <typename T, int PER> struct Logits {
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[i] = widen(few[i]);
     }
-    if (__ballot(n < PER)) {  // padding tokens, experts that are no multiple of the lanes' share
+    if (__ballot(have < LANES * PER)) {  // padding tokens, experts that do not fill the lanes
 #pragma unroll
-      for (int i = 0; i < PER; ++i) v[i] = i < n ? v[i] : -INFINITY;
+      for (int i = 0; i < PER; ++i) v[i] = expert_of<LANES, PER>(t, i) < have ? v[i] : -INFINITY;
     }
   }
 };
@@ -170,7 +185,6 @@ __global__ __launch_bounds__(WG) void route_fwd_kernel(RouteArgs a) {
   __shared__ float sums[WAVES][LANES * PER];
   __shared__ int32_t ntok;
   const int t = threadIdx.x % LANES, sub = threadIdx.x / LANES;
-  const int base = t * PER, mine = a.experts - base;
   for (int e = threadIdx.x; e < LANES * PER; e += WG) hist[e] = 0;
   if (threadIdx.x == 0) {
     ntok = 0;
@@ -184,20 +198,20 @@ __global__ __launch_bounds__(WG) void route_fwd_kernel(RouteArgs a) {
   for (int64_t row0 = int64_t(blockIdx.x) * TOK; row0 < a.rows; row0 += int64_t(gridDim.x) * TOK) {
     const int64_t row = row0 + sub;
     const bool in = row < a.rows;
-    const int have = in && (!a.valid || a.valid[row] != 0) ? mine : 0;  // of the lane's logits
-    Logits<T, PER> raw;
-    raw.load((const T*)a.logits + row * a.ld + base, have);
+    const int have = in && (!a.valid || a.valid[row] != 0) ? a.experts : 0;
+    Logits<T, LANES, PER> raw;
+    raw.load((const T*)a.logits + row * a.ld, t, have);
     float v[PER];
-    raw.floats(have, v);
+    raw.floats(t, have, v);
     uint32_t key[PER];
 #pragma unroll
-    for (int i = 0; i < PER; ++i) key[i] = Choice<T>::key(v[i], base + i);
+    for (int i = 0; i < PER; ++i) key[i] = Choice<T>::key(v[i], expert_of<LANES, PER>(t, i));
     int expert;
-    const uint32_t top = take_largest<T, LANES, PER>(key, base, expert);
+    const uint32_t top = take_largest<T, LANES, PER>(key, t, expert);
     uint32_t won = t == 0 ? top : 0u;
     int idx = expert;
     for (int j = 1; j < a.k; ++j) {
-      const uint32_t m = take_largest<T, LANES, PER>(key, base, expert);
+      const uint32_t m = take_largest<T, LANES, PER>(key, t, expert);
       won = t == j ? m : won;
       idx = t == j ? expert : idx;
     }
@@ -231,7 +245,7 @@ __global__ __launch_bounds__(WG) void route_fwd_kernel(RouteArgs a) {
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const float s = across_groups<LANES>(psum[i]);
-    if ((threadIdx.x & 63) < LANES) sums[threadIdx.x / 64][base + i] = s;
+    if ((threadIdx.x & 63) < LANES) sums[threadIdx.x / 64][expert_of<LANES, PER>(t, i)] = s;
   }
   __syncthreads();
   const bool lone = gridDim.x == 1;
@@ -358,14 +372,14 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
   constexpr int TOK = kRouteBwdThreads / LANES;
   __shared__ __attribute__((aligned(16))) float slots[TOK][PER > 2 ? LANES * PER : 1];
   const int t = threadIdx.x % LANES, sub = threadIdx.x / LANES;
-  const int base = t * PER, mine = a.experts - base;
   // A constant added to every dp of a token changes nothing (sum p = 1), so
   // the counts enter as E c_e - sum c, exact in fp64: near balance the
   // differences are what matters.
   int32_t c[PER], own = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    c[i] = i < mine ? a.counts[base + i] : 0;
+    const int e = expert_of<LANES, PER>(t, i);
+    c[i] = e < a.experts ? a.counts[e] : 0;
     own += c[i];
   }
   const int32_t all = lane_reduce<LANES>(own, [](int32_t x, int32_t y) { return x + y; });
@@ -378,8 +392,9 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
     const int64_t row = row0 + sub;
     const bool in = row < a.rows;
     const bool live = in && (!a.valid || a.valid[row] != 0);
-    Logits<T, PER> raw;
-    raw.load((const T*)a.logits + row * a.ld + base, live ? mine : 0);
+    const int have = live ? a.experts : 0;
+    Logits<T, LANES, PER> raw;
+    raw.load((const T*)a.logits + row * a.ld, t, have);
     // lane t holds the token's choice t
     int idx = -1;
     float dg = 0.0f;
@@ -392,7 +407,7 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
       }
     }
     float v[PER];
-    raw.floats(live ? mine : 0, v);
+    raw.floats(t, have, v);
     float mx = v[0];
 #pragma unroll
     for (int i = 1; i < PER; ++i) mx = fmaxf(mx, v[i]);
@@ -421,14 +436,14 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
       float* mem = slots[sub];
       if constexpr (PER > 2) {
 #pragma unroll
-        for (int i = 0; i < PER; ++i) mem[base + i] = dp[i];
+        for (int i = 0; i < PER; ++i) mem[expert_of<LANES, PER>(t, i)] = dp[i];
         wave_lds_order();
       }
-      add_choices<LANES, PER, 0>(dp, mem, t, idx, dg, base, a.k);
+      add_choices<LANES, PER, 0>(dp, mem, t, idx, dg, t * PER, a.k);
       if constexpr (PER > 2) {
         wave_lds_order();
 #pragma unroll
-        for (int i = 0; i < PER; ++i) dp[i] = mem[base + i];
+        for (int i = 0; i < PER; ++i) dp[i] = mem[expert_of<LANES, PER>(t, i)];
         wave_lds_order();
       }
     }
@@ -442,24 +457,25 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] *= dp[i] - dot;
     if (in) {
-      T* out = (T*)a.dlogits + row * a.ld_d + base;
+      T* out = (T*)a.dlogits + row * a.ld_d;
       if constexpr (PER >= 8) {
 #pragma unroll
         for (int i = 0; i < PER; i += 8) {
+          const int e = expert_of<LANES, PER>(t, i);
           float w[8];
 #pragma unroll
           for (int j = 0; j < 8; ++j) w[j] = v[i + j];
-          store8(out + i, mine - i, pack8(w, (const T*)nullptr));
+          store8(out + e, a.experts - e, pack8(w, (const T*)nullptr));
         }
-      } else if (mine >= PER) {
-        typename Logits<T, PER>::V w;
+      } else if (t * PER + PER <= a.experts) {
+        typename Logits<T, LANES, PER>::V w;
 #pragma unroll
         for (int i = 0; i < PER; ++i) w[i] = narrow<T>(v[i]);
-        *(typename Logits<T, PER>::VU*)out = w;
+        *(typename Logits<T, LANES, PER>::VU*)(out + t * PER) = w;
       } else {
 #pragma unroll
         for (int i = 0; i < PER; ++i)
-          if (i < mine) Elem<T>::store(out + i, v[i]);
+          if (t * PER + i < a.experts) Elem<T>::store(out + t * PER + i, v[i]);
       }
     }
   }
