@@ -372,6 +372,21 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
   constexpr int TOK = kRouteBwdThreads / LANES;
   __shared__ __attribute__((aligned(16))) float slots[TOK][PER > 2 ? LANES * PER : 1];
   const int t = threadIdx.x % LANES, sub = threadIdx.x / LANES;
+  // one token of a group; the first one's loads are under way while the
+  // balance terms, which wait for the counts, are formed
+  Logits<T, LANES, PER> raw;
+  int have = 0, idx = -1;
+  float dg = 0.0f;
+  auto fetch = [&](int64_t row) {
+    const bool live = row < a.rows && (!a.valid || a.valid[row] != 0);
+    have = live ? a.experts : 0;
+    raw.load((const T*)a.logits + row * a.ld, t, have);
+    // lane t holds the token's choice t
+    const bool mine = live && a.dgates && t < a.k;
+    idx = mine ? a.idx[row * a.k + t] : -1;
+    dg = mine ? a.dgates[row * a.k + t] : 0.0f;
+  };
+  fetch(int64_t(blockIdx.x) * TOK + sub);
   // A constant added to every dp of a token changes nothing (sum p = 1), so
   // the counts enter as E c_e - sum c, exact in fp64: near balance the
   // differences are what matters.
@@ -388,23 +403,13 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
   float bal[PER];
 #pragma unroll
   for (int i = 0; i < PER; ++i) bal[i] = float(up * (double(c[i]) * a.experts - double(all)));
-  for (int64_t row0 = int64_t(blockIdx.x) * TOK; row0 < a.rows; row0 += int64_t(gridDim.x) * TOK) {
+  const int64_t step = int64_t(gridDim.x) * TOK;
+  for (int64_t row0 = int64_t(blockIdx.x) * TOK; row0 < a.rows; row0 += step) {
     const int64_t row = row0 + sub;
     const bool in = row < a.rows;
-    const bool live = in && (!a.valid || a.valid[row] != 0);
-    const int have = live ? a.experts : 0;
-    Logits<T, LANES, PER> raw;
-    raw.load((const T*)a.logits + row * a.ld, t, have);
-    // lane t holds the token's choice t
-    int idx = -1;
-    float dg = 0.0f;
-    if (live && a.dgates && t < a.k) {
-      idx = a.idx[row * a.k + t];
-      dg = a.dgates[row * a.k + t];
-      if (idx < 0 || idx >= a.experts) {
-        idx = -1;
-        dg = 0.0f;
-      }
+    if (idx < 0 || idx >= a.experts) {
+      idx = -1;
+      dg = 0.0f;
     }
     float v[PER];
     raw.floats(t, have, v);
@@ -478,6 +483,7 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
           if (t * PER + i < a.experts) Elem<T>::store(out + t * PER + i, v[i]);
       }
     }
+    fetch(row + step);
   }
 }
 
