@@ -56,7 +56,7 @@ constexpr int kRouteThreads = 512, kRouteBwdThreads = 256;
 // like the norm's: two for each of 256 compute units, one beyond 128 experts,
 // where a partial sum costs more than the second workgroup hides (bf16, with
 // 512 and 256: 65536 x 128 22.1 and 23.8 us, 16384 x 256 15.5 and 14.1).  One,
-// and no second launch, for tokens that it takes in two rounds.
+// and no second launch, for tokens that it takes in two steps.
 constexpr int kRouteMaxParts = 512;
 inline int64_t route_parts(int64_t rows, int64_t experts) {
   const int64_t per = kRouteThreads / route_lanes(experts), most = experts <= 128 ? kRouteMaxParts : kRouteMaxParts / 2;
