@@ -13,7 +13,7 @@ template <typename T, typename W, int NT, int NV, int WG, bool FUSED, bool RAG>
 __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdArgs a) {
   constexpr int RPB = WG / NT;
   constexpr bool EARLY = NV <= 2;
-  __shared__ float red[2][WG / 64];
+  __shared__ float red[4][WG / 64], pair[WG / 64][2];
   const int t = threadIdx.x % NT, sub = row_group<NT>();
   const int cols = a.cols;
   const uint64_t off = FUSED ? drop_offset(a.drop) : 0;
@@ -62,7 +62,7 @@ __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdArgs a) {
 #pragma unroll
       for (int j = 0; j < 8; ++j) s += !RAG || j < n ? v[i][j] : 0.0f;  // 0 in a vector that does not exist
     }
-    const float mean = row_sum<NT>(s, red[0]) / float(cols);
+    float mean = row_sum<NT>(s, red[0]) / float(cols);
     float q = 0.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -74,7 +74,66 @@ __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdArgs a) {
         q = !RAG || j < n ? fmaf(v[i][j], v[i][j], q) : q;
       }
     }
-    const float rstd = 1.0f / sqrtf(row_sum<NT>(q, red[1]) / float(cols) + a.eps);
+    // The mean's roundings are of the size of the row's offset.  Where that is
+    // more than two deviations, the mean of the deviations is taken off as well
+    // and the squares are summed again (without this a constant row of 1000.1
+    // gave y = 0.04 at 4096 columns); elsewhere the error is a few roundings of
+    // the deviation.  A test of each row, not the same for all: two more
+    // operations an element for every row cost 8 to 14 % of a pass out of the
+    // cache (bf16 20000 x 1536, 65536 x 200).  The branch is taken together by
+    // the threads that share its sums' lanes or barriers: with two rows a
+    // workgroup each tests the other row as well.
+    const float square = mean * mean * float(cols);
+    bool offset, any;
+    if constexpr (NT > 64 && RPB == 2) {
+      constexpr int NW = NT / 64;
+      const int wave = threadIdx.x / 64, own = wave / NW * NW, other = own ^ NW;
+      q = lane_sum<64>(q);
+      if (threadIdx.x % 64 == 0) {
+        pair[wave][0] = q;
+        pair[wave][1] = square;
+      }
+      __syncthreads();
+      q = pair[own][0];
+      float w = pair[other][0];
+#pragma unroll
+      for (int i = 1; i < NW; ++i) {
+        q += pair[own + i][0];
+        w += pair[other + i][0];
+      }
+      offset = !(square <= 4.0f * q);
+      any = offset || !(pair[other][1] <= 4.0f * w);
+    } else {
+      static_assert(NT <= 64 || RPB == 1);
+      q = row_sum<NT>(q, red[1]);
+      offset = !(square <= 4.0f * q);
+      any = NT > 64 ? offset : __any(offset);
+    }
+    if (any) {
+      float d = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int n = cols - 8 * (i * NT + t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) d += j < n ? v[i][j] : 0.0f;
+      }
+      d = row_sum<NT>(d, red[2]) / float(cols);
+      d = offset ? d : 0.0f;
+      mean += d;
+      s = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int n = cols - 8 * (i * NT + t);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          v[i][j] -= d;
+          s = j < n ? fmaf(v[i][j], v[i][j], s) : s;
+        }
+      }
+      s = row_sum<NT>(s, red[3]);
+      q = offset ? s : q;
+    }
+    const float rstd = 1.0f / sqrtf(q / float(cols) + a.eps);
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const unsigned col = 8 * (i * NT + t);
@@ -104,7 +163,10 @@ template <typename T, typename W, bool FUSED, bool RAG> struct FwdLaunch {
   // others reduce (16384 x 4096 bf16: 48.8 us; 52.6 to 66.3 with the rows
   // dealt to 512 .. 2048 workgroups that loop).
   template <int NT, int NV> static void fwd(const NormFwdArgs& a, hipStream_t st) {
-    constexpr int WG = NT < 256 ? 256 : NT;
+    // 128 threads a row: two rows a workgroup, but one in the leanest kernels
+    // (20000 x 1536: bf16 26.3 us with one, 27.5 with two; fused bf16 47.1 and
+    // 47.3, ragged 67.4 and 64.1; fp32 53.2 and 50.1).
+    constexpr int WG = NT == 128 && sizeof(T) == 2 && !FUSED && !RAG ? 128 : NT < 256 ? 256 : NT;
     const int64_t need = (a.rows + WG / NT - 1) / (WG / NT);
     hipLaunchKernelGGL((norm_fwd_kernel<T, W, NT, NV, WG, FUSED, RAG>), dim3(unsigned(std::min(need, kOpsMaxGrid))),
                        dim3(WG), 0, st, a);

@@ -11,8 +11,9 @@
 //             dresidual = dh, dx = dropout of dh with the same mask
 //
 // A row is read once and held in registers by 8 to 1024 threads, so the mean
-// comes before the squared deviations are formed (no cancellation) without a
-// second pass over memory.  All sums are fp32; each output is rounded once.
+// (and for a row far off 0 the mean of the deviations from it) comes before the
+// squared deviations are formed, without a second pass over memory.  All sums
+// are fp32; each output is rounded once.
 #pragma once
 
 #include "ops_dev.hpp"
@@ -24,8 +25,8 @@
 namespace muon {
 
 // Sum over the NT threads of a row; `red` holds one word per wave and row.
-// The caller alternates two `red` buffers, so that one barrier per sum is
-// enough.
+// Sums that follow one another take different `red` buffers, so that one
+// barrier per sum is enough.
 template <int NT> __device__ __forceinline__ float row_sum(float v, float* red) {
   if constexpr (NT <= 64) {
     return lane_sum<NT>(v);
