@@ -228,7 +228,9 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
     }
     row_sum2<NT>(s1, s2, red[side]);
     side ^= 1;
-    const float c1 = s1 * inv, c2 = s2 * inv;
+    // mean * rstd overflows only for rows whose elements all equal the mean,
+    // where xh is 0 and s2 with it; lanes without an element have added 0 * inf
+    const float c1 = s1 * inv, c2 = fabsf(r.mean * r.rstd) == INFINITY ? 0.0f : s2 * inv;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const unsigned col = 8 * (i * NT + opaque(t));

@@ -6,7 +6,8 @@ import numpy as np
 import pytest
 import torch
 
-from newton_schulz_05_amd import dropout_add_layer_norm, layer_norm
+from newton_schulz_05_amd import (dropout_add_layer_norm, dropout_add_layer_norm_backward, layer_norm,
+                                  layer_norm_backward)
 from oracle import ops_ref as R
 from tests.ops_helpers import DEV, DTYPES, K, U, draw, h64, half_step, within
 
@@ -92,3 +93,26 @@ def test_tiny_eps():
     within(mean, wm, bm, "mean")
     within(rstd, wr, br, "rstd")
     within(y, wy, by, "y")
+
+
+@pytest.mark.parametrize("rows", [3, 600])
+@pytest.mark.parametrize("cols", [3, 8, 13, 40, 100])
+def test_gradient_of_huge_constant_rows(cols, rows):
+    """Constant rows so large that mean * rstd overflows: their xh is 0, so
+    dx = rstd (g - mean(g)), whatever threads hold no element of the row."""
+    x = torch.full((rows, cols), 2.0 ** 121, device=DEV)
+    x[1] = -(2.0 ** 121)
+    dy = draw((rows, cols), 5).to(DEV)
+    y, mean, rstd = torch.empty_like(x), torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    layer_norm(x, None, None, y, mean=mean, rstd=rstd, eps=EPS)
+    assert torch.equal(mean, x[:, 0].contiguous()) and not y.any()
+    assert torch.isinf(mean * rstd).all()
+    dx, dg, db = torch.empty_like(x), torch.full((cols,), 5.0, device=DEV), torch.empty(cols, device=DEV)
+    layer_norm_backward(dy, x, None, mean, rstd, dx, dgamma=dg, dbeta=db)
+    g, r = h64(dy), h64(rstd)[:, None]
+    want = r * (g - g.mean(1, keepdims=True))
+    within(dx, want, U * np.abs(want) * (1 + 1e-6) + K * U * r * (np.abs(g) + np.abs(g).mean(1, keepdims=True)), "dx")
+    assert not dg.any()
+    dx2, dres = torch.empty_like(x), torch.empty_like(x)
+    dropout_add_layer_norm_backward(dy, x, None, mean, rstd, dx2, dres, p=0.0, seed=1)
+    assert torch.equal(dres, dx) and torch.equal(dx2, dx)
