@@ -389,20 +389,24 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
   fetch(int64_t(blockIdx.x) * TOK + sub);
   // A constant added to every dp of a token changes nothing (sum p = 1), so
   // the counts enter as E c_e - sum c, exact in fp64: near balance the
-  // differences are what matters.
-  int32_t c[PER], own = 0;
+  // differences are what matters.  Counts summed over ranks have a sum beyond
+  // 32 bits; it is formed over the lanes in two parts.
+  int32_t c[PER];
+  uint64_t own = 0;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     const int e = expert_of<LANES, PER>(t, i);
     c[i] = e < a.experts ? a.counts[e] : 0;
-    own += c[i];
+    own += uint32_t(c[i]);
   }
-  const int32_t all = lane_reduce<LANES>(own, [](int32_t x, int32_t y) { return x + y; });
+  auto add = [](uint32_t x, uint32_t y) { return x + y; };
+  const double all = 16777216.0 * lane_reduce<LANES>(uint32_t(own >> 24), add) +
+                     lane_reduce<LANES>(uint32_t(own) & 0xffffffu, add);
   const int ntok = a.n_tokens[0];
   const double up = ntok > 0 ? double(a.coef) * (a.dloss ? double(a.dloss[0]) : 1.0) / (double(a.k) * ntok * ntok) : 0.0;
   float bal[PER];
 #pragma unroll
-  for (int i = 0; i < PER; ++i) bal[i] = float(up * (double(c[i]) * a.experts - double(all)));
+  for (int i = 0; i < PER; ++i) bal[i] = float(up * (double(c[i]) * a.experts - all));
   const int64_t step = int64_t(gridDim.x) * TOK;
   for (int64_t row0 = int64_t(blockIdx.x) * TOK; row0 < a.rows; row0 += step) {
     const int64_t row = row0 + sub;

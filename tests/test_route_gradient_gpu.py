@@ -1,0 +1,71 @@
+"""GPU router gradient where its terms are far smaller than what they are the
+difference of, or where what reaches it is not finite."""
+from __future__ import annotations
+
+import numpy as np
+import pytest
+import torch
+
+from newton_schulz_05_amd import route, route_backward
+from oracle import ops_ref as R
+from tests.ops_helpers import DEV, DTYPES, K, U, draw, h64, half_step, within
+
+pytestmark = pytest.mark.gpu
+
+
+def _forward(x, k, renorm, valid=None):
+    rows, experts = x.shape
+    idx, gates = torch.empty(rows, k, dtype=torch.int32, device=DEV), torch.empty(rows, k, device=DEV)
+    counts, n = torch.empty(experts, dtype=torch.int32, device=DEV), torch.empty(1, dtype=torch.int32, device=DEV)
+    route(x, idx, gates, counts, n, torch.empty(1, device=DEV), coef=0.1, renorm=renorm, valid=valid)
+    return idx, counts, n
+
+
+def _gradient(x, idx, dgates, counts, n, coef, renorm):
+    """(dlogits, bound) in fp64 from differences to the token's most probable
+    expert, whose p is 1 less the others': dlogit = p (dp - sum p dp) with
+    dp - dp_top in the place of dp, and likewise for renormalised gates.  The
+    bound counts roundings of what those differences are taken of; the
+    exponential's argument has one of the size of the distance."""
+    rows, e = x.shape
+    r, k = np.arange(rows), idx.shape[1]
+    top = x.argmax(1)
+    z = np.exp(x - x[r, top][:, None])
+    p = z / z.sum(1, keepdims=True)
+    rel = 2 * (K + np.ptp(x, axis=1)[:, None]) * U
+    dg, at = np.asarray(dgates, float), np.asarray(idx)
+    mag = np.abs(dg)
+    if renorm:
+        q = np.take_along_axis(p, at, 1)
+        s = q.sum(1, keepdims=True)
+        best = q.argmax(1)
+        dg = dg - dg[r, best][:, None]
+        mag = np.abs(dg)
+        mid, mmid = ((v * q / s).sum(1, keepdims=True) for v in (dg, mag))
+        dg, mag = (dg - mid) / s, (mag + mmid) / s
+    c = np.asarray(counts, float)
+    bal = coef * (e * c - c.sum()) / (k * n ** 2)  # less a constant, which sum p = 1 takes out
+    dp, m = np.tile(bal, (rows, 1)), np.tile(np.abs(bal), (rows, 1))
+    for j in range(k):
+        dp[r, at[:, j]] += dg[:, j]
+        m[r, at[:, j]] += mag[:, j]
+    dp, m = dp - dp[r, top][:, None], m + m[r, top][:, None]
+    m[r, top] = 0
+    want = p * (dp - (p * dp).sum(1, keepdims=True))
+    return want, rel * p * (m + (p * m).sum(1, keepdims=True))
+
+
+@pytest.mark.parametrize("experts,k", [(8, 4), (24, 4), (64, 4), (512, 4), (1000, 16)])
+def test_counts_of_many_ranks(experts, k):
+    """Counts summed over ranks: each fits its type, their sum k n need not.
+    Near balance their differences are what matters."""
+    n = (1 << 31) - 5
+    counts = k * n // experts + np.random.default_rng(experts).integers(-1000, 1000, experts)
+    assert counts.max() < 1 << 31 < counts.sum()
+    x = draw((50, experts), 9).to(DEV)
+    idx, _, _ = _forward(x, k, False)
+    dx = torch.empty_like(x)
+    route_backward(x, idx, torch.tensor(counts, dtype=torch.int32, device=DEV),
+                   torch.tensor([n], dtype=torch.int32, device=DEV), dx, coef=float(n), renorm=False)
+    want, bound = _gradient(h64(x), idx.cpu().numpy(), np.zeros((50, k)), counts, n, float(np.float32(n)), False)
+    within(dx, want, bound + U * (np.abs(want) + bound), "dlogits")
