@@ -465,6 +465,10 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
     dot = lane_sum<LANES>(dot);
 #pragma unroll
     for (int i = 0; i < PER; ++i) v[i] *= dp[i] - dot;
+    if (__ballot(!some)) {  // 0 by selection: what reaches a token may not be finite
+#pragma unroll
+      for (int i = 0; i < PER; ++i) v[i] = some ? v[i] : 0.0f;
+    }
     if (in) {
       T* out = (T*)a.dlogits + row * a.ld_d;
       if constexpr (PER >= 8) {

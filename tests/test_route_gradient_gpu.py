@@ -69,3 +69,27 @@ def test_counts_of_many_ranks(experts, k):
                    torch.tensor([n], dtype=torch.int32, device=DEV), dx, coef=float(n), renorm=False)
     want, bound = _gradient(h64(x), idx.cpu().numpy(), np.zeros((50, k)), counts, n, float(np.float32(n)), False)
     within(dx, want, bound + U * (np.abs(want) + bound), "dlogits")
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("experts,k", [(8, 2), (24, 2), (64, 4), (300, 8)])
+@pytest.mark.parametrize("dloss", [float("inf"), float("-inf"), float("nan")])
+def test_overflowed_loss_scale_leaves_padding_at_zero(experts, k, dt, dloss):
+    """A gradient of the loss that is not finite reaches the tokens with a
+    choice only."""
+    rows = 150
+    x = draw((rows, experts), 3, 1.0, 0.0, DTYPES[dt]).to(DEV)
+    x[20:30] = float("-inf")                     # every expert shut off
+    valid = torch.ones(rows, dtype=torch.uint8, device=DEV)
+    valid[40:55] = 0
+    valid[149] = 0
+    idx, counts, n = _forward(x, k, True, valid)
+    x[40:55] = float("nan")
+    dgates = draw((rows, k), 7).to(DEV)
+    for dg in (dgates, None):
+        dx = torch.full_like(x, 5.0)
+        route_backward(x, idx, counts, n, dx, dgates=dg, dloss=torch.tensor([dloss], device=DEV), coef=0.1, valid=valid)
+        none = torch.zeros(rows, dtype=torch.bool, device=DEV)
+        none[20:30] = none[40:55] = none[149] = True
+        assert (dx[none] == 0).all()
+        assert not torch.isfinite(dx[~none]).any()
