@@ -367,6 +367,12 @@ __device__ __forceinline__ void add_choices(float (&dp)[PER], float* mem, int t,
   }
 }
 
+// The value of one of the group's lanes that have one (the largest word, so
+// that equals agree on it); the others come with 0.
+template <int LANES> __device__ __forceinline__ float reference(float v) {
+  return __uint_as_float(lane_max<LANES>(__float_as_uint(v)));
+}
+
 template <typename T, int LANES, int PER>
 __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArgs a) {
   constexpr int TOK = kRouteBwdThreads / LANES;
@@ -434,8 +440,12 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
     if (a.dgates && a.renorm) {
       const float q = idx >= 0 ? exp_neg(Elem<T>::load((const T*)a.logits + row * a.ld + idx) - mx) * inv : 0.0f;
       const float sum = lane_sum<LANES>(q);
-      const float share = sum > 0.0f ? q / sum : 0.0f;  // exactly 1 for a lone choice, which has no gradient
-      const float mid = lane_sum<LANES>(dg * share);
+      const float share = sum > 0.0f ? q / sum : 0.0f;
+      // dg - sum share dg by the difference to the gate of the largest share (a
+      // lone choice has exactly 0), see below
+      const uint32_t most = lane_max<LANES>(__float_as_uint(q));
+      dg -= reference<LANES>(idx >= 0 && __float_as_uint(q) == most ? dg : 0.0f);
+      const float mid = lane_sum<LANES>(idx >= 0 ? dg * share : 0.0f);
       dg = sum > 0.0f ? (dg - mid) / sum : 0.0f;
     }
     float dp[PER];
@@ -456,15 +466,24 @@ __global__ __launch_bounds__(kRouteBwdThreads) void route_bwd_kernel(RouteBwdArg
         wave_lds_order();
       }
     }
+    // dlogit = p (dp - sum p dp).  Where one p is near 1 the sum is near its dp
+    // and their difference is all roundings, so dp is counted from the most
+    // probable expert's (whose exponential is exactly 1): that adds nothing to
+    // the sum, and the gradients are sums of the others' small terms.
+    float ref = 0.0f;
+#pragma unroll
+    for (int i = 0; i < PER; ++i) ref = v[i] == 1.0f ? dp[i] : ref;
+    ref = reference<LANES>(ref);
     float dot = 0.0f;
 #pragma unroll
     for (int i = 0; i < PER; ++i) {
-      v[i] *= inv;
+      dp[i] -= ref;
       dot = fmaf(v[i], dp[i], dot);
     }
-    dot = lane_sum<LANES>(dot);
+    dot = lane_sum<LANES>(dot) * inv;
+    const float shift = dot * inv;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) v[i] *= dp[i] - dot;
+    for (int i = 0; i < PER; ++i) v[i] *= fmaf(dp[i], inv, -shift);
     if (__ballot(!some)) {  // 0 by selection: what reaches a token may not be finite
 #pragma unroll
       for (int i = 0; i < PER; ++i) v[i] = some ? v[i] : 0.0f;

@@ -93,3 +93,30 @@ def test_overflowed_loss_scale_leaves_padding_at_zero(experts, k, dt, dloss):
         none[20:30] = none[40:55] = none[149] = True
         assert (dx[none] == 0).all()
         assert not torch.isfinite(dx[~none]).any()
+
+
+
+
+@pytest.mark.parametrize("coef", [0.0, 0.3])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("experts,k", [(2, 1), (2, 2), (8, 1), (8, 2), (16, 2), (24, 3), (64, 6), (100, 1), (128, 8),
+                                       (256, 8), (512, 4), (1000, 2)])
+def test_confident_tokens(experts, k, dt, renorm, coef):
+    """One expert far above the rest: the gradients are those of the rest's
+    small probabilities, to a relative error."""
+    gaps = np.array([8.0, 12.0, 13.0, 14.0, 15.0, 16.0, 17.0, 18.0, 20.0, 24.0, 40.0, 60.0])
+    rows = len(gaps)
+    x = draw((rows, experts), experts + k, 0.3)
+    top = torch.from_numpy(np.random.default_rng(k).integers(0, experts, rows))
+    x[torch.arange(rows), top] = torch.from_numpy(gaps).float() + experts ** 0.1
+    x = x.to(DTYPES[dt]).to(DEV)
+    idx, counts, n = _forward(x, k, renorm)
+    dgates = draw((rows, k), 7).to(DEV)
+    dx = torch.full_like(x, 5.0)
+    route_backward(x, idx, counts, n, dx, dgates=dgates, coef=coef, renorm=renorm)
+    want, bound = _gradient(h64(x), idx.cpu().numpy(), h64(dgates), counts.cpu().numpy(), rows, coef, renorm)
+    within(dx, want, bound + half_step(x.dtype) * (np.abs(want) * (1 + 1e-6) + bound), "dlogits")
+    # the oracle's plain formula in fp64 agrees as far as its own cancellation allows
+    plain = R.route_backward(h64(x), idx.cpu().numpy(), counts.cpu().numpy(), rows, k, coef, renorm, h64(dgates), 1.0)
+    assert (np.abs(plain - want) <= 1e-12 * (np.abs(h64(dgates)).max() + coef * experts) * 4 * experts).all()
