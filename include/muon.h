@@ -371,7 +371,9 @@ muon_status muon_dropout_add_layer_norm_bwd(const void* dy, int64_t ld_dy, const
  *               may hold anything).  Such a token, and one whose experts are
  *               all shut off, has no choice and enters no sum.
  *   renorm    : 1: the gates of a token are divided by their sum; 0: they are
- *               p itself.
+ *               p itself.  A p whose ratio to the token's largest is below
+ *               2^-126 (a logit about 87.3 lower) may be 0; the choices and
+ *               counts go by the logits.
  *   indices   : [tokens, k] int32, by falling logit; -1 where no expert is
  *               left (gate 0).
  *   gates     : [tokens, k] floats.

@@ -92,7 +92,8 @@ __device__ __forceinline__ uint32_t take_largest(uint32_t (&key)[PER], int t, in
 
 // exp(x) for x <= 0 (NaN stays NaN) from the hardware's 2^t: x log2(e) is split
 // into its rounded product t and the rest r, and 2^(t + r) = 2^t (1 + r ln 2),
-// which keeps the relative error at a few 2^-24 however large |x| is.
+// which keeps the relative error at a few 2^-24 down to 2^-126 (x about -87.3),
+// however large |x| log2(e) has grown; smaller results are 0.
 __device__ __forceinline__ float exp_neg(float x) {
   x = x < -150.0f ? -150.0f : x;  // 2^-216: 0 in fp32
   const float t = x * 1.44269502f;
