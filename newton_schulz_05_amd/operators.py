@@ -158,7 +158,13 @@ def _param_dtype(x: torch.Tensor, *params) -> torch.dtype:
 
 def _u64(v: int, what: str) -> int:
     if type(v) is not int:
-        v = int(v)
+        try:
+            whole = int(v) if not isinstance(v, str) else None
+        except (TypeError, ValueError, OverflowError):
+            whole = None
+        if whole is None or whole != v:
+            raise MuonError(1, f"{what} must be an unsigned 64-bit integer")
+        v = whole
     if not 0 <= v < 1 << 64:
         raise MuonError(1, f"{what} must be an unsigned 64-bit integer")
     return v
