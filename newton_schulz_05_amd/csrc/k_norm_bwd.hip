@@ -160,14 +160,12 @@ enum NormSums {
 //
 // Bound by memory: x and dy are read and dx written once.  For many rows one
 // workgroup of 1024 threads on each of 256 units, one 16-byte vector a thread
-// (16 sums to keep) measured best: at 16384 x 8192 bf16 148.7 us against
-// 159.8 with two workgroups of 512 threads and two vectors, and 163.1 without
-// the next row's loads in flight (AHEAD) over the reduction; at 16384 x 4096
-// 77.4 against 105.6.  The fused pass has a third stream in flight and gains
-// nothing from AHEAD (125.1 without, 127.6 with); with more vectors AHEAD spills
-// or gains nothing (2000 x 9000 bf16, two vectors: 39.8 without, 44.9 with).
-// Rows above 20480 columns have no registers for the sums: see
-// norm_cols_kernel.
+// (16 sums to keep), with the next row's loads in flight over the reduction
+// (AHEAD), measured best: 16384 x 8192 bf16 149.6 us, 157.0 without AHEAD; 16384 x
+// 4096 79.1 and 81.0.  The fused pass has a third stream in flight and gains
+// nothing from it (16384 x 4096 129.1 without, 127.7 with), nor do two vectors a
+// thread (4000 x 16384 88.9 without, 89.7 with).  Rows above 20480 columns have no
+// registers for the sums: see norm_cols_kernel.
 template <typename T, typename W, int NT, int NV, int WG, bool FUSED, bool RAG, NormSums WHERE>
 __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
   constexpr int RPB = WG / NT, JOIN = NT < 64 ? WG / 64 : RPB;
@@ -288,7 +286,7 @@ __global__ __launch_bounds__(WG) void norm_bwd_kernel(NormBwdArgs a) {
 // The sums of rows wider than 20480 columns, in a pass of its own over x and
 // dy: blockIdx.x takes 2048 columns, a vector a thread, and blockIdx.y every
 // gridDim.y-th row.  With the sums in norm_bwd_kernel four vectors a thread
-// spilled (2048 x 32768 bf16: 288 us).
+// spilled (2048 x 32768 bf16: 288 us; 147 so).
 template <typename T, bool RAG>
 __global__ __launch_bounds__(256) void norm_cols_kernel(NormBwdArgs a) {
   const unsigned col = 8 * (blockIdx.x * 256 + threadIdx.x);

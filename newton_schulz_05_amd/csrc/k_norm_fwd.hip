@@ -5,8 +5,8 @@ namespace muon {
 
 namespace {
 
-// Bound by memory: x is read and y written once (16384 x 4096 bf16: 5 TB/s,
-// the rate of a large copy).  gamma and beta come from the cache, their loads
+// Bound by memory: x is read and y written once (16384 x 4096 bf16: 51.5
+// us, 5.2 TB/s, the rate of a large copy).  gamma and beta come from the cache, their loads
 // behind those of x; with three and more vectors a thread they are read after
 // the reductions, over which they would take registers.
 template <typename T, typename W, int NT, int NV, int WG, bool FUSED, bool RAG>
@@ -160,12 +160,13 @@ __global__ __launch_bounds__(WG) void norm_fwd_kernel(NormFwdArgs a) {
 
 template <typename T, typename W, bool FUSED, bool RAG> struct FwdLaunch {
   // One group of rows a workgroup: new workgroups keep loads in flight while
-  // others reduce (16384 x 4096 bf16: 48.8 us; 52.6 to 66.3 with the rows
-  // dealt to 512 .. 2048 workgroups that loop).
+  // others reduce (16384 x 4096 bf16: 51.5 us; 59.2 with the rows dealt to 2048
+  // workgroups that loop, 66.0 to 512).
   template <int NT, int NV> static void fwd(const NormFwdArgs& a, hipStream_t st) {
     // 128 threads a row: two rows a workgroup, but one in the leanest kernels
-    // (20000 x 1536: bf16 26.3 us with one, 27.5 with two; fused bf16 47.1 and
-    // 47.3, ragged 67.4 and 64.1; fp32 53.2 and 50.1).
+    // (bf16 20000 x 1536 26.1 us with one, 27.4 with two, 60000 rows 66.7 and
+    // 71.4; 1537 columns 38.9 and 38.0, fused 67.3 and 64.5; fp32 1536 columns
+    // 53.3 and 49.9).
     constexpr int WG = NT == 128 && sizeof(T) == 2 && !FUSED && !RAG ? 128 : NT < 256 ? 256 : NT;
     const int64_t need = (a.rows + WG / NT - 1) / (WG / NT);
     hipLaunchKernelGGL((norm_fwd_kernel<T, W, NT, NV, WG, FUSED, RAG>), dim3(unsigned(std::min(need, kOpsMaxGrid))),
@@ -173,10 +174,10 @@ template <typename T, typename W, bool FUSED, bool RAG> struct FwdLaunch {
   }
   static hipError_t fwd(const NormFwdArgs& a, hipStream_t st) {
     // The narrowest fit that keeps several workgroups on a compute unit: three
-    // to five vectors a thread rather than 512 or 1024 threads a row (8192
-    // columns bf16: 51.6 us with 256 threads, 66.6 with 512; 20000 columns: 61
-    // with 512, 105 with 1024; 2048 columns: 48.6 with 128, 59.6 with 256; 200
-    // columns, 65536 rows: 17.9 with 32, 29.9 with 64).
+    // to five vectors a thread rather than 512 or 1024 threads a row (bf16 16384
+    // x 8192: 98.5 us with 256 threads, 107.0 with 512; 3300 x 20000: 60.1 with
+    // 512, 66.9 with 1024; 16384 x 2048: 26.9 with 128, 28.6 with 256; 65536 x
+    // 200: 13.0 with 32, 22.0 with 64).
     const int vecs = (a.cols + 7) / 8;
     if (vecs <= 8) fwd<8, 1>(a, st);
     else if (vecs <= 16) fwd<16, 1>(a, st);

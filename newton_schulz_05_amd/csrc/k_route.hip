@@ -55,8 +55,8 @@ template <int N> __device__ __forceinline__ uint32_t lane_min(uint32_t v) {
 }
 
 // The i-th expert of lane t: runs of 8 dealt to the lanes in turn, so that a
-// group's 16-byte accesses are adjacent (backward of 32768 x 256 fp32 20.1 us,
-// 23.7 with PER consecutive experts a lane); fewer than 8 a lane are
+// group's 16-byte accesses are adjacent (backward of 32768 x 256 fp32 20.9 us,
+// 24.8 with PER consecutive experts a lane); fewer than 8 a lane are
 // consecutive.  Experts rise with i.
 template <int LANES, int PER> __device__ __forceinline__ int expert_of(int t, int i) {
   return PER >= 8 ? ((i >> 3) * LANES + t) * 8 + (i & 7) : t * PER + i;
@@ -92,8 +92,8 @@ __device__ __forceinline__ uint32_t take_largest(uint32_t (&key)[PER], int t, in
 
 // exp(x) for x <= 0 (NaN stays NaN) from the hardware's 2^t: x log2(e) is split
 // into its rounded product t and the rest r, and 2^(t + r) = 2^t (1 + r ln 2),
-// which keeps the relative error at a few 2^-24 down to 2^-126 (x about -87.3),
-// however large |x| log2(e) has grown; smaller results are 0.
+// which keeps the relative error at a few 2^-24 for results down to 2^-126 (x of
+// about -87.3); smaller ones are 0.
 __device__ __forceinline__ float exp_neg(float x) {
   x = x < -150.0f ? -150.0f : x;  // 2^-216: 0 in fp32
   const float t = x * 1.44269502f;

@@ -54,8 +54,8 @@ template <int NT> __device__ __forceinline__ int row_group() {
 // Vectors of a row at col, n = cols - col elements of it existing (0 in dead
 // rows).  Without RAG cols is a multiple of 8, so that a vector exists whole or
 // not at all; with it see load_row8.  (One code for both costs whole rows their
-// tests of n and the shift: 20000 x 1536 bf16 forward 24.7 us without RAG, 34.1
-// with; 16384 x 8192 backward 150.6 and 164.)
+// tests of n and the shift: 20000 x 1536 bf16 forward 25.6 us without RAG, 37.9
+// with; 16384 x 8192 backward 150.9 and 161.6.)
 template <bool RAG, typename T>
 __device__ __forceinline__ Raw8<T> load_vec(const T* row, unsigned col, int n, int cols) {
   if constexpr (RAG) return load_row8(row, col, n, cols);

@@ -20,7 +20,8 @@ constexpr int64_t kOpsMaxGrid = 1 << 20;  // workgroups of a launch; a kernel lo
 // which a second launch joins.
 //   up to 256 rows: no partial sums; one launch, whose last workgroups sum 64
 //     columns each over all rows (they read x and dy again, out of the cache:
-//     64 x 1536 bf16 fused 12.0 us a call against 16.2 with two launches);
+//     64 x 1536 bf16 fused 2.9 us against 7.3 with two launches, 256 x 4096 5.7
+//     against 10.2);
 //   many rows: one partial sum a workgroup, 1024 threads on each of 256 compute
 //     units (a fixed number, so that results do not depend on the device's),
 //     or, for narrow rows, 256 threads as long as 256 such workgroups take all
@@ -29,10 +30,11 @@ constexpr int64_t kOpsMaxGrid = 1 << 20;  // workgroups of a launch; a kernel lo
 //     sums of each strip of 2048 columns.
 // A thread holds one vector of 8 elements of its row up to 8192 columns; then
 // 512 threads three (up to 12288), 1024 two (16384), 512 five (20480), 1024
-// three or four: what measured best in each range (bf16 9000 columns: 95 us
-// with 512 x 3, 98 with 1024 x 2, and fused 144 and 153; 16384 columns: 85
-// with 1024 x 2, 89 with 512 x 4; 20000 columns: 96 with 512 x 5, 130 with the
-// sums apart).
+// three or four.  512 x 3 against 1024 x 2 gains where registers are short (fused
+// fp32 7000 x 8200: 228 us against 264, 5000 x 12000 245 against 262) and is
+// within 4 % elsewhere; 4000 x 16384 bf16 takes 89.0 us with 1024 x 2, 93.5 with
+// 512 x 4; 3300 x 20000 bf16 98 us with 512 x 5, 133 with the sums apart (fused
+// 194 and 203, but fused fp32, where 512 x 5 spills most, 423 and 389).
 struct NormBwdSplit {
   int row_threads, threads, parts;
 };
@@ -55,7 +57,7 @@ constexpr int kRouteThreads = 512, kRouteBwdThreads = 256;
 // Workgroups of the router's forward pass (one partial sum each), a fixed number
 // like the norm's: two for each of 256 compute units, one beyond 128 experts,
 // where a partial sum costs more than the second workgroup hides (bf16, with
-// 512 and 256: 65536 x 128 22.1 and 23.8 us, 16384 x 256 15.5 and 14.1).  One,
+// 512 and 256: 65536 x 128 23.2 and 24.5 us, 16384 x 256 16.2 and 14.5).  One,
 // and no second launch, for tokens that it takes in two steps.
 constexpr int kRouteMaxParts = 512;
 inline int64_t route_parts(int64_t rows, int64_t experts) {
