@@ -401,6 +401,164 @@ muon_status muon_route_bwd(const void* logits, int64_t ld, muon_dtype dt, int64_
                            const int32_t* counts, const int32_t* n_tokens, const float* dgates, const float* dloss,
                            void* dlogits, int64_t ld_d, void* stream);
 
+/* ---- The two ends of a training step ---------------------------------------
+ * What stands between a projection and attention (the norm of every query and
+ * key head with the position rotation; its gains take muon_adamw_step), and
+ * what starts the backward pass: the log-probabilities of a batch's tokens and
+ * the losses on them.  The conventions are those of the training operators
+ * above.  Positions, targets and offsets are 64-bit words on the device
+ * (8-byte aligned); one outside its range is no fault, see there. */
+
+/* Strides, in elements, of a tensor [batch, tokens, heads, dim] whose last
+ * dimension is contiguous.  Any order of the three dimensions is allowed as
+ * long as they nest: each (of more than one entry) is at least as long as all
+ * that lies within it.  Slices of a projection's output and tensors with the
+ * heads before the tokens are such tensors. */
+typedef struct {
+  int64_t batch, token, head;
+} muon_head_strides;
+
+/* Norm and rotation of every head of q and k, in one launch:
+ *   r = 1 / sqrt(sum x^2 / dim + eps),  y = x r gamma,
+ * and in the first `rot` elements of y, with h = rot / 2, the pairs
+ * (y_i, y_i+h) (interleaved: (y_2i, y_2i+1)) turned by the token's angles,
+ *   (a, b) -> (a cos - b sin, b cos + a sin),
+ * in fp32, rounded once.  The other elements keep y.
+ *   q, k, q_out, k_out : [batch, tokens, heads, dim] of dt; k and k_out null
+ *                      for queries alone (heads_k is then 0).  q_out may be q
+ *                      itself and k_out k itself.
+ *   dim              : 1 .. 512; batch * tokens * heads < 2^31.
+ *   gamma_q, gamma_k : dim elements of param_dt, or null for 1.
+ *   eps              : finite, > 0.
+ *   cos, sin         : [table_rows, rot / 2] floats; null if rot = 0.
+ *   rot              : even, 0 .. dim.  interleaved: 0 or 1.
+ *   positions        : null: token t of every sequence takes row t of cos and
+ *                      sin; else token t of sequence b takes row
+ *                      positions[b * positions_batch + t] (positions_batch = 0
+ *                      for positions common to all sequences, else >= tokens).
+ *                      A token whose row is outside 0 .. table_rows - 1 is not
+ *                      turned. */
+muon_status muon_qk_norm_rope_fwd(const void* q, const muon_head_strides* s_q, const void* k,
+                                  const muon_head_strides* s_k, muon_dtype dt, int64_t batch, int64_t tokens,
+                                  int32_t heads_q, int32_t heads_k, int32_t dim, const void* gamma_q,
+                                  const void* gamma_k, muon_dtype param_dt, float eps, const float* cos,
+                                  const float* sin, int64_t table_rows, int32_t rot, int32_t interleaved,
+                                  const int64_t* positions, int64_t positions_batch, void* q_out,
+                                  const muon_head_strides* s_qo, void* k_out, const muon_head_strides* s_ko,
+                                  void* stream);
+
+/* Bytes of workspace (16-byte aligned) of the backward pass, for rows_q =
+ * batch * tokens * heads_q and rows_k likewise; 0 means that a null workspace
+ * will do.  Not needed when neither dgamma_q nor dgamma_k is asked for. */
+muon_status muon_qk_norm_rope_workspace_bytes(int64_t rows_q, int64_t rows_k, int32_t dim, size_t* bytes);
+
+/* Its gradients: with g = dy turned back by the token's angles,
+ *   dgamma = sum over tokens and heads of g x r,
+ *   dx = r (g gamma - x r mean(g gamma x r)).
+ *   dq_out, dk_out     : the gradients that reach q_out and k_out.
+ *   q, k               : the forward pass's inputs (r is formed again).
+ *   dq, dk             : [batch, tokens, heads, dim] of dt; dq may be dq_out
+ *                        itself and dk dk_out itself.
+ *   dgamma_q, dgamma_k : dim elements of param_dt, overwritten; null if not
+ *                        wanted. */
+muon_status muon_qk_norm_rope_bwd(const void* dq_out, const muon_head_strides* s_dqo, const void* dk_out,
+                                  const muon_head_strides* s_dko, const void* q, const muon_head_strides* s_q,
+                                  const void* k, const muon_head_strides* s_k, muon_dtype dt, int64_t batch,
+                                  int64_t tokens, int32_t heads_q, int32_t heads_k, int32_t dim,
+                                  const void* gamma_q, const void* gamma_k, muon_dtype param_dt, float eps,
+                                  const float* cos, const float* sin, int64_t table_rows, int32_t rot,
+                                  int32_t interleaved, const int64_t* positions, int64_t positions_batch, void* dq,
+                                  const muon_head_strides* s_dq, void* dk, const muon_head_strides* s_dk,
+                                  void* dgamma_q, void* dgamma_k, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* Log-probability of every token's target under the softmax of its logits:
+ * with z = scale logits, lse = log(sum over the vocabulary of exp z) and
+ *   logp = z_target - lse,
+ * accurate relative to itself where the target is nearly certain too (the sum
+ * leaves the target out and -log(1 + rest) is formed).
+ *   logits  : [tokens, vocab] of dt; vocab in 1 .. 2^24.  -inf is a
+ *             word that cannot be; a row that holds NaN or +inf has NaN.
+ *   targets : tokens words.  One outside 0 .. vocab - 1 (a prompt or padding
+ *             token) is none: logp = lse = 0, whatever the row holds.  So is
+ *             every target of a row that is -inf throughout (lse = -inf).
+ *   scale   : finite, > 0: the inverse of a temperature.
+ *   logp, lse : tokens floats each.
+ *   workspace : muon_token_logp_workspace_bytes(), 16-byte aligned. */
+muon_status muon_token_logp_workspace_bytes(int64_t tokens, int64_t vocab, size_t* bytes);
+muon_status muon_token_logp_fwd(const void* logits, int64_t ld, muon_dtype dt, int64_t tokens, int64_t vocab,
+                                const int64_t* targets, float scale, float* logp, float* lse, void* workspace,
+                                size_t workspace_bytes, void* stream);
+
+/* Its gradient: dlogit_j = scale dlogp ([j = target] - exp(z_j - lse)), the
+ * target's 1 - exp(logp) formed from logp; 0 in the rows of tokens without a
+ * target and those whose dlogp is 0 (they are not read).
+ *   logp, lse : as the forward pass wrote them.
+ *   dlogp     : tokens floats, as the losses below write them.
+ *   dlogits   : [tokens, vocab] of dt; may be logits itself. */
+muon_status muon_token_logp_bwd(const void* logits, int64_t ld, muon_dtype dt, int64_t tokens, int64_t vocab,
+                                const int64_t* targets, float scale, const float* logp, const float* lse,
+                                const float* dlogp, void* dlogits, int64_t ld_d, void* stream);
+
+/* Clipped policy loss with a KL term, and its gradient by logp, in one pass
+ * over the tokens.  With d = logp - old_logp, A = advantage and
+ * u = ref_logp - logp, a token has
+ *   pg = -min(A e^d, A clip(e^d, 1 - clip_low, 1 + clip_high)),
+ *   kl = e^u - u - 1,
+ * and loss = sum of weight (pg + beta kl).  dlogp = dloss * weight *
+ * (-A e^d + beta (1 - e^u)), without the first term where the token is clipped:
+ * A > 0 and d > log(1 + clip_high), or A < 0 and d < log(1 - clip_low).  A
+ * token's terms and all sums are formed in fp64.
+ *   logp       : tokens floats (muon_token_logp_fwd's).
+ *   old_logp   : of the policy that sampled the tokens; null: logp itself.
+ *   ref_logp   : of the reference policy; null: no KL term.
+ *   advantages : tokens floats.
+ *   weight     : tokens floats, for a mean 1 / their number; null: 1 each.  A
+ *                token of weight 0 (prompt, padding) enters nothing, whatever
+ *                its other values.
+ *   clip_low in [0, 1], clip_high >= 0, beta: finite.
+ *   dloss      : one float on the device, or null for 1.
+ *   loss       : one float.  terms: null, or three: the sums of weight pg, of
+ *                weight kl, and of the weights of clipped tokens.
+ *   dlogp      : tokens floats, or null if not wanted.
+ *   tokens     : < 2^40.
+ *   workspace  : muon_policy_loss_workspace_bytes(), 16-byte aligned. */
+muon_status muon_policy_loss_workspace_bytes(int64_t tokens, size_t* bytes);
+muon_status muon_policy_loss(const float* logp, const float* old_logp, const float* ref_logp,
+                             const float* advantages, const float* weight, int64_t tokens, float clip_low,
+                             float clip_high, float beta, const float* dloss, float* loss, float* terms,
+                             float* dlogp, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Preference loss on pairs of answers, and its gradient by logp.  Sequence s of
+ * 0 .. 2 pairs - 1 holds the tokens offsets[s] .. offsets[s + 1] - 1; pair i is
+ * sequence i, the preferred answer, and sequence pairs + i.
+ *   reward_s = beta * (sum over the sequence of logp - ref_logp), with
+ *              average = 1 divided by its number of tokens (0 without one),
+ *   m = reward_i - reward_(pairs + i) - margin,
+ *   loss = sum over the pairs of weight (-(1 - smoothing) log sigma(m)
+ *          - smoothing log sigma(-m)),  sigma(m) = 1 / (1 + e^-m).
+ * Sums and the loss's terms are formed in fp64.
+ *   logp     : tokens floats;  ref_logp: as many, or null for 0.
+ *   valid    : null, or one byte a token, 0 for a token that enters nothing
+ *              (nor its sequence's number of tokens), whatever its logp.
+ *   offsets  : 2 pairs + 1 words, rising; each is taken as at least 0 and at
+ *              most tokens, and a sequence that ends before its start as empty.
+ *   pairs    : 0 .. 2^20;  tokens: < 2^40.
+ *   weight   : pairs floats, or null for 1 / pairs.  A pair of weight 0 enters
+ *              nothing.
+ *   beta, margin : finite;  smoothing in [0, 1];  average 0 or 1.
+ *   dloss    : one float on the device, or null for 1.
+ *   loss     : one float.  rewards: 2 pairs floats, or null.
+ *   dlogp    : tokens floats, or null if not wanted; the tokens before the
+ *              first sequence and behind the last are left as they were.
+ *   workspace : muon_preference_loss_workspace_bytes(), 16-byte aligned. */
+muon_status muon_preference_loss_workspace_bytes(int64_t tokens, int64_t pairs, size_t* bytes);
+muon_status muon_preference_loss(const float* logp, const float* ref_logp, const uint8_t* valid, int64_t tokens,
+                                 const int64_t* offsets, int64_t pairs, const float* weight, float beta,
+                                 float margin, float smoothing, int32_t average, const float* dloss, float* loss,
+                                 float* rewards, float* dlogp, void* workspace, size_t workspace_bytes,
+                                 void* stream);
+
 /* ---- Diagnostics of the skinny path ---------------------------------------
  * The skinny path (bf16, min(rows, cols) <= 32) runs one persistent launch
  * per chunk whose workgroups exchange partial sums, so they must all be

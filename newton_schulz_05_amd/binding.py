@@ -39,6 +39,10 @@ EXPORTS = ["muon_plan_create", "muon_plan_destroy", "muon_plan_workspace_bytes",
            "muon_layer_norm_fwd", "muon_layer_norm_workspace_bytes", "muon_layer_norm_bwd", "muon_dropout",
            "muon_dropout_add_layer_norm_fwd", "muon_dropout_add_layer_norm_bwd",
            "muon_route_workspace_bytes", "muon_route_fwd", "muon_route_bwd",
+           "muon_qk_norm_rope_fwd", "muon_qk_norm_rope_workspace_bytes", "muon_qk_norm_rope_bwd",
+           "muon_token_logp_workspace_bytes", "muon_token_logp_fwd", "muon_token_logp_bwd",
+           "muon_policy_loss_workspace_bytes", "muon_policy_loss",
+           "muon_preference_loss_workspace_bytes", "muon_preference_loss",
            "muon_kernel_timing", "muon_kernel_timing_read",
            "muon_status_str", "muon_last_error_detail", "muon_version"]
 
@@ -57,6 +61,10 @@ class MuonError(RuntimeError):
 
 class MuonShape(ctypes.Structure):
     _fields_ = [("batch", ctypes.c_int64), ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class MuonHeadStrides(ctypes.Structure):
+    _fields_ = [("batch", ctypes.c_int64), ("token", ctypes.c_int64), ("head", ctypes.c_int64)]
 
 
 _lib = None
@@ -121,6 +129,30 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.muon_route_fwd.restype = i32
     lib.muon_route_bwd.argtypes = [vp, i64, i32, i64, i32, i32, vp, i32, f32, vp, vp, vp, vp, vp, vp, i64, vp]
     lib.muon_route_bwd.restype = i32
+    # addresses of muon_head_strides go as plain pointers
+    angles = [f32, vp, vp, i64, i32, i32, vp, i64]  # eps, cos, sin, table rows, rot, interleaved, positions and their stride
+    lib.muon_qk_norm_rope_fwd.argtypes = [vp, vp, vp, vp, i32, i64, i64, i32, i32, i32, vp, vp, i32, *angles, vp, vp, vp, vp,
+                                          vp]
+    lib.muon_qk_norm_rope_fwd.restype = i32
+    lib.muon_qk_norm_rope_workspace_bytes.argtypes = [i64, i64, i32, P(sz)]
+    lib.muon_qk_norm_rope_workspace_bytes.restype = i32
+    lib.muon_qk_norm_rope_bwd.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, i32, i64, i64, i32, i32, i32, vp, vp, i32, *angles,
+                                          vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.muon_qk_norm_rope_bwd.restype = i32
+    lib.muon_token_logp_workspace_bytes.argtypes = [i64, i64, P(sz)]
+    lib.muon_token_logp_workspace_bytes.restype = i32
+    lib.muon_token_logp_fwd.argtypes = [vp, i64, i32, i64, i64, vp, f32, vp, vp, vp, sz, vp]
+    lib.muon_token_logp_fwd.restype = i32
+    lib.muon_token_logp_bwd.argtypes = [vp, i64, i32, i64, i64, vp, f32, vp, vp, vp, vp, i64, vp]
+    lib.muon_token_logp_bwd.restype = i32
+    lib.muon_policy_loss_workspace_bytes.argtypes = [i64, P(sz)]
+    lib.muon_policy_loss_workspace_bytes.restype = i32
+    lib.muon_policy_loss.argtypes = [vp, vp, vp, vp, vp, i64, f32, f32, f32, vp, vp, vp, vp, vp, sz, vp]
+    lib.muon_policy_loss.restype = i32
+    lib.muon_preference_loss_workspace_bytes.argtypes = [i64, i64, P(sz)]
+    lib.muon_preference_loss_workspace_bytes.restype = i32
+    lib.muon_preference_loss.argtypes = [vp, vp, vp, i64, vp, i64, vp, f32, f32, f32, i32, vp, vp, vp, vp, vp, sz, vp]
+    lib.muon_preference_loss.restype = i32
     lib.muon_workspace_status.argtypes = [vp, vp, sz, vp, P(i32)]
     lib.muon_workspace_status.restype = i32
     lib.muon_set_wait_limit.argtypes = [ctypes.c_uint32]

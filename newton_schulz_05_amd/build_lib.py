@@ -23,8 +23,9 @@ DEVICE_FLAGS = ["-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops"]
 COMMON = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-Wall",
           "-Wno-unused-function", "-Wno-unused-variable"] + DEVICE_FLAGS
 
-SOURCES = ["plan.cpp", "validate.cpp", "validate_ops.cpp", "api.cpp", "api_ops.cpp", "timer.cpp",
-           "k_large.hip", "k_skinny.hip", "k_elem.hip", "k_norm_fwd.hip", "k_norm_bwd.hip", "k_dropout.hip", "k_route.hip"]
+SOURCES = ["plan.cpp", "validate.cpp", "validate_ops.cpp", "api.cpp", "api_ops.cpp", "api_ends.cpp", "timer.cpp",
+           "k_large.hip", "k_skinny.hip", "k_elem.hip", "k_norm_fwd.hip", "k_norm_bwd.hip", "k_dropout.hip", "k_route.hip",
+           "k_heads.hip", "k_logp.hip", "k_loss.hip"]
 
 
 def _compile(src: str) -> str:

@@ -7,25 +7,12 @@
 #include <string>
 #include <vector>
 
-#include "../../include/muon.h"
-#include "launch.hpp"
-#include "ops.hpp"
-#include "validate_ops.hpp"
+#include "api_ops.hpp"
 
 namespace {
 
+using namespace muon::api;
 using muon::Operand;
-
-int64_t elem(muon_dtype dt) { return dt == MUON_BF16 ? 2 : 4; }
-
-Operand matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, muon_dtype dt, bool written,
-               bool optional = false) {
-  return {name, p, rows, cols * elem(dt), ld * elem(dt), int(elem(dt)), written, optional};
-}
-// n elements of `size` bytes.
-Operand vec(const char* name, const void* p, int64_t n, int64_t size, bool written, bool optional = false) {
-  return {name, p, n > 0 ? 1 : 0, n * size, n * size, int(size), written, optional};
-}
 
 muon::DropArgs drop_args(float p, uint64_t seed, uint64_t offset, const uint64_t* offset_dev) {
   muon::DropArgs d{};
@@ -37,28 +24,6 @@ muon::DropArgs drop_args(float p, uint64_t seed, uint64_t offset, const uint64_t
   d.offset_dev = offset_dev;
   return d;
 }
-
-muon_status launched(hipError_t e) {
-  if (e == hipSuccess) return MUON_OK;
-  return muon::api_fail(MUON_ERR_HIP, std::string("kernel launch failed: ") + hipGetErrorString(e));
-}
-
-// No C++ exception (an out-of-memory std::bad_alloc of the argument lists)
-// leaves a C entry point.
-template <typename F> muon_status guarded(F f) {
-  try {
-    std::string d;
-    const muon_status s = f(&d);
-    return s == MUON_OK || d.empty() ? s : muon::api_fail(s, d);
-  } catch (...) {
-    return MUON_ERR_INVALID_ARG;
-  }
-}
-
-#define MUON_TRY(call)                                   \
-  do {                                                   \
-    if (const muon_status s_ = (call); s_ != MUON_OK) return s_; \
-  } while (0)
 
 muon_status norm_fwd(const void* x, int64_t ld_x, const void* res, int64_t ld_res, muon_dtype dt, const void* gamma,
                      const void* beta, muon_dtype param_dt, int64_t rows, int64_t cols, float eps,

@@ -1,5 +1,6 @@
 // Host-side launch interface of the training operators beside the step:
-// layer norm, dropout, the two fused, and the expert router.
+// layer norm, dropout, the two fused, the expert router, the norm and rotation of
+// query and key heads, token log-probabilities and the losses on them.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -96,11 +97,106 @@ struct RouteBwdArgs {
   void* dlogits;
 };
 
+// Quotients of numbers below 2^31 by d: floor(r mul / 2^(32 + shift)).
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+
+// The heads of queries or of keys as rows, in the order of their input's
+// memory: row r stands at (i0, i1, i2), i0 = r % n0, i1 = r / n0 % n1.
+struct HeadRows {
+  const void* x;
+  const void* dy;     // backward
+  void* out;          // forward: y; backward: dx
+  const void* gamma;  // null: 1
+  void* dgamma;       // null: not wanted
+  float* part;        // [wgs][dim] partial sums of dgamma, or null
+  FastDiv n0, n1;
+  int64_t s_x[3], s_dy[3], s_out[3];
+  int64_t s_pos[3];   // of the word of positions, or of the table's row
+  uint32_t rows;
+  int wgs;            // workgroups that take these rows
+};
+
+struct HeadArgs {
+  HeadRows q, k;
+  const float* cos;
+  const float* sin;
+  const int64_t* positions;  // null: s_pos leads to the table's row itself
+  int64_t table_rows;
+  int dim, rot;
+  float eps;
+  bool wbf16;
+};
+
+struct LogpArgs {
+  const void* logits;
+  const int64_t* targets;
+  int64_t rows, cols, ld;
+  float scale, scale2;  // scale2 = scale log2(e)
+  float* logp;
+  float* lse;
+  int parts;
+  float* part;          // [rows][parts][2]: maximum and sum
+};
+
+struct LogpBwdArgs {
+  const void* logits;
+  const int64_t* targets;
+  int64_t rows, cols, ld, ld_d;
+  float scale;
+  const float* logp;
+  const float* lse;
+  const float* dlogp;
+  void* dlogits;
+};
+
+struct PolicyArgs {
+  const float* logp;
+  const float* old_logp;  // null: logp
+  const float* ref;       // null: no KL term
+  const float* adv;
+  const float* weight;    // null: 1
+  const float* dloss;     // null: 1
+  int64_t tokens;
+  double low, high;           // 1 - clip_low, 1 + clip_high
+  double log_low, log_high;
+  double beta;
+  float* loss;
+  float* terms;           // or null
+  float* dlogp;           // or null
+  int parts;
+  double* part;           // [parts][3]
+};
+
+struct PrefArgs {
+  const float* logp;
+  const float* ref;      // null: 0
+  const uint8_t* valid;  // null: every token counts
+  const int64_t* offsets;
+  const float* weight;   // null: 1 / pairs
+  const float* dloss;    // null: 1
+  int64_t tokens, pairs;
+  double beta, margin, smoothing;
+  int average;
+  float* loss;
+  float* rewards;        // or null
+  float* dlogp;          // or null
+  int chunks;
+  double* part;          // [2 pairs][chunks][2]: sum and number of tokens
+};
+
 // `bf16`: element type of the activations, `wbf16`: of gamma and beta.
 hipError_t run_norm_fwd(const NormFwdArgs& a, bool bf16, bool wbf16, bool fused, hipStream_t st);
 hipError_t run_norm_bwd(const NormBwdArgs& a, bool bf16, bool wbf16, bool fused, hipStream_t st);
 hipError_t run_dropout(const DropoutArgs& a, bool bf16, hipStream_t st);
 hipError_t run_route_fwd(const RouteArgs& a, bool bf16, hipStream_t st);
 hipError_t run_route_bwd(const RouteBwdArgs& a, bool bf16, hipStream_t st);
+hipError_t run_heads_fwd(const HeadArgs& a, bool bf16, bool interleaved, hipStream_t st);
+hipError_t run_heads_bwd(const HeadArgs& a, bool bf16, bool interleaved, hipStream_t st);
+hipError_t run_logp_fwd(const LogpArgs& a, bool bf16, hipStream_t st);
+hipError_t run_logp_bwd(const LogpBwdArgs& a, bool bf16, hipStream_t st);
+hipError_t run_policy_loss(const PolicyArgs& a, hipStream_t st);
+hipError_t run_preference_loss(const PrefArgs& a, hipStream_t st);
 
 }  // namespace muon

@@ -184,12 +184,12 @@ template <int CTRL> __device__ __forceinline__ uint32_t dpp(uint32_t x) {
 }
 
 template <int N, typename V, typename F> __device__ __forceinline__ V lane_reduce(V v, F f) {
-  static_assert(sizeof(V) == 4 && (N == 8 || N == 16 || N == 32 || N == 64));
+  static_assert(sizeof(V) == 4 && (N == 4 || N == 8 || N == 16 || N == 32 || N == 64));
   auto bits = [](V x) { return __builtin_bit_cast(uint32_t, x); };
   auto val = [](uint32_t x) { return __builtin_bit_cast(V, x); };
   v = f(v, val(dpp<0xB1>(bits(v))));   // quad_perm [1,0,3,2]
   v = f(v, val(dpp<0x4E>(bits(v))));   // quad_perm [2,3,0,1]
-  v = f(v, val(dpp<0x141>(bits(v))));  // mirror of 8 lanes
+  if constexpr (N >= 8) v = f(v, val(dpp<0x141>(bits(v))));   // mirror of 8 lanes
   if constexpr (N >= 16) v = f(v, val(dpp<0x140>(bits(v))));  // mirror of 16 lanes
   if constexpr (N >= 32) {
     const auto a = __builtin_amdgcn_permlane16_swap(bits(v), bits(v), false, false);
@@ -208,7 +208,8 @@ template <int N> __device__ __forceinline__ float lane_sum(float v) {
 // Sum over the lanes that stand at the same place of their group of
 // LANES.
 template <int LANES> __device__ __forceinline__ float across_groups(float v) {
-  if constexpr (LANES == 8) v += __uint_as_float(dpp<0x128>(__float_as_uint(v)));  // 8 lanes on within 16
+  if constexpr (LANES <= 8) v += __uint_as_float(dpp<0x128>(__float_as_uint(v)));  // 8 lanes on within 16
+  if constexpr (LANES == 4) v += __uint_as_float(dpp<0x124>(__float_as_uint(v)));  // 4 lanes on within 16
   if constexpr (LANES <= 16) {
     const uint32_t x = __float_as_uint(v);
     const auto a = __builtin_amdgcn_permlane16_swap(x, x, false, false);

@@ -65,4 +65,59 @@ inline int64_t route_parts(int64_t rows, int64_t experts) {
   return rows <= 2 * per ? 1 : std::min<int64_t>((rows + per - 1) / per, most);
 }
 
+// ---- norm and rotation of query and key heads ----
+constexpr int64_t kHeadMaxDim = 512;  // a head's row is held by at most one wave
+constexpr int64_t kHeadMaxRows = 0x7fffffff;
+constexpr int kHeadThreads = 256;
+
+// Lanes that share one head's row, each with two vectors of 8 elements.  Pairs
+// that lie rot / 2 apart are one lane's: the vectors of the first half of the
+// turned elements each with that of the second half, then the elements that are
+// not turned two vectors a lane.
+inline int head_lanes(int dim, int rot, bool interleaved) {
+  const int need = interleaved || rot == 0 ? (dim + 15) / 16 : (rot / 2 + 7) / 8 + (dim - rot + 15) / 16;
+  int lanes = 4;
+  while (lanes < need) lanes *= 2;
+  return lanes;
+}
+
+// Workgroups of the backward pass, one partial sum of dgamma each: a fixed number
+// in all, queries and keys in proportion to their rows.
+constexpr int kHeadMaxParts = 1024;
+struct HeadSplit {
+  int q, k;
+};
+inline HeadSplit head_split(int64_t rows_q, int64_t rows_k) {
+  // a fixed number of rows a workgroup at least, whatever the lanes of a row
+  const int64_t all = rows_q + rows_k, parts = std::min<int64_t>(kHeadMaxParts, (all + 63) / 64);
+  HeadSplit s{0, 0};
+  if (rows_k > 0) s.k = int(std::max<int64_t>(1, parts * rows_k / all));
+  if (rows_q > 0) s.q = int(std::max<int64_t>(1, parts - s.k));
+  return s;
+}
+
+// ---- token log-probabilities ----
+constexpr int64_t kLogpMaxVocab = int64_t(1) << 24;
+// Workgroups that share one row of the forward pass: one for many rows or short
+// ones.
+constexpr int kLogpMaxParts = 64;
+inline int logp_parts(int64_t rows, int64_t vocab) {
+  if (rows >= 512 || vocab <= 16384) return 1;
+  const int64_t want = (512 + rows - 1) / std::max<int64_t>(rows, 1);
+  return int(std::min<int64_t>({want, (vocab + 4095) / 4096, int64_t(kLogpMaxParts)}));
+}
+
+// ---- losses ----
+constexpr int64_t kLossMaxTokens = int64_t(1) << 40;
+constexpr int64_t kPrefMaxPairs = int64_t(1) << 20;
+constexpr int kPolicyMaxParts = 256, kPrefMaxChunks = 64;
+inline int policy_parts(int64_t tokens) {
+  return tokens <= 4096 ? 1 : int(std::min<int64_t>((tokens + 1023) / 1024, kPolicyMaxParts));
+}
+// Workgroups that share one sequence of the preference loss.
+inline int pref_chunks(int64_t tokens, int64_t pairs) {
+  const int64_t each = tokens / std::max<int64_t>(2 * pairs, 1);
+  return int(std::max<int64_t>(1, std::min<int64_t>((each + 2047) / 2048, kPrefMaxChunks)));
+}
+
 }  // namespace muon

@@ -1,6 +1,7 @@
 // Argument validation of the training operators (see validate_ops.hpp).
 #include "validate_ops.hpp"
 
+#include <algorithm>
 #include <cmath>
 
 namespace muon {
@@ -32,6 +33,10 @@ bool overlap(const Operand& a, const Operand& b) {
 
 muon_status check_operands(const std::vector<Operand>& ops, std::string* detail, int alias_written, int alias_read_a,
                            int alias_read_b) {
+  return check_operands(ops, detail, {{alias_written, alias_read_a}, {alias_written, alias_read_b}});
+}
+
+muon_status check_operands(const std::vector<Operand>& ops, std::string* detail, const std::vector<Alias>& same) {
   for (const Operand& o : ops) {
     if (!o.p) {
       if (o.optional || o.rows < 1) continue;
@@ -45,9 +50,8 @@ muon_status check_operands(const std::vector<Operand>& ops, std::string* detail,
     if (!ops[i].written) continue;
     for (size_t j = 0; j < ops.size(); ++j) {
       if (j == i || (ops[j].written && j < i) || !overlap(ops[i], ops[j])) continue;
-      if (int(i) == alias_written && (int(j) == alias_read_a || int(j) == alias_read_b) && ops[i].p == ops[j].p &&
-          (ops[i].pitch == ops[j].pitch || ops[i].rows == 1))
-        continue;
+      const bool may = std::find(same.begin(), same.end(), Alias(int(i), int(j))) != same.end();
+      if (may && ops[i].p == ops[j].p && (ops[i].pitch == ops[j].pitch || ops[i].rows == 1)) continue;
       return fail(MUON_ERR_INVALID_ARG, detail, std::string(ops[i].name) + " and " + ops[j].name + " overlap");
     }
   }
@@ -106,6 +110,102 @@ muon_status check_route(int64_t tokens, int64_t ld, int32_t experts, int32_t k, 
     return fail(MUON_ERR_SHAPE, detail, "tokens * k must fit in 32 bits (the counts' type)");
   if (renorm != 0 && renorm != 1) return fail(MUON_ERR_INVALID_ARG, detail, "renorm must be 0 or 1");
   if (!std::isfinite(coef)) return fail(MUON_ERR_INVALID_ARG, detail, "coef must be finite");
+  return MUON_OK;
+}
+
+muon_status head_operand(const char* name, const void* p, const muon_head_strides* s, int64_t batch, int64_t tokens,
+                         int64_t heads, int64_t dim, int size, bool written, Operand* op, std::string* detail) {
+  *op = {name, p, batch * tokens * heads > 0 ? 1 : 0, dim * size, dim * size, size, written, false};
+  if (op->rows == 0) return MUON_OK;
+  if (!s) return fail(MUON_ERR_INVALID_ARG, detail, std::string(name) + ": strides are null");
+  struct Dim {
+    int64_t n, stride;
+  } d[3] = {{batch, s->batch}, {tokens, s->token}, {heads, s->head}};
+  // innermost first; a dimension of one entry has no stride
+  std::sort(d, d + 3, [](const Dim& a, const Dim& b) { return (a.n > 1 ? a.stride : 0) < (b.n > 1 ? b.stride : 0); });
+  int64_t span = dim;  // elements up to the end of the dimensions so far
+  for (const Dim& x : d) {
+    if (x.n == 1) continue;
+    if (x.stride < span)
+      return fail(MUON_ERR_INVALID_ARG, detail, std::string(name) + ": the dimensions do not nest (a stride is smaller than what lies within)");
+    if (x.stride > kMaxExtent / x.n) return fail(MUON_ERR_SHAPE, detail, std::string(name) + ": tensor too large");
+    span += (x.n - 1) * x.stride;
+  }
+  // outermost first: dimensions that follow one another without a gap are one
+  op->width = span * size;
+  op->pitch = span * size;
+  for (int i = 2; i >= 0; --i) {
+    if (d[i].n == 1) continue;
+    if (op->rows > 1 && op->pitch != d[i].n * d[i].stride * size) break;
+    op->rows *= d[i].n;
+    op->pitch = d[i].stride * size;
+    span -= (d[i].n - 1) * d[i].stride;
+    op->width = span * size;
+  }
+  return MUON_OK;
+}
+
+muon_status check_heads(muon_dtype dt, muon_dtype param_dt, int64_t batch, int64_t tokens, int32_t heads_q,
+                        int32_t heads_k, bool keys, int32_t dim, float eps, const float* cos, const float* sin,
+                        int64_t table_rows, int32_t rot, int32_t interleaved, const int64_t* positions,
+                        int64_t positions_batch, std::string* detail) {
+  muon_status s = check_op_dtype(dt, "dt", detail);
+  if (s == MUON_OK) s = check_op_dtype(param_dt, "param_dt", detail);
+  if (s != MUON_OK) return s;
+  if (dim < 1 || dim > kHeadMaxDim)
+    return fail(MUON_ERR_SHAPE, detail, "dim must be in 1.." + std::to_string(kHeadMaxDim));
+  if (batch < 0 || tokens < 0) return fail(MUON_ERR_SHAPE, detail, "batch and tokens must be >= 0");
+  if (heads_q < 1) return fail(MUON_ERR_SHAPE, detail, "heads_q must be >= 1");
+  if (keys ? heads_k < 1 : heads_k != 0)
+    return fail(MUON_ERR_SHAPE, detail, "heads_k must be >= 1, or 0 without keys");
+  const int64_t heads = std::max(heads_q, heads_k);
+  if (batch > kHeadMaxRows || tokens > kHeadMaxRows || batch * tokens > kHeadMaxRows / heads)
+    return fail(MUON_ERR_SHAPE, detail, "batch * tokens * heads must be below 2^31");
+  if (!(std::isfinite(eps) && eps > 0.0f)) return fail(MUON_ERR_INVALID_ARG, detail, "eps must be finite and > 0");
+  if (interleaved != 0 && interleaved != 1) return fail(MUON_ERR_INVALID_ARG, detail, "interleaved must be 0 or 1");
+  if (rot < 0 || rot > dim || rot % 2 != 0)
+    return fail(MUON_ERR_SHAPE, detail, "rot must be even and in 0..dim");
+  if (rot > 0) {
+    if (table_rows < 0 || table_rows > kMaxExtent / rot) return fail(MUON_ERR_SHAPE, detail, "table_rows is out of range");
+    if (table_rows > 0 && (!cos || !sin)) return fail(MUON_ERR_INVALID_ARG, detail, "cos or sin is null");
+    if (positions && batch > 1 && positions_batch != 0 && positions_batch < tokens)
+      return fail(MUON_ERR_INVALID_ARG, detail, "positions_batch must be 0 or at least tokens");
+    if (positions_batch < 0 || (batch > 1 && positions_batch > kMaxExtent / batch))
+      return fail(MUON_ERR_SHAPE, detail, "positions_batch is out of range");
+  }
+  return MUON_OK;
+}
+
+muon_status check_logp(int64_t tokens, int64_t vocab, const std::vector<int64_t>& pitches, muon_dtype dt, float scale,
+                       std::string* detail) {
+  muon_status s = check_op_dtype(dt, "dt", detail);
+  if (s == MUON_OK) s = check_rows(tokens, vocab, kLogpMaxVocab, pitches, detail);
+  if (s != MUON_OK) return s;
+  if (tokens > kHeadMaxRows) return fail(MUON_ERR_SHAPE, detail, "tokens must be below 2^31");
+  // the factor under the exponential is scale log2(e)
+  if (!(scale > 0.0f && scale <= 1e30f)) return fail(MUON_ERR_INVALID_ARG, detail, "scale must be > 0 and at most 1e30");
+  return MUON_OK;
+}
+
+muon_status check_policy(int64_t tokens, float clip_low, float clip_high, float beta, std::string* detail) {
+  if (tokens < 0 || tokens > kLossMaxTokens) return fail(MUON_ERR_SHAPE, detail, "tokens is out of range");
+  if (!(clip_low >= 0.0f && clip_low <= 1.0f)) return fail(MUON_ERR_INVALID_ARG, detail, "clip_low must be in [0, 1]");
+  if (!(std::isfinite(clip_high) && clip_high >= 0.0f))
+    return fail(MUON_ERR_INVALID_ARG, detail, "clip_high must be finite and >= 0");
+  if (!std::isfinite(beta)) return fail(MUON_ERR_INVALID_ARG, detail, "beta must be finite");
+  return MUON_OK;
+}
+
+muon_status check_preference(int64_t tokens, int64_t pairs, float beta, float margin, float smoothing,
+                             int32_t average, std::string* detail) {
+  if (tokens < 0 || tokens > kLossMaxTokens) return fail(MUON_ERR_SHAPE, detail, "tokens is out of range");
+  if (pairs < 0 || pairs > kPrefMaxPairs)
+    return fail(MUON_ERR_SHAPE, detail, "pairs must be in 0.." + std::to_string(kPrefMaxPairs));
+  if (!std::isfinite(beta) || !std::isfinite(margin))
+    return fail(MUON_ERR_INVALID_ARG, detail, "beta and margin must be finite");
+  if (!(smoothing >= 0.0f && smoothing <= 1.0f))
+    return fail(MUON_ERR_INVALID_ARG, detail, "smoothing must be in [0, 1]");
+  if (average != 0 && average != 1) return fail(MUON_ERR_INVALID_ARG, detail, "average must be 0 or 1");
   return MUON_OK;
 }
 

@@ -1,5 +1,5 @@
 // Argument validation of the training operators' entry points (layer norm,
-// dropout, router).  Pure C++ (no HIP calls), like validate.hpp: each function
+// dropout, router, query and key heads, token log-probabilities, losses).  Pure C++ (no HIP calls), like validate.hpp: each function
 // returns MUON_OK, or an error status with `detail` filled, before anything is
 // enqueued, and none of them touches device memory.
 #pragma once
@@ -8,6 +8,7 @@
 #include <stdint.h>
 
 #include <string>
+#include <utility>
 #include <vector>
 
 #include "../../include/muon.h"
@@ -36,6 +37,29 @@ bool overlap(const Operand& a, const Operand& b);
 muon_status check_operands(const std::vector<Operand>& ops, std::string* detail, int alias_written = -1,
                            int alias_read_a = -1, int alias_read_b = -1);
 
+// The same with any number of pairs (written, read) that may be one tensor.
+typedef std::pair<int, int> Alias;
+muon_status check_operands(const std::vector<Operand>& ops, std::string* detail, const std::vector<Alias>& same);
+
+// A tensor [batch, tokens, heads, dim] of `size`-byte elements: its dimensions
+// nest, and its offsets stay far inside 64 bits.  `op` receives it as runs of
+// one pitch: the outer dimensions that follow one another, and in each run all
+// that lies within.
+muon_status head_operand(const char* name, const void* p, const muon_head_strides* s, int64_t batch, int64_t tokens,
+                         int64_t heads, int64_t dim, int size, bool written, Operand* op, std::string* detail);
+
+// Sizes and scalars of a call on query and key heads.
+muon_status check_heads(muon_dtype dt, muon_dtype param_dt, int64_t batch, int64_t tokens, int32_t heads_q,
+                        int32_t heads_k, bool keys, int32_t dim, float eps, const float* cos, const float* sin,
+                        int64_t table_rows, int32_t rot, int32_t interleaved, const int64_t* positions,
+                        int64_t positions_batch, std::string* detail);
+
+muon_status check_logp(int64_t tokens, int64_t vocab, const std::vector<int64_t>& pitches, muon_dtype dt, float scale,
+                       std::string* detail);
+muon_status check_policy(int64_t tokens, float clip_low, float clip_high, float beta, std::string* detail);
+muon_status check_preference(int64_t tokens, int64_t pairs, float beta, float margin, float smoothing,
+                             int32_t average, std::string* detail);
+
 muon_status check_op_dtype(muon_dtype dt, const char* what, std::string* detail);
 
 // rows >= 0, cols in 1 .. max_cols, every pitch (elements) >= cols, and sizes
@@ -59,6 +83,23 @@ constexpr int64_t kRouteTerms = kRouteMaxExperts / 16;
 inline size_t route_workspace_bytes(int64_t rows, int64_t experts) {
   const int64_t parts = route_parts(rows, experts);
   return parts > 1 ? size_t(kRouteTerms) * 8 + 16 + size_t(parts) * (size_t(experts) * 8 + 4) : 0;
+}
+
+// Partial sums of dgamma: none where one workgroup takes all rows of a kind.
+inline size_t heads_workspace_bytes(int64_t rows_q, int64_t rows_k, int64_t dim) {
+  const HeadSplit s = head_split(rows_q, rows_k);
+  return size_t((s.q > 1 ? s.q : 0) + (s.k > 1 ? s.k : 0)) * size_t(dim) * 4;
+}
+inline size_t logp_workspace_bytes(int64_t tokens, int64_t vocab) {
+  const int parts = logp_parts(tokens, vocab);
+  return parts > 1 ? size_t(tokens) * size_t(parts) * 8 : 0;
+}
+inline size_t policy_workspace_bytes(int64_t tokens) {
+  const int parts = policy_parts(tokens);
+  return parts > 1 ? size_t(parts) * 24 : 0;
+}
+inline size_t preference_workspace_bytes(int64_t tokens, int64_t pairs) {
+  return size_t(2 * pairs) * size_t(pref_chunks(tokens, pairs)) * 16;
 }
 
 // Sizes of a router call.

@@ -1,5 +1,7 @@
 """Binding of the training operators beside the step (include/muon.h): layer
-norm, dropout, the two fused with the residual add, and the expert router.
+norm, dropout, the two fused with the residual add, the expert router, the norm
+and rotation of query and key heads, token log-probabilities, and the policy and
+preference losses on them.
 
 Argument marshalling only, like ``binding``: the caller gives the output
 tensors, every call is one C call on the current stream of the tensors'
@@ -16,7 +18,7 @@ from typing import Optional, Tuple
 
 import torch
 
-from .binding import MUON_BF16, MUON_F32, MuonError, _check, load_library
+from .binding import MUON_BF16, MUON_F32, MuonError, MuonHeadStrides, _check, load_library
 
 
 _CODES = {torch.float32: MUON_F32, torch.bfloat16: MUON_BF16}
@@ -312,3 +314,216 @@ def route_backward(logits, indices, counts, n_tokens, dlogits, *, dgates=None, d
     _call(dev, load_library().muon_route_bwd, logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, experts, k, v,
           1 if renorm else 0, coef, indices.data_ptr(), c, n, None if dgates is None else dgates.data_ptr(), dl,
           dlogits.data_ptr(), ld_d, st)
+
+
+@functools.lru_cache(maxsize=1024)
+def _head_strides(batch: int, token: int, head: int):
+    """(structure, its address) of a muon_head_strides."""
+    s = MuonHeadStrides(batch, token, head)
+    return s, ctypes.addressof(s)
+
+
+def _heads(t: torch.Tensor, what: str, like: Optional[torch.Tensor] = None):
+    """Strides' structure of a tensor of heads, [batch, tokens, heads, dim] or
+    [tokens, heads, dim], that has to match `like`."""
+    shape, stride = t.shape, t.stride()
+    if like is not None:
+        if shape != like.shape:
+            raise MuonError(2, f"{what} has shape {tuple(shape)}, expected {tuple(like.shape)}")
+        if t.dtype is not like.dtype:
+            raise MuonError(3, f"{what} has dtype {t.dtype}, expected {like.dtype}")
+    if stride[-1] != 1 and shape[-1] > 1:
+        raise MuonError(1, f"{what}: the last dimension is not contiguous")
+    return _head_strides(stride[0] if len(shape) == 4 else 0, stride[-3], stride[-2])
+
+
+def _head_sizes(q: torch.Tensor, k: Optional[torch.Tensor]) -> Tuple[int, int, int, int, int]:
+    """(batch, tokens, query heads, key heads, dim)."""
+    shape = q.shape
+    if len(shape) not in (3, 4):
+        raise MuonError(2, f"q has {len(shape)} dimensions, expected [batch, tokens, heads, dim] or [tokens, heads, dim]")
+    if k is not None:
+        ks = k.shape
+        if len(ks) != len(shape) or ks[:-2] != shape[:-2] or ks[-1] != shape[-1]:
+            raise MuonError(2, f"k has shape {tuple(ks)}, q {tuple(shape)}: they may differ in their heads only")
+        if k.dtype is not q.dtype:
+            raise MuonError(3, f"k has dtype {k.dtype}, expected {q.dtype}")
+    return (shape[0] if len(shape) == 4 else 1), shape[-3], shape[-2], (0 if k is None else k.shape[-2]), shape[-1]
+
+
+def _angles(cos, sin, positions, batch: int, tokens: int) -> Tuple:
+    """(cos, sin, table rows, rot, positions, their batch stride)."""
+    if (cos is None) != (sin is None):
+        raise MuonError(1, "cos and sin come together")
+    if cos is None:
+        return None, None, 0, 0, None, 0
+    if cos.dim() != 2 or sin.shape != cos.shape:
+        raise MuonError(2, f"cos and sin have shapes {tuple(cos.shape)} and {tuple(sin.shape)}, expected [table rows, rot / 2]")
+    rows, half = cos.shape
+    c, s = _flat(cos, rows * half, _F32, "cos"), _flat(sin, rows * half, _F32, "sin")
+    if positions is None:
+        return c, s, rows, 2 * half, None, 0
+    if positions.dtype is not torch.int64:
+        raise MuonError(3, f"positions has dtype {positions.dtype}, expected torch.int64")
+    shape = tuple(positions.shape)
+    if shape == (tokens,):
+        each = 0
+    elif shape == (batch, tokens):
+        each = positions.stride(0)
+        if batch > 1 and each != 0 and each < tokens:
+            raise MuonError(1, "positions: the sequences overlap")
+    else:
+        raise MuonError(2, f"positions has shape {shape}, expected ({tokens},) or ({batch}, {tokens})")
+    if tokens > 1 and positions.stride(-1) != 1:
+        raise MuonError(1, "positions: the last dimension is not contiguous")
+    return c, s, rows, 2 * half, positions.data_ptr(), each if batch > 1 else 0
+
+
+def qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, q_out, k_out, *, positions=None, interleaved: bool = False,
+                 eps: float = 1e-6, stream=None) -> None:
+    """q_out and k_out = the heads of q and k divided by their root mean square,
+    times gamma, their first 2 * cos.shape[1] elements turned by the tokens'
+    angles (muon_qk_norm_rope_fwd).  Heads are tensors [batch, tokens, heads,
+    dim] or [tokens, heads, dim] of any order in memory (slices of a projection's
+    output, transposed ones); k, gamma_k and k_out may be None.  cos and sin:
+    [table rows, rot / 2] float32, or None for no rotation.  positions: int64,
+    [batch, tokens] or [tokens] (None: 0, 1, ...): the rows of cos and sin; a
+    token whose row does not exist is not turned.  q_out may be q itself, k_out k
+    itself."""
+    batch, tokens, hq, hk, dim = _head_sizes(q, k)
+    sq, sqo = _heads(q, "q"), _heads(q_out, "q_out", q)
+    if (k is None) != (k_out is None):
+        raise MuonError(1, "k and k_out come together")
+    sk, sko = (None, 0) if k is None else _heads(k, "k"), (None, 0) if k is None else _heads(k_out, "k_out", k)
+    wdt = _param_dtype(q, gamma_q, gamma_k)
+    gq, gk = _param(gamma_q, wdt, dim, "gamma_q"), _param(gamma_k, wdt, dim, "gamma_k")
+    c, s, rows, rot, pos, each = _angles(cos, sin, positions, batch, tokens)
+    dev, st = _device(stream, q, k, gamma_q, gamma_k, cos, sin, positions, q_out, k_out)
+    _call(dev, load_library().muon_qk_norm_rope_fwd, q.data_ptr(), sq[1], None if k is None else k.data_ptr(), sk[1],
+          _dtype_code(q.dtype), batch, tokens, hq, hk, dim, gq, gk, _dtype_code(wdt), eps, c, s, rows, rot,
+          1 if interleaved else 0, pos, each, q_out.data_ptr(), sqo[1], None if k is None else k_out.data_ptr(), sko[1], st)
+
+
+@functools.lru_cache(maxsize=256)
+def _heads_workspace(rows_q: int, rows_k: int, dim: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().muon_qk_norm_rope_workspace_bytes(rows_q, rows_k, dim, ctypes.byref(n)))
+    return n.value
+
+
+def qk_norm_rope_backward(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, dq, dk, *, dgamma_q=None, dgamma_k=None,
+                          positions=None, interleaved: bool = False, eps: float = 1e-6,
+                          workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of qk_norm_rope (muon_qk_norm_rope_bwd) from those that reach
+    q_out and k_out and the forward call's q and k: dq and dk, and dgamma_q and
+    dgamma_k where given, in the gains' dtype (the `grads` of adamw_step).  dq
+    may be dq_out itself, dk dk_out itself."""
+    batch, tokens, hq, hk, dim = _head_sizes(q, k)
+    sq, sdqo, sdq = _heads(q, "q"), _heads(dq_out, "dq_out", q), _heads(dq, "dq", q)
+    if (k is None) != (dk_out is None) or (k is None) != (dk is None):
+        raise MuonError(1, "k, dk_out and dk come together")
+    sk = sdko = sdk = (None, 0)
+    if k is not None:
+        sk, sdko, sdk = _heads(k, "k"), _heads(dk_out, "dk_out", k), _heads(dk, "dk", k)
+    wdt = _param_dtype(q, gamma_q, gamma_k, dgamma_q, dgamma_k)
+    gq, gk = _param(gamma_q, wdt, dim, "gamma_q"), _param(gamma_k, wdt, dim, "gamma_k")
+    dgq, dgk = _param(dgamma_q, wdt, dim, "dgamma_q"), _param(dgamma_k, wdt, dim, "dgamma_k")
+    c, s, rows, rot, pos, each = _angles(cos, sin, positions, batch, tokens)
+    dev, st = _device(stream, q, k, dq_out, dk_out, gamma_q, gamma_k, cos, sin, positions, dq, dk, dgamma_q, dgamma_k,
+                      workspace)
+    need = _heads_workspace(batch * tokens * hq, batch * tokens * hk, dim) if dgq or dgk else 0
+    keep, ws, ws_bytes = _workspace(workspace, need, stream, dev, st)
+    ptr = (lambda t: None) if k is None else torch.Tensor.data_ptr
+    _call(dev, load_library().muon_qk_norm_rope_bwd, dq_out.data_ptr(), sdqo[1], ptr(dk_out), sdko[1], q.data_ptr(), sq[1],
+          ptr(k), sk[1], _dtype_code(q.dtype), batch, tokens, hq, hk, dim, gq, gk, _dtype_code(wdt), eps, c, s, rows,
+          rot, 1 if interleaved else 0, pos, each, dq.data_ptr(), sdq[1], ptr(dk), sdk[1], dgq, dgk, ws, ws_bytes, st)
+
+
+@functools.lru_cache(maxsize=256)
+def _logp_workspace(rows: int, vocab: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().muon_token_logp_workspace_bytes(rows, vocab, ctypes.byref(n)))
+    return n.value
+
+
+def token_logp(logits, targets, logp, lse, *, scale: float = 1.0, workspace: Optional[torch.Tensor] = None,
+               stream=None) -> None:
+    """logp = log softmax(scale * logits) of every token's target, lse = log of
+    the softmax's sum (muon_token_logp_fwd).  targets: int64, one a token; one
+    outside the vocabulary (a prompt or padding token) gives 0 in both."""
+    rows, vocab, ld = _matrix(logits, "logits")
+    t = _flat(targets, rows, _WORD, "targets")
+    lp, ls = _flat(logp, rows, _F32, "logp"), _flat(lse, rows, _F32, "lse")
+    dev, st = _device(stream, logits, targets, logp, lse, workspace)
+    keep, ws, ws_bytes = _workspace(workspace, _logp_workspace(rows, vocab), stream, dev, st)
+    _call(dev, load_library().muon_token_logp_fwd, logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, vocab, t,
+          scale, lp, ls, ws, ws_bytes, st)
+
+
+def token_logp_backward(logits, targets, logp, lse, dlogp, dlogits, *, scale: float = 1.0, stream=None) -> None:
+    """Gradient of token_logp's logp by the logits (muon_token_logp_bwd), from
+    the logp and lse that it wrote and the gradient dlogp that reaches logp.
+    dlogits may be logits itself."""
+    rows, vocab, ld = _matrix(logits, "logits")
+    ld_d = _same(dlogits, logits, "dlogits")
+    t = _flat(targets, rows, _WORD, "targets")
+    lp, ls, d = _flat(logp, rows, _F32, "logp"), _flat(lse, rows, _F32, "lse"), _flat(dlogp, rows, _F32, "dlogp")
+    dev, st = _device(stream, logits, targets, logp, lse, dlogp, dlogits)
+    _call(dev, load_library().muon_token_logp_bwd, logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, vocab, t,
+          scale, lp, ls, d, dlogits.data_ptr(), ld_d, st)
+
+
+@functools.lru_cache(maxsize=256)
+def _policy_workspace(tokens: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().muon_policy_loss_workspace_bytes(tokens, ctypes.byref(n)))
+    return n.value
+
+
+def policy_loss(logp, old_logp, advantages, loss, *, ref_logp=None, weight=None, dlogp=None, dloss=None, terms=None,
+                clip_low: float = 0.2, clip_high: float = 0.2, beta: float = 0.0,
+                workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Clipped policy loss with a KL term, and its gradient dlogp where given
+    (muon_policy_loss): the loss is the sum of weight times a token's term, so
+    weight is 1 / n for a mean and 0 for tokens that do not count.  old_logp
+    None: logp itself (ratio 1); ref_logp None: no KL term; dloss, a device
+    float: what dlogp is multiplied by.  terms receives the policy sum, the KL sum
+    and the weight of the clipped tokens."""
+    n = logp.numel()
+    lp, ol = _flat(logp, n, _F32, "logp"), _flat(old_logp, n, _F32, "old_logp")
+    rf, ad = _flat(ref_logp, n, _F32, "ref_logp"), _flat(advantages, n, _F32, "advantages")
+    w, g = _flat(weight, n, _F32, "weight"), _flat(dlogp, n, _F32, "dlogp")
+    up, lo, tm = _flat(dloss, 1, _F32, "dloss"), _flat(loss, 1, _F32, "loss"), _flat(terms, 3, _F32, "terms")
+    dev, st = _device(stream, logp, old_logp, ref_logp, advantages, weight, dlogp, dloss, loss, terms, workspace)
+    keep, ws, ws_bytes = _workspace(workspace, _policy_workspace(n), stream, dev, st)
+    _call(dev, load_library().muon_policy_loss, lp, ol, rf, ad, w, n, clip_low, clip_high, beta, up, lo, tm, g, ws,
+          ws_bytes, st)
+
+
+@functools.lru_cache(maxsize=256)
+def _preference_workspace(tokens: int, pairs: int) -> int:
+    n = ctypes.c_size_t()
+    _check(load_library().muon_preference_loss_workspace_bytes(tokens, pairs, ctypes.byref(n)))
+    return n.value
+
+
+def preference_loss(logp, offsets, loss, *, ref_logp=None, valid=None, weight=None, rewards=None, dlogp=None, dloss=None,
+                    beta: float = 0.1, margin: float = 0.0, smoothing: float = 0.0, average: bool = False,
+                    workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Preference loss on pairs of answers, and its gradient dlogp where given
+    (muon_preference_loss).  offsets: int64, 2 * pairs + 1 rising ends of the
+    answers in logp, the preferred ones of all pairs first.  valid: uint8 or bool,
+    0 for tokens that do not count; weight: one a pair (None: 1 / pairs);
+    rewards receives beta times each answer's log-ratio (average: its mean)."""
+    n, ends = logp.numel(), offsets.numel()
+    if ends % 2 == 0:
+        raise MuonError(2, f"offsets has {ends} elements, expected 2 * pairs + 1")
+    pairs = ends // 2
+    lp, rf = _flat(logp, n, _F32, "logp"), _flat(ref_logp, n, _F32, "ref_logp")
+    v, off = _flat(valid, n, _MASK, "valid"), _flat(offsets, ends, _WORD, "offsets")
+    w, rw = _flat(weight, pairs, _F32, "weight"), _flat(rewards, 2 * pairs, _F32, "rewards")
+    g, up, lo = _flat(dlogp, n, _F32, "dlogp"), _flat(dloss, 1, _F32, "dloss"), _flat(loss, 1, _F32, "loss")
+    dev, st = _device(stream, logp, ref_logp, valid, offsets, weight, rewards, dlogp, dloss, loss, workspace)
+    keep, ws, ws_bytes = _workspace(workspace, _preference_workspace(n, pairs), stream, dev, st)
+    _call(dev, load_library().muon_preference_loss, lp, rf, v, n, off, pairs, w, beta, margin, smoothing,
+          1 if average else 0, up, lo, rw, g, ws, ws_bytes, st)
