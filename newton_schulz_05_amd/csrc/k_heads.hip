@@ -7,9 +7,8 @@
 //   backward  g = dy turned back, dgamma = sum over rows of g x r,
 //             dx = r (g gamma - x r mean(g gamma x r))
 //
-// A head's row is read once and held by 4 to 64 lanes with two vectors of 8
-// elements each.  Pairs that lie rot / 2 apart are one lane's two vectors, so
-// turning needs no exchange between lanes.  Sums are fp32; each output is rounded
+// A head's row is read once and held by 4 to 64 lanes, 16 elements each.  Both
+// elements of a pair are one lane's, so turning needs no exchange between lanes.  Sums are fp32; each output is rounded
 // once.
 #include "ops_dev.hpp"
 
@@ -29,58 +28,125 @@ __device__ __forceinline__ uint32_t quotient(uint32_t r, const FastDiv& f) {
   return f.d == 1 ? r : __umulhi(r, f.mul) >> f.shift;
 }
 
-// What a lane holds of every row: n0 elements at column c0 and n1 at c1, of
-// which the pairs up to nc are turned by the angles 8 t and on.
-struct LanePart {
-  int c0, c1, n0, n1, nc;
+// What a lane holds of every row: 16 elements in pieces of 16 bytes, n[i] of
+// them at column c[i].  A segment's pieces are dealt to its lanes in turn, so that
+// a wave's accesses are adjacent in either type.
+template <typename T> struct LanePart {
+  static constexpr int E = Piece<T>::N, P = 16 / E;
+  int c[P], n[P];
+  bool turned;
 };
-template <bool INTER> __device__ __forceinline__ LanePart lane_part(int t, int dim, int rot) {
-  auto some = [](int n) { return n < 0 ? 0 : n > 8 ? 8 : n; };
-  LanePart p;
+__device__ __forceinline__ int some(int n, int most) { return n < 0 ? 0 : n > most ? most : n; }
+
+template <typename T, bool INTER> __device__ __forceinline__ LanePart<T> lane_part(int t, int dim, int rot) {
+  constexpr int E = LanePart<T>::E, P = LanePart<T>::P;
+  LanePart<T> p;
   const int half = rot / 2, first = INTER ? 0 : (half + 7) / 8;
+  p.turned = INTER || t < first;
   if (INTER || t >= first) {
-    p.c0 = (INTER ? 0 : rot) + 16 * (t - first);
-    p.c1 = p.c0 + 8;
-    p.n0 = some(dim - p.c0);
-    p.n1 = some(dim - p.c1);
-    p.nc = INTER ? some(half - 8 * t) : 0;
+    const int from = INTER ? 0 : rot, lanes = (dim - from + 15) / 16, u = t - first;
+#pragma unroll
+    for (int i = 0; i < P; ++i) {
+      p.c[i] = from + E * (u + lanes * i);
+      p.n[i] = u < lanes ? some(dim - p.c[i], E) : 0;
+    }
   } else {
-    p.c0 = 8 * t;
-    p.c1 = half + 8 * t;
-    p.n0 = p.n1 = p.nc = some(half - 8 * t);
+#pragma unroll
+    for (int i = 0; i < P / 2; ++i) {
+      p.c[i] = E * (t + first * i);
+      p.c[P / 2 + i] = half + p.c[i];
+      p.n[i] = p.n[P / 2 + i] = some(half - p.c[i], E);
+    }
   }
   return p;
 }
 
-// n elements at col of a row of dim; with RAG the last ones behind n hold
-// anything until settled, without it n is 0 or 8.
-template <bool RAG, typename T>
-__device__ __forceinline__ Raw8<T> load_part(const T* row, int col, int n, int dim) {
-  if constexpr (RAG) return load_row8(row, unsigned(col), n > 0 ? dim - col : 0, dim);
-  else return load8(row + col, n > 0 ? 8 : 0);
-}
-template <bool RAG, typename T> __device__ __forceinline__ void store_part(T* p, int n, const Raw8<T>& r) {
-  store8(p, RAG ? n : (n > 0 ? 8 : 0), r);
-}
-template <bool RAG, typename T>
-__device__ __forceinline__ void unpack_part(Raw8<T> r, int col, int n, int dim, float (&v)[8]) {
-  if constexpr (RAG) settle8(r, n > 0 ? dim - col : 0, dim);
-  unpack8(r, v);
-  if constexpr (RAG) {
+// What does not fill its pieces: nothing; the angles alone (interleaved pairs,
+// rot no multiple of a piece); elements as well.
+enum Ragged { kWhole, kRaggedAngles, kRagged };
+
+// A lane's elements of a row.
+template <typename T> struct Held {
+  Piece<T> r[LanePart<T>::P];
+};
+template <int RAG, typename T> __device__ __forceinline__ void load_held(const T* row, const LanePart<T>& p, bool live, int dim, Held<T>& h) {
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = j < n ? v[j] : 0.0f;
+  for (int i = 0; i < LanePart<T>::P; ++i) {
+    const int n = live ? p.n[i] : 0;
+    if constexpr (RAG == kRagged && sizeof(T) == 2) h.r[i].r = load_row8(row, unsigned(p.c[i]), n > 0 ? dim - p.c[i] : 0, dim);
+    else h.r[i].template load<false>(row + p.c[i], RAG == kRagged ? n : (n > 0 ? LanePart<T>::E : 0));
+  }
+}
+template <int RAG, typename T> __device__ __forceinline__ void unpack_held(Held<T> h, const LanePart<T>& p, bool live, int dim, float (&v)[16]) {
+  constexpr int E = LanePart<T>::E;
+#pragma unroll
+  for (int i = 0; i < LanePart<T>::P; ++i) {
+    const int n = live ? p.n[i] : 0;
+    if constexpr (RAG == kRagged && sizeof(T) == 2) settle8(h.r[i].r, n > 0 ? dim - p.c[i] : 0, dim);
+    float w[E];
+    h.r[i].get(w);
+#pragma unroll
+    for (int j = 0; j < E; ++j) v[E * i + j] = RAG != kRagged || j < n ? w[j] : 0.0f;
+  }
+}
+template <int RAG, typename T>
+__device__ __forceinline__ void store_held(T* row, const LanePart<T>& p, bool live, const float (&v)[16], bool stream) {
+  constexpr int E = LanePart<T>::E;
+#pragma unroll
+  for (int i = 0; i < LanePart<T>::P; ++i) {
+    const int n = live ? p.n[i] : 0;
+    float w[E];
+#pragma unroll
+    for (int j = 0; j < E; ++j) w[j] = v[E * i + j];
+    Piece<T>::store(row + p.c[i], RAG == kRagged ? n : (n > 0 ? E : 0), w, stream);
   }
 }
 
-// gamma, in fp32 whatever it is stored in; 1 if null.
-__device__ __forceinline__ void load_gamma(const void* gamma, bool bf16, int col, int n, float (&v)[8]) {
-  if (!gamma) {
+// N consecutive elements at p, of which n exist.
+template <int N> __device__ __forceinline__ void load_run(const float* p, int n, float* v) {
+  if constexpr (N == 2) {
+    if (n >= 2) {
+      const f32x2 w = *(const f32x2_u*)p;
+      v[0] = w[0];
+      v[1] = w[1];
+    } else {
+      v[0] = n > 0 ? *p : 0.0f;
+      v[1] = 0.0f;
+    }
+  } else if constexpr (N == 4) {
+    Piece<float> w;
+    float u[4];
+    w.load<false>(p, n);
+    w.get(u);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) v[j] = 1.0f;
-  } else if (bf16) {
-    unpack8(load8((const uint16_t*)gamma + col, n), v);
+    for (int j = 0; j < 4; ++j) v[j] = u[j];
   } else {
-    unpack8(load8((const float*)gamma + col, n), v);
+    float u[8];
+    unpack8(load8(p, n), u);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = u[j];
+  }
+}
+template <int N> __device__ __forceinline__ void load_run(const uint16_t* p, int n, float* v) {
+  float u[8];
+  unpack8(load8(p, N == 8 ? n : n < N ? n : N), u);
+#pragma unroll
+  for (int j = 0; j < N; ++j) v[j] = u[j];
+}
+
+// gamma, in fp32 whatever it is stored in; 1 if null.
+template <typename T> __device__ __forceinline__ void load_gamma(const void* gamma, bool bf16, const LanePart<T>& p, float (&v)[16]) {
+  constexpr int E = LanePart<T>::E;
+#pragma unroll
+  for (int i = 0; i < LanePart<T>::P; ++i) {
+    if (!gamma) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[E * i + j] = 1.0f;
+    } else if (bf16) {
+      load_run<E>((const uint16_t*)gamma + p.c[i], p.n[i], v + E * i);
+    } else {
+      load_run<E>((const float*)gamma + p.c[i], p.n[i], v + E * i);
+    }
   }
 }
 
@@ -95,162 +161,134 @@ __device__ __forceinline__ Place place(const HeadRows& h, uint32_t r) {
   return {at(h.s_x), at(h.s_dy), at(h.s_out), at(h.s_pos)};
 }
 
-// The angles of a row for one lane.
-struct Angles {
-  Raw8<float> c, s;
-  int n;
+// The angles of a lane's 8 pairs, in runs that lie apart like its pieces.
+template <typename T, bool INTER> struct Angles {
+  static constexpr int LEN = INTER ? Piece<T>::N / 2 : Piece<T>::N, RUNS = 8 / LEN;
+  float c[8], s[8];
+  int n[RUNS];
 };
-template <bool RAG>
-__device__ __forceinline__ Angles load_angles(const HeadArgs& a, int64_t pos, int t, int n) {
-  Angles r;
+template <int RAG, typename T, bool INTER>
+__device__ __forceinline__ void load_angles(const HeadArgs& a, int64_t pos, const LanePart<T>& p, bool live, Angles<T, INTER>& g) {
+  constexpr int LEN = Angles<T, INTER>::LEN;
   const int half = a.rot / 2;
-  const int64_t row = n > 0 && a.positions ? a.positions[pos] : pos;
-  r.n = uint64_t(row) < uint64_t(a.table_rows) ? n : 0;
-  r.c = load_part<RAG>(a.cos + row * half, 8 * t, r.n, half);
-  r.s = load_part<RAG>(a.sin + row * half, 8 * t, r.n, half);
-  if constexpr (RAG) {
-    settle8(r.c, r.n > 0 ? half - 8 * t : 0, half);
-    settle8(r.s, r.n > 0 ? half - 8 * t : 0, half);
+  const bool turned = live && p.turned && half > 0;
+  const int64_t row = turned && a.positions ? a.positions[pos] : pos;
+  const bool in = turned && uint64_t(row) < uint64_t(a.table_rows);
+#pragma unroll
+  for (int i = 0; i < Angles<T, INTER>::RUNS; ++i) {
+    const int at = INTER ? p.c[i] / 2 : p.c[i];
+    int n = in ? some(half - at, LEN) : 0;
+    if constexpr (RAG == kWhole) n = n > 0 ? LEN : 0;
+    g.n[i] = n;
+    load_run<LEN>(a.cos + row * half + at, n, g.c + LEN * i);
+    load_run<LEN>(a.sin + row * half + at, n, g.s + LEN * i);
   }
-  return r;
 }
 
 // Turns a lane's elements by its angles, or back.
-template <bool INTER, bool RAG, bool BACK>
-__device__ __forceinline__ void turn(const Angles& g, float (&u)[8], float (&v)[8]) {
-  float c[8], s[8];
-  unpack8(g.c, c);
-  unpack8(g.s, s);
-  auto pair = [&](int j, float& a, float& b) {
-    const float w = BACK ? -s[j] : s[j];
-    const float x = fmaf(a, c[j], -(b * w)), y = fmaf(b, c[j], a * w);
-    a = x;
-    b = y;
-  };
-  auto one = [&](int j) {
-    if constexpr (!INTER) pair(j, u[j], v[j]);
-    else if (j < 4) pair(j, u[2 * j], u[2 * j + 1]);
-    else pair(j, v[2 * (j - 4)], v[2 * (j - 4) + 1]);
-  };
-  if (g.n == 8) {
+template <int RAG, bool BACK, typename T, bool INTER> __device__ __forceinline__ void turn(const Angles<T, INTER>& g, float (&v)[16]) {
+  constexpr int LEN = Angles<T, INTER>::LEN;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) one(j);
-  } else if (g.n > 0) {
+  for (int i = 0; i < Angles<T, INTER>::RUNS; ++i) {
+    if (g.n[i] <= 0) continue;
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (j < g.n) one(j);
+    for (int j = 0; j < LEN; ++j) {
+      const int k = LEN * i + j;
+      if (RAG != kWhole && j >= g.n[i]) continue;
+      float &a = v[INTER ? 2 * k : k], &b = v[INTER ? 2 * k + 1 : k + 8];
+      const float s = BACK ? -g.s[k] : g.s[k];
+      const float x = fmaf(a, g.c[k], -(b * s)), y = fmaf(b, g.c[k], a * s);
+      a = x;
+      b = y;
+    }
   }
 }
 
-template <typename T, int LANES, bool INTER, bool RAG>
+template <typename T, int LANES, bool INTER, int RAG>
 __global__ __launch_bounds__(WG) void heads_fwd_kernel(HeadArgs a) {
   constexpr int ROWS = WG / LANES;
   const bool keys = int(blockIdx.x) >= a.q.wgs;
   const HeadRows& h = keys ? a.k : a.q;
   const uint32_t wg = keys ? blockIdx.x - a.q.wgs : blockIdx.x;
-  const int t = threadIdx.x % LANES;
-  const LanePart p = lane_part<INTER>(t, a.dim, a.rot);
+  const LanePart<T> p = lane_part<T, INTER>(threadIdx.x % LANES, a.dim, a.rot);
   const float inv = 1.0f / float(a.dim);
-  float ga[8], gb[8];
-  load_gamma(h.gamma, a.wbf16, p.c0, p.n0, ga);
-  load_gamma(h.gamma, a.wbf16, p.c1, p.n1, gb);
+  float gv[16];
+  load_gamma(h.gamma, a.wbf16, p, gv);
   for (uint64_t row = uint64_t(wg) * ROWS + threadIdx.x / LANES; row < h.rows; row += uint64_t(h.wgs) * ROWS) {
     const Place at = place(h, uint32_t(row));
-    const T* x = (const T*)h.x + at.x;
-    const Raw8<T> ra = load_part<RAG>(x, p.c0, p.n0, a.dim), rb = load_part<RAG>(x, p.c1, p.n1, a.dim);
-    const Angles ang = load_angles<RAG>(a, at.pos, t, p.nc);
-    float u[8], v[8];
-    unpack_part<RAG>(ra, p.c0, p.n0, a.dim, u);
-    unpack_part<RAG>(rb, p.c1, p.n1, a.dim, v);
+    Held<T> held;
+    Angles<T, INTER> ang;
+    load_held<RAG>((const T*)h.x + at.x, p, true, a.dim, held);
+    load_angles<RAG>(a, at.pos, p, true, ang);
+    float v[16];
+    unpack_held<RAG>(held, p, true, a.dim, v);
     float q = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) q = fmaf(u[j], u[j], q);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) q = fmaf(v[j], v[j], q);
+    for (int j = 0; j < 16; ++j) q = fmaf(v[j], v[j], q);
     q = lane_sum<LANES>(q);
     const float r = rsqrtf(fmaf(q, inv, a.eps));
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      u[j] = u[j] * r * ga[j];
-      v[j] = v[j] * r * gb[j];
-    }
-    turn<INTER, RAG, false>(ang, u, v);
-    T* out = (T*)h.out + at.out;
-    store_part<RAG>(out + p.c0, p.n0, pack8(u, (const T*)nullptr));
-    store_part<RAG>(out + p.c1, p.n1, pack8(v, (const T*)nullptr));
+    for (int j = 0; j < 16; ++j) v[j] = v[j] * r * gv[j];
+    turn<RAG, false>(ang, v);
+    store_held<RAG>((T*)h.out + at.out, p, true, v, a.stream_out);
   }
 }
 
-template <typename T, int LANES, bool INTER, bool RAG>
+template <typename T, int LANES, bool INTER, int RAG>
 __global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
   constexpr int ROWS = WG / LANES, WAVES = WG / 64;
   __shared__ float sums[WAVES][16 * LANES];
   const bool keys = int(blockIdx.x) >= a.q.wgs;
   const HeadRows& h = keys ? a.k : a.q;
   const uint32_t wg = keys ? blockIdx.x - a.q.wgs : blockIdx.x;
-  const int t = threadIdx.x % LANES;
-  const LanePart p = lane_part<INTER>(t, a.dim, a.rot);
+  const LanePart<T> p = lane_part<T, INTER>(threadIdx.x % LANES, a.dim, a.rot);
   const float inv = 1.0f / float(a.dim);
-  float ga[8], gb[8], da[8], db[8];
-  load_gamma(h.gamma, a.wbf16, p.c0, p.n0, ga);
-  load_gamma(h.gamma, a.wbf16, p.c1, p.n1, gb);
+  float gv[16], acc[16];
+  load_gamma(h.gamma, a.wbf16, p, gv);
 #pragma unroll
-  for (int j = 0; j < 8; ++j) da[j] = db[j] = 0.0f;
+  for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
   const uint64_t step = uint64_t(h.wgs) * ROWS;
   for (uint64_t row0 = uint64_t(wg) * ROWS; row0 < h.rows; row0 += step) {
     const uint64_t row = row0 + threadIdx.x / LANES;
     const bool live = row < h.rows;
     const Place at = place(h, live ? uint32_t(row) : h.rows - 1);
-    const int n0 = live ? p.n0 : 0, n1 = live ? p.n1 : 0;
-    const T *x = (const T*)h.x + at.x, *dy = (const T*)h.dy + at.dy;
-    const Raw8<T> xa = load_part<RAG>(x, p.c0, n0, a.dim), xb = load_part<RAG>(x, p.c1, n1, a.dim);
-    const Raw8<T> ya = load_part<RAG>(dy, p.c0, n0, a.dim), yb = load_part<RAG>(dy, p.c1, n1, a.dim);
-    const Angles ang = load_angles<RAG>(a, at.pos, t, live ? p.nc : 0);
-    float u[8], v[8], g[8], f[8];
-    unpack_part<RAG>(xa, p.c0, n0, a.dim, u);
-    unpack_part<RAG>(xb, p.c1, n1, a.dim, v);
-    unpack_part<RAG>(ya, p.c0, n0, a.dim, g);
-    unpack_part<RAG>(yb, p.c1, n1, a.dim, f);
-    turn<INTER, RAG, true>(ang, g, f);
+    Held<T> hx, hy;
+    Angles<T, INTER> ang;
+    load_held<RAG>((const T*)h.x + at.x, p, live, a.dim, hx);
+    load_held<RAG>((const T*)h.dy + at.dy, p, live, a.dim, hy);
+    load_angles<RAG>(a, at.pos, p, live, ang);
+    float x[16], g[16];
+    unpack_held<RAG>(hx, p, live, a.dim, x);
+    unpack_held<RAG>(hy, p, live, a.dim, g);
+    turn<RAG, true>(ang, g);
     float q = 0.0f, dot = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      q = fmaf(u[j], u[j], q);
-      dot = fmaf(g[j] * ga[j], u[j], dot);
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      q = fmaf(v[j], v[j], q);
-      dot = fmaf(f[j] * gb[j], v[j], dot);
+    for (int j = 0; j < 16; ++j) {
+      q = fmaf(x[j], x[j], q);
+      dot = fmaf(g[j] * gv[j], x[j], dot);
     }
     q = lane_sum<LANES>(q);
     dot = lane_sum<LANES>(dot);
     const float r = rsqrtf(fmaf(q, inv, a.eps)), c = dot * r * inv;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float xu = u[j] * r, xv = v[j] * r;
-      da[j] = fmaf(g[j], xu, da[j]);
-      db[j] = fmaf(f[j], xv, db[j]);
-      u[j] = r * fmaf(-xu, c, g[j] * ga[j]);
-      v[j] = r * fmaf(-xv, c, f[j] * gb[j]);
+    for (int j = 0; j < 16; ++j) {
+      const float xh = x[j] * r;
+      acc[j] = fmaf(g[j], xh, acc[j]);
+      x[j] = r * fmaf(-xh, c, g[j] * gv[j]);
     }
-    T* out = (T*)h.out + at.out;
-    store_part<RAG>(out + p.c0, n0, pack8(u, (const T*)nullptr));
-    store_part<RAG>(out + p.c1, n1, pack8(v, (const T*)nullptr));
+    store_held<RAG>((T*)h.out + at.out, p, live, x, a.stream_out);
   }
   if (!h.dgamma) return;
   // the rows of a wave across its lanes, the waves in order
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    da[j] = across_groups<LANES>(da[j]);
-    db[j] = across_groups<LANES>(db[j]);
-  }
+  for (int j = 0; j < 16; ++j) acc[j] = across_groups<LANES>(acc[j]);
   if ((threadIdx.x & 63) < LANES) {
+    constexpr int E = LanePart<T>::E;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if (j < p.n0) sums[threadIdx.x / 64][p.c0 + j] = da[j];
-      if (j < p.n1) sums[threadIdx.x / 64][p.c1 + j] = db[j];
-    }
+    for (int i = 0; i < LanePart<T>::P; ++i)
+#pragma unroll
+      for (int j = 0; j < E; ++j)
+        if (j < p.n[i]) sums[threadIdx.x / 64][p.c[i] + j] = acc[E * i + j];
   }
   __syncthreads();
   for (int c = threadIdx.x; c < a.dim; c += WG) {
@@ -263,22 +301,32 @@ __global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
   }
 }
 
-// Joins the workgroups' sums: 32 columns a workgroup, 32 slices of the parts,
-// joined in order; blockIdx.y 0 for queries, 1 for keys.
-constexpr int kCols = 32, kSlices = 32;
+// Joins the workgroups' sums: 16 columns a workgroup, 64 slices of the at most
+// 1024 parts, whose at most 16 loads are in flight at once; the slices of a wave
+// are joined across its lanes, the waves in order.  blockIdx.y 0 for queries, 1
+// for keys.
+constexpr int kCols = 16, kSlices = 64;
 __global__ __launch_bounds__(kCols* kSlices) void heads_gain_kernel(HeadArgs a) {
-  __shared__ float sums[kSlices][kCols];
+  constexpr int EACH = (kHeadMaxParts + kSlices - 1) / kSlices, WAVES = kCols * kSlices / 64;
+  __shared__ float sums[WAVES][kCols];
   const HeadRows& h = blockIdx.y ? a.k : a.q;
   if (!h.dgamma || !h.part) return;
   const int lane = threadIdx.x % kCols, slice = threadIdx.x / kCols, c = int(blockIdx.x) * kCols + lane;
-  float s = 0.0f;
-#pragma unroll 8
-  for (int p = slice; p < h.wgs; p += kSlices) s += c < a.dim ? h.part[int64_t(p) * a.dim + c] : 0.0f;
-  sums[slice][lane] = s;
-  __syncthreads();
-  if (slice == 0 && c < a.dim) {
+  float v[EACH];
 #pragma unroll
-    for (int i = 1; i < kSlices; ++i) s += sums[i][lane];
+  for (int i = 0; i < EACH; ++i) {
+    const int p = slice + kSlices * i;
+    v[i] = c < a.dim && p < h.wgs ? h.part[int64_t(p) * a.dim + c] : 0.0f;
+  }
+  float s = v[0];
+#pragma unroll
+  for (int i = 1; i < EACH; ++i) s += v[i];
+  s = across_groups<kCols>(s);
+  if ((threadIdx.x & 63) < kCols) sums[threadIdx.x / 64][lane] = s;
+  __syncthreads();
+  if (threadIdx.x < kCols && c < a.dim) {
+#pragma unroll
+    for (int i = 1; i < WAVES; ++i) s += sums[i][lane];
     if (a.wbf16) Elem<uint16_t>::store((uint16_t*)h.dgamma + c, s);
     else Elem<float>::store((float*)h.dgamma + c, s);
   }
@@ -305,14 +353,25 @@ template <typename F> hipError_t by_kind(const HeadArgs& a, bool bf16, bool inte
       default: f(t, in, rag, std::integral_constant<int, 64>{});
     }
   };
-  // whole vectors only: the halves' and the rest's lengths are multiples of 8
-  const bool rag = a.dim % 8 != 0 || (!inter && a.rot / 2 % 8 != 0) || (inter && a.rot % 16 != 0);
+  typedef std::integral_constant<int, kWhole> Whole;
+  typedef std::integral_constant<int, kRaggedAngles> RaggedAngles;
+  typedef std::integral_constant<int, kRagged> AllRagged;
+  const int half = a.rot / 2;
   auto kind = [&](auto t) {
-    if (inter) rag ? lanes(t, std::true_type{}, std::true_type{}) : lanes(t, std::true_type{}, std::false_type{});
-    else rag ? lanes(t, std::false_type{}, std::true_type{}) : lanes(t, std::false_type{}, std::false_type{});
+    constexpr int E = Piece<decltype(t)>::N;
+    if (inter) {
+      if (a.dim % E != 0) lanes(t, std::true_type{}, AllRagged{});
+      else half % (E / 2) != 0 ? lanes(t, std::true_type{}, RaggedAngles{}) : lanes(t, std::true_type{}, Whole{});
+    } else {
+      a.dim % E != 0 || half % E != 0 ? lanes(t, std::false_type{}, AllRagged{}) : lanes(t, std::false_type{}, Whole{});
+    }
   };
   bf16 ? kind(uint16_t{}) : kind(float{});
   return hipGetLastError();
+}
+
+bool streams(const HeadArgs& a, int64_t size) {
+  return (int64_t(a.q.rows) + a.k.rows) * a.dim * size > kStreamOut;
 }
 
 }  // namespace
@@ -324,12 +383,15 @@ hipError_t run_heads_fwd(const HeadArgs& args, bool bf16, bool interleaved, hipS
     auto need = [](uint32_t rows) { return int(std::min<int64_t>((int64_t(rows) + ROWS - 1) / ROWS, kOpsMaxGrid)); };
     a.q.wgs = need(a.q.rows);
     a.k.wgs = need(a.k.rows);
+    a.stream_out = streams(a, sizeof(t));
     hipLaunchKernelGGL((heads_fwd_kernel<decltype(t), L, decltype(inter)::value, decltype(rag)::value>),
                        dim3(unsigned(a.q.wgs + a.k.wgs)), dim3(WG), 0, st, a);
   });
 }
 
-hipError_t run_heads_bwd(const HeadArgs& a, bool bf16, bool interleaved, hipStream_t st) {
+hipError_t run_heads_bwd(const HeadArgs& args, bool bf16, bool interleaved, hipStream_t st) {
+  HeadArgs a = args;
+  a.stream_out = streams(a, bf16 ? 2 : 4);
   if (a.q.rows + a.k.rows == 0) {
     hipLaunchKernelGGL(heads_zero_kernel, dim3(1), dim3(WG), 0, st, a);
     return hipGetLastError();

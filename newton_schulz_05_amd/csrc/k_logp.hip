@@ -60,11 +60,11 @@ __device__ __forceinline__ void put_row(const LogpArgs& a, int64_t row, MaxSum r
   a.lse[row] = lse;
 }
 
-// NT threads take a row, or with a.parts > 1 every a.parts-th run of vectors of
-// it; U vectors of 8 elements a thread are in flight at once.
-template <typename T, int NT, int WG, int U>
+// NT threads take a row, or with a.parts > 1 every a.parts-th run of pieces of
+// it; U pieces a thread are in flight at once.
+template <typename T, int NT, int WG, int U, bool STREAM>
 __global__ __launch_bounds__(WG) void logp_fwd_kernel(LogpArgs a) {
-  constexpr int ROWS = WG / NT, NW = NT / 64;
+  constexpr int ROWS = WG / NT, NW = NT / 64, N = Piece<T>::N;
   __shared__ MaxSum waves[WG / 64];
   const int t = threadIdx.x % NT;
   const int part = int(blockIdx.x) % a.parts;
@@ -78,36 +78,37 @@ __global__ __launch_bounds__(WG) void logp_fwd_kernel(LogpArgs a) {
     const T* x = (const T*)a.logits + (live ? row : 0) * a.ld;
     const float xt = some ? Elem<T>::load(x + target) : 0.0f;
     MaxSum mine{-INFINITY, 0.0f};
-    if (some) {
+    if (some) {  // a row without a target is not read
       const int cols = int(a.cols), at = int(target);
-      for (int col0 = part * NT * 8 * U; col0 < cols; col0 += a.parts * NT * 8 * U) {
-        Raw8<T> raw[U];
-        float v[U][8];
+      for (int col0 = part * NT * N * U; col0 < cols; col0 += a.parts * NT * N * U) {
+        Piece<T> raw[U];
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          const int col = col0 + (i * NT + t) * 8;
-          raw[i] = load8(x + col, cols - col);
+          const int col = col0 + (i * NT + t) * N;
+          raw[i].template load<STREAM>(x + col, cols - col);
         }
 #pragma unroll
         for (int i = 0; i < U; ++i) {
-          const int col = col0 + (i * NT + t) * 8;
-          unpack8(raw[i], v[i]);
-          if (col + 8 > cols || unsigned(at - col) < 8u) {
+          const int col = col0 + (i * NT + t) * N;
+          float v[N];
+          raw[i].get(v);
+          if (col + N > cols || unsigned(at - col) < unsigned(N)) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[i][j] = col + j < cols && col + j != at ? v[i][j] : -INFINITY;
+            for (int j = 0; j < N; ++j) v[j] = col + j < cols && col + j != at ? v[j] : -INFINITY;
           }
-          add_block(mine, v[i], c);
+          add_block(mine, v, c);
         }
       }
     }
     mine = lanes_join<64>(mine, c);
     if constexpr (NW > 1) {
+      const int first = threadIdx.x / NT * NW;
       __syncthreads();
       if (threadIdx.x % 64 == 0) waves[threadIdx.x / 64] = mine;
       __syncthreads();
-      mine = waves[threadIdx.x / NT * NW];
+      mine = waves[first];
 #pragma unroll
-      for (int w = 1; w < NW; ++w) mine = join(mine, waves[threadIdx.x / NT * NW + w], c);
+      for (int w = 1; w < NW; ++w) mine = join(mine, waves[first + w], c);
     }
     if (t == 0 && live) {
       if (a.parts == 1) {
@@ -139,84 +140,96 @@ __global__ __launch_bounds__(64) void logp_join_kernel(LogpArgs a, bool bf16) {
   if (lane == 0) put_row(a, row, mine, some, xt);
 }
 
-// NT threads take 8 U NT elements of a row; blockIdx.x counts these along it,
+// NT threads take U NT pieces of a row; blockIdx.x counts these along it,
 // blockIdx.y the rows.
-template <typename T, int NT, int WG, int U>
+template <typename T, int NT, int WG, int U, bool STREAM>
 __global__ __launch_bounds__(WG) void logp_bwd_kernel(LogpBwdArgs a) {
-  constexpr int ROWS = WG / NT;
+  constexpr int ROWS = WG / NT, N = Piece<T>::N;
   const int t = threadIdx.x % NT;
-  const int cols = int(a.cols), col0 = int(blockIdx.x) * (NT * 8 * U) + t * 8;
+  const int cols = int(a.cols), col0 = int(blockIdx.x) * (NT * N * U) + t * N;
   for (int64_t row = int64_t(blockIdx.y) * ROWS + threadIdx.x / NT; row < a.rows; row += int64_t(gridDim.y) * ROWS) {
     const int64_t target = a.targets[row];
-    const float lse = a.lse[row], g = a.dlogp[row] * a.scale;
-    const bool some = uint64_t(target) < uint64_t(a.cols) && a.dlogp[row] != 0.0f && lse != -INFINITY;
+    const float lse = a.lse[row], up = a.dlogp[row], g = up * a.scale;
+    const bool some = uint64_t(target) < uint64_t(a.cols) && up != 0.0f && lse != -INFINITY;
     const T* x = (const T*)a.logits + row * a.ld;
     T* out = (T*)a.dlogits + row * a.ld_d;
     if (!some) {
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int col = col0 + i * NT * 8;
-        const float zero[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-        store8(out + col, cols - col, pack8(zero, (const T*)nullptr));
+        const int col = col0 + i * NT * N;
+        const float zero[N] = {};
+        Piece<T>::store(out + col, cols - col, zero, a.stream_out);
       }
       continue;
     }
-    Raw8<T> raw[U];
+    Piece<T> raw[U];
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int col = col0 + i * NT * 8;
-      raw[i] = load8(x + col, cols - col);
+      const int col = col0 + i * NT * N;
+      raw[i].template load<STREAM>(x + col, cols - col);
     }
+    const int at = int(target);
 #pragma unroll
     for (int i = 0; i < U; ++i) {
-      const int col = col0 + i * NT * 8;
-      float v[8];
-      unpack8(raw[i], v);
+      const int col = col0 + i * NT * N;
+      float v[N];
+      raw[i].get(v);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = -g * __builtin_amdgcn_exp2f(fmaf(v[j], a.scale, -lse) * 1.44269504f);
-      if (uint64_t(target - col) < 8) {
+      for (int j = 0; j < N; ++j) v[j] = -g * __builtin_amdgcn_exp2f(fmaf(v[j], a.scale, -lse) * 1.44269504f);
+      if (unsigned(at - col) < unsigned(N)) {
         const float own = -g * expm1f(a.logp[row]);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = col + j == target ? own : v[j];
+        for (int j = 0; j < N; ++j) v[j] = col + j == at ? own : v[j];
       }
-      store8(out + col, cols - col, pack8(v, (const T*)nullptr));
+      Piece<T>::store(out + col, cols - col, v, a.stream_out);
     }
   }
 }
+
+template <int V> using Num = std::integral_constant<int, V>;
+template <bool V> using Flag = std::integral_constant<bool, V>;
 
 }  // namespace
 
 hipError_t run_logp_fwd(const LogpArgs& a, bool bf16, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
-  auto go = [&](auto t, auto nt, auto wg, auto u) {
-    constexpr int NT = decltype(nt)::value, WG = decltype(wg)::value;
+  auto go = [&](auto t, auto nt, auto u, auto stream) {
+    constexpr int NT = decltype(nt)::value, WG = 256;
     const int64_t groups = (a.rows + WG / NT - 1) / (WG / NT);
-    hipLaunchKernelGGL((logp_fwd_kernel<decltype(t), NT, WG, decltype(u)::value>),
+    hipLaunchKernelGGL((logp_fwd_kernel<decltype(t), NT, WG, decltype(u)::value, decltype(stream)::value>),
                        dim3(unsigned(std::min(groups, kOpsMaxGrid) * a.parts)), dim3(WG), 0, st, a);
   };
   auto by_cols = [&](auto t) {
-    typedef std::integral_constant<int, 64> I64;
-    typedef std::integral_constant<int, 256> I256;
-    if (a.cols <= 2048) go(t, I64{}, I256{}, std::integral_constant<int, 1>{});
-    else go(t, I256{}, I256{}, std::integral_constant<int, 4>{});
+    // A wave a row where rows are short or there are many of them: what lanes and
+    // pieces behind a row's end cost, and a workgroup's barriers, are most of it
+    // there (30000 x 500 bf16 18.8 us, 34.6 with two waves a row of two pieces,
+    // 61.0 with four; 8192 x 5000 19.0, 22.5, 28.2; 16384 x 2000 fp32 30.1, 28.4,
+    // 32.0; but 600 x 5000 6.3, 5.7, 5.5).  Longer rows: four waves of four pieces
+    // (4096 x 32768 bf16 54.0 us, 57.5 with a wave; 4096 x 131072 171 and 180).
+    const bool many = a.rows >= 4096;
+    if (a.cols <= 64 * Piece<decltype(t)>::N || (a.cols <= 2048 && !many)) go(t, Num<64>{}, Num<1>{}, Flag<false>{});
+    else if (a.cols <= 1024 * Piece<decltype(t)>::N && many) go(t, Num<64>{}, Num<2>{}, Flag<false>{});
+    else if (a.rows * a.cols * int64_t(sizeof(t)) > kStreamIn) go(t, Num<256>{}, Num<4>{}, Flag<true>{});
+    else go(t, Num<256>{}, Num<4>{}, Flag<false>{});
   };
   bf16 ? by_cols(uint16_t{}) : by_cols(float{});
   if (a.parts > 1) hipLaunchKernelGGL(logp_join_kernel, dim3(unsigned(a.rows)), dim3(64), 0, st, a, bf16);
   return hipGetLastError();
 }
 
-hipError_t run_logp_bwd(const LogpBwdArgs& a, bool bf16, hipStream_t st) {
-  auto go = [&](auto t, auto nt, auto wg, auto u) {
-    constexpr int NT = decltype(nt)::value, WG = decltype(wg)::value, U = decltype(u)::value;
-    const int64_t runs = (a.cols + NT * 8 * U - 1) / (NT * 8 * U), groups = (a.rows + WG / NT - 1) / (WG / NT);
-    hipLaunchKernelGGL((logp_bwd_kernel<decltype(t), NT, WG, U>), dim3(unsigned(runs), unsigned(std::min<int64_t>(groups, 65535))),
-                       dim3(WG), 0, st, a);
+hipError_t run_logp_bwd(const LogpBwdArgs& args, bool bf16, hipStream_t st) {
+  LogpBwdArgs a = args;
+  a.stream_out = a.rows * a.cols * (bf16 ? 2 : 4) > kStreamOut;
+  auto go = [&](auto t, auto nt, auto u, auto stream) {
+    constexpr int NT = decltype(nt)::value, WG = 256, U = decltype(u)::value, RUN = NT * Piece<decltype(t)>::N * U;
+    const int64_t runs = (a.cols + RUN - 1) / RUN, groups = (a.rows + WG / NT - 1) / (WG / NT);
+    hipLaunchKernelGGL((logp_bwd_kernel<decltype(t), NT, WG, U, decltype(stream)::value>),
+                       dim3(unsigned(runs), unsigned(std::min<int64_t>(groups, 65535))), dim3(WG), 0, st, a);
   };
   auto by_cols = [&](auto t) {
-    typedef std::integral_constant<int, 64> I64;
-    typedef std::integral_constant<int, 256> I256;
-    if (a.cols <= 2048) go(t, I64{}, I256{}, std::integral_constant<int, 1>{});
-    else go(t, I256{}, I256{}, std::integral_constant<int, 4>{});
+    if (a.cols <= 256 * Piece<decltype(t)>::N) go(t, Num<64>{}, Num<1>{}, Flag<false>{});
+    else if (a.rows * a.cols * int64_t(sizeof(t)) > kStreamIn) go(t, Num<256>{}, Num<4>{}, Flag<true>{});
+    else go(t, Num<256>{}, Num<4>{}, Flag<false>{});
   };
   bf16 ? by_cols(uint16_t{}) : by_cols(float{});
   return hipGetLastError();

@@ -11,33 +11,41 @@ namespace muon {
 
 namespace {
 
-template <int WG> __device__ __forceinline__ double block_sum(double v, double* red) {
-  for (int d = 32; d >= 1; d >>= 1) v += __shfl_xor(v, d, 64);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x / 64] = v;
-  __syncthreads();
-  double s = red[0];
+// Sums of N values over a workgroup, in a fixed order; in every thread.
+template <int WG, int N> __device__ __forceinline__ void block_sum(double (&v)[N], double (*red)[N]) {
+  for (int d = 32; d >= 1; d >>= 1) {
 #pragma unroll
-  for (int w = 1; w < WG / 64; ++w) s += red[w];
-  return s;
+    for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], d, 64);
+  }
+  if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) red[threadIdx.x / 64][i] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = red[0][i];
+#pragma unroll
+    for (int w = 1; w < WG / 64; ++w) v[i] += red[w][i];
+  }
 }
 
 // ---- policy loss ---------------------------------------------------------------
 
-__device__ __forceinline__ void put_policy(const PolicyArgs& a, double pg, double kl, double cut) {
-  a.loss[0] = float(pg + a.beta * kl);
+// Policy sum, KL sum and the weight of the clipped tokens.
+__device__ __forceinline__ void put_policy(const PolicyArgs& a, const double (&s)[3]) {
+  a.loss[0] = float(s[0] + a.beta * s[1]);
   if (a.terms) {
-    a.terms[0] = float(pg);
-    a.terms[1] = float(kl);
-    a.terms[2] = float(cut);
+#pragma unroll
+    for (int i = 0; i < 3; ++i) a.terms[i] = float(s[i]);
   }
 }
 
 constexpr int kPolicyThreads = 1024;
 __global__ __launch_bounds__(kPolicyThreads) void policy_kernel(PolicyArgs a) {
-  __shared__ double red[kPolicyThreads / 64];
+  __shared__ double red[kPolicyThreads / 64][3];
   const double up = a.dloss ? double(a.dloss[0]) : 1.0;
-  double sum_pg = 0.0, sum_kl = 0.0, sum_cut = 0.0;
+  double sum[3] = {0.0, 0.0, 0.0};
   for (int64_t i = int64_t(blockIdx.x) * kPolicyThreads + threadIdx.x; i < a.tokens;
        i += int64_t(gridDim.x) * kPolicyThreads) {
     const double w = a.weight ? double(a.weight[i]) : 1.0, lp = a.logp[i], adv = a.adv[i];
@@ -47,34 +55,29 @@ __global__ __launch_bounds__(kPolicyThreads) void policy_kernel(PolicyArgs a) {
     const double gain = adv == 0.0 ? 0.0 : adv * exp(d), e = a.ref ? expm1(u) : 0.0;
     const double pg = cut ? -adv * (adv > 0.0 ? a.high : a.low) : -gain;
     if (w != 0.0) {
-      sum_pg += w * pg;
-      sum_kl += w * (e - u);
-      sum_cut += cut ? w : 0.0;
+      sum[0] += w * pg;
+      sum[1] += w * (e - u);
+      sum[2] += cut ? w : 0.0;
     }
     if (a.dlogp) a.dlogp[i] = w != 0.0 ? float(up * w * ((cut ? 0.0 : -gain) - a.beta * e)) : 0.0f;
   }
-  sum_pg = block_sum<kPolicyThreads>(sum_pg, red);
-  sum_kl = block_sum<kPolicyThreads>(sum_kl, red);
-  sum_cut = block_sum<kPolicyThreads>(sum_cut, red);
+  block_sum<kPolicyThreads>(sum, red);
   if (threadIdx.x != 0) return;
   if (a.parts == 1) {
-    put_policy(a, sum_pg, sum_kl, sum_cut);
+    put_policy(a, sum);
   } else {
-    double* to = a.part + int64_t(blockIdx.x) * 3;
-    to[0] = sum_pg;
-    to[1] = sum_kl;
-    to[2] = sum_cut;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) a.part[int64_t(blockIdx.x) * 3 + i] = sum[i];
   }
 }
 
 __global__ __launch_bounds__(kPolicyMaxParts) void policy_join_kernel(PolicyArgs a) {
-  __shared__ double red[kPolicyMaxParts / 64];
-  const bool have = int(threadIdx.x) < a.parts;
-  const double* from = a.part + threadIdx.x * 3;
-  const double pg = block_sum<kPolicyMaxParts>(have ? from[0] : 0.0, red);
-  const double kl = block_sum<kPolicyMaxParts>(have ? from[1] : 0.0, red);
-  const double cut = block_sum<kPolicyMaxParts>(have ? from[2] : 0.0, red);
-  if (threadIdx.x == 0) put_policy(a, pg, kl, cut);
+  __shared__ double red[kPolicyMaxParts / 64][3];
+  double sum[3];
+#pragma unroll
+  for (int i = 0; i < 3; ++i) sum[i] = int(threadIdx.x) < a.parts ? a.part[threadIdx.x * 3 + i] : 0.0;
+  block_sum<kPolicyMaxParts>(sum, red);
+  if (threadIdx.x == 0) put_policy(a, sum);
 }
 
 // ---- preference loss -------------------------------------------------------------
@@ -92,73 +95,131 @@ __device__ __forceinline__ Run run_of(const PrefArgs& a, int64_t s, int c) {
   return {b + from, b + (from + each < n ? from + each : n)};
 }
 
+// Four tokens at i (those before n), 0 behind.
+__device__ __forceinline__ f32x4 load4(const float* p, int64_t i, int64_t n) {
+  if (i + 4 <= n) return *(const f32x4_u*)(p + i);
+  f32x4 v{0, 0, 0, 0};
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (i + j < n) v[j] = p[i + j];
+  return v;
+}
+__device__ __forceinline__ bool counts(const PrefArgs& a, int64_t i) { return !a.valid || a.valid[i] != 0; }
+
 __global__ __launch_bounds__(kPrefThreads) void pref_sum_kernel(PrefArgs a) {
-  __shared__ double red[kPrefThreads / 64];
+  __shared__ double red[kPrefThreads / 64][2];
   const int64_t s = blockIdx.x;
   const Run r = run_of(a, s, int(blockIdx.y));
-  double sum = 0.0, count = 0.0;
-  for (int64_t i = r.from + threadIdx.x; i < r.to; i += kPrefThreads) {
-    const bool in = !a.valid || a.valid[i] != 0;
-    if (in) {
-      sum += a.ref ? double(a.logp[i]) - double(a.ref[i]) : double(a.logp[i]);
-      count += 1.0;
-    }
+  double sum[2] = {0.0, 0.0};  // and the number of tokens
+  for (int64_t i = r.from + threadIdx.x * 4; i < r.to; i += kPrefThreads * 4) {
+    const f32x4 x = load4(a.logp, i, r.to), y = a.ref ? load4(a.ref, i, r.to) : f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (i + j < r.to && counts(a, i + j)) {
+        sum[0] += double(x[j]) - double(y[j]);
+        sum[1] += 1.0;
+      }
   }
-  sum = block_sum<kPrefThreads>(sum, red);
-  count = block_sum<kPrefThreads>(count, red);
+  block_sum<kPrefThreads>(sum, red);
   if (threadIdx.x == 0) {
     double* to = a.part + (s * a.chunks + blockIdx.y) * 2;
-    to[0] = sum;
-    to[1] = count;
+    to[0] = sum[0];
+    to[1] = sum[1];
   }
 }
 
-// Reward of a sequence and what multiplies a token's gradient.
+// Reward of a sequence and what multiplies a token's gradient, from the sum and
+// the number of its tokens.
 struct Reward {
   double r, share;
 };
-__device__ __forceinline__ Reward reward(const PrefArgs& a, int64_t s) {
-  double sum = 0.0, count = 0.0;
-  for (int c = 0; c < a.chunks; ++c) {
-    sum += a.part[(s * a.chunks + c) * 2];
-    count += a.part[(s * a.chunks + c) * 2 + 1];
-  }
+__device__ __forceinline__ Reward reward(const PrefArgs& a, double sum, double count) {
   const double share = a.average ? (count > 0.0 ? a.beta / count : 0.0) : a.beta;
   return {share * sum, share};
+}
+// A pair's rewards: by one thread, or by a wave with a chunk a lane (in every
+// lane; 64 chunks one after the other took 5 us of a workgroup).
+struct Pair {
+  Reward x, y;
+  double m, w;
+};
+template <bool WAVE> __device__ __forceinline__ Pair pair_of(const PrefArgs& a, int64_t i) {
+  double s[4] = {0.0, 0.0, 0.0, 0.0};
+  const double *p = a.part + i * a.chunks * 2, *q = a.part + (a.pairs + i) * a.chunks * 2;
+  auto add = [&](int c) {
+    s[0] += p[2 * c];
+    s[1] += p[2 * c + 1];
+    s[2] += q[2 * c];
+    s[3] += q[2 * c + 1];
+  };
+  if constexpr (WAVE) {
+    static_assert(kPrefMaxChunks == 64);
+    const int lane = threadIdx.x & 63;
+    if (lane < a.chunks) add(lane);
+    for (int d = 32; d >= 1; d >>= 1) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) s[k] += __shfl_xor(s[k], d, 64);
+    }
+  } else {
+    for (int c = 0; c < a.chunks; ++c) add(c);
+  }
+  Pair r;
+  r.x = reward(a, s[0], s[1]);
+  r.y = reward(a, s[2], s[3]);
+  r.m = r.x.r - r.y.r - a.margin;
+  r.w = a.weight ? double(a.weight[i]) : 1.0 / double(a.pairs);
+  return r;
 }
 
 // log(1 + e^x)
 __device__ __forceinline__ double softplus(double x) { return (x > 0.0 ? x : 0.0) + log1p(exp(-fabs(x))); }
 
-__global__ __launch_bounds__(kPrefThreads) void pref_grad_kernel(PrefArgs a) {
-  __shared__ double red[kPrefThreads / 64];
-  if (int64_t(blockIdx.x) == 2 * a.pairs) {  // the loss
-    if (blockIdx.y != 0) return;
-    double loss = 0.0;
-    for (int64_t i = threadIdx.x; i < a.pairs; i += kPrefThreads) {
-      const Reward x = reward(a, i), y = reward(a, a.pairs + i);
-      const double m = x.r - y.r - a.margin, w = a.weight ? double(a.weight[i]) : 1.0 / double(a.pairs);
-      if (w != 0.0) loss += w * ((1.0 - a.smoothing) * softplus(-m) + a.smoothing * softplus(m));
-      if (a.rewards) {
-        a.rewards[i] = float(x.r);
-        a.rewards[a.pairs + i] = float(y.r);
-      }
+// The loss, by one workgroup; a pair's rewards come with it.
+template <bool WAVE> __device__ __forceinline__ void pref_loss(const PrefArgs& a, double (*red)[1]) {
+  constexpr int EACH = WAVE ? 64 : 1;
+  const bool first = threadIdx.x % EACH == 0;
+  double loss[1] = {0.0};
+  for (int64_t i = threadIdx.x / EACH; i < a.pairs; i += kPrefThreads / EACH) {
+    const Pair p = pair_of<WAVE>(a, i);
+    if (!first) continue;
+    if (p.w != 0.0) loss[0] += p.w * ((1.0 - a.smoothing) * softplus(-p.m) + a.smoothing * softplus(p.m));
+    if (a.rewards) {
+      a.rewards[i] = float(p.x.r);
+      a.rewards[a.pairs + i] = float(p.y.r);
     }
-    loss = block_sum<kPrefThreads>(loss, red);
-    if (threadIdx.x == 0) a.loss[0] = float(loss);
+  }
+  block_sum<kPrefThreads>(loss, red);
+  if (threadIdx.x == 0) a.loss[0] = float(loss[0]);
+}
+
+// A few chunks are added by one thread for each pair.
+constexpr int kFewChunks = 8;
+
+__global__ __launch_bounds__(kPrefThreads) void pref_grad_kernel(PrefArgs a) {
+  __shared__ double red[kPrefThreads / 64][1];
+  if (int64_t(blockIdx.x) == 2 * a.pairs) {
+    if (blockIdx.y != 0) return;
+    if (a.chunks <= kFewChunks) pref_loss<false>(a, red);
+    else pref_loss<true>(a, red);
     return;
   }
   const int64_t s = blockIdx.x, pair = s < a.pairs ? s : s - a.pairs;
   const Run r = run_of(a, s, int(blockIdx.y));
   if (!a.dlogp || r.from >= r.to) return;
-  const Reward x = reward(a, pair), y = reward(a, a.pairs + pair);
-  const double m = x.r - y.r - a.margin, w = a.weight ? double(a.weight[pair]) : 1.0 / double(a.pairs);
+  const Pair p = a.chunks <= kFewChunks ? pair_of<false>(a, pair) : pair_of<true>(a, pair);
   const double up = a.dloss ? double(a.dloss[0]) : 1.0;
   // d loss / d m = w (smoothing sigma(m) - (1 - smoothing) sigma(-m))
-  const double slope = w * (a.smoothing / (1.0 + exp(-m)) - (1.0 - a.smoothing) / (1.0 + exp(m)));
-  const float g = w != 0.0 ? float(up * slope * (s < a.pairs ? x.share : -y.share)) : 0.0f;
-  for (int64_t i = r.from + threadIdx.x; i < r.to; i += kPrefThreads)
-    a.dlogp[i] = !a.valid || a.valid[i] != 0 ? g : 0.0f;
+  const double slope = p.w * (a.smoothing / (1.0 + exp(-p.m)) - (1.0 - a.smoothing) / (1.0 + exp(p.m)));
+  const float g = p.w != 0.0 ? float(up * slope * (s < a.pairs ? p.x.share : -p.y.share)) : 0.0f;
+  for (int64_t i = r.from + threadIdx.x * 4; i < r.to; i += kPrefThreads * 4) {
+    if (i + 4 <= r.to && !a.valid) {
+      *(f32x4_u*)(a.dlogp + i) = f32x4{g, g, g, g};
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (i + j < r.to) a.dlogp[i + j] = counts(a, i + j) ? g : 0.0f;
+    }
+  }
 }
 
 }  // namespace

@@ -127,6 +127,7 @@ struct HeadArgs {
   int dim, rot;
   float eps;
   bool wbf16;
+  bool stream_out;           // outputs that the caches do not hold
 };
 
 struct LogpArgs {
@@ -149,6 +150,7 @@ struct LogpBwdArgs {
   const float* lse;
   const float* dlogp;
   void* dlogits;
+  bool stream_out;
 };
 
 struct PolicyArgs {

@@ -174,6 +174,64 @@ __device__ __forceinline__ void store8(float* p, int n, const Raw8<float>& r) {
   }
 }
 
+// 16 bytes of an output, past the caches if it is a stream (see kStreamOut).  The
+// empty statements keep the compiler from making one ordinary store of the two.
+__device__ __forceinline__ void put16(void* p, const u32x4& w, bool stream) {
+  if (stream) {
+    asm volatile("" ::: "memory");
+    __builtin_nontemporal_store(w, (u32x4_u*)p);
+    asm volatile("" ::: "memory");
+  } else {
+    *(u32x4_u*)p = w;
+  }
+}
+
+// 16 bytes of a row: what a lane reads and writes at a time, so that a wave's
+// accesses are adjacent in either type.
+template <typename T> struct Piece;
+template <> struct Piece<uint16_t> {
+  static constexpr int N = 8;
+  Raw8<uint16_t> r;
+  template <bool STREAM> __device__ __forceinline__ void load(const uint16_t* p, int n) {
+    if (STREAM && n >= 8) r.w = __builtin_nontemporal_load((const u32x4_u*)p);
+    else r = load8(p, n);
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const { unpack8(r, v); }
+  static __device__ __forceinline__ void store(uint16_t* p, int n, const float (&v)[8], bool stream) {
+    const Raw8<uint16_t> w = pack8(v, p);
+    if (n >= 8) put16(p, w.w, stream);
+    else store8(p, n, w);
+  }
+};
+template <> struct Piece<float> {
+  static constexpr int N = 4;
+  f32x4 r;
+  template <bool STREAM> __device__ __forceinline__ void load(const float* p, int n) {
+    r = f32x4{0, 0, 0, 0};
+    if (n >= 4) {
+      r = STREAM ? __builtin_nontemporal_load((const f32x4_u*)p) : *(const f32x4_u*)p;
+    } else if (n > 0) {
+      f32x2 two{0, 0};
+      float one = 0;
+      if (n & 2) two = *(const f32x2_u*)p;
+      if (n & 1) one = p[n & 2];
+      r = (n & 2) ? f32x4{two[0], two[1], one, 0} : f32x4{one, 0, 0, 0};
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[4]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = r[j];
+  }
+  static __device__ __forceinline__ void store(float* p, int n, const float (&v)[4], bool stream) {
+    if (n >= 4) {
+      put16(p, __builtin_bit_cast(u32x4, f32x4{v[0], v[1], v[2], v[3]}), stream);
+    } else if (n > 0) {
+      if (n & 2) *(f32x2_u*)p = f32x2{v[0], v[1]};
+      if (n & 1) p[n & 2] = v[n & 2];
+    }
+  }
+};
+
 // ---- reductions over groups of N adjacent lanes ---------------------------------
 // Every lane of the group ends with the result; the order of the operations
 // is fixed by the lane pattern.  Within 16 lanes by DPP (quad_perm, then

@@ -65,15 +65,24 @@ inline int64_t route_parts(int64_t rows, int64_t experts) {
   return rows <= 2 * per ? 1 : std::min<int64_t>((rows + per - 1) / per, most);
 }
 
+// ---- tensors that the caches do not hold ----
+// Inputs beyond kStreamIn bytes are read past the caches: the last-level cache
+// holds 256 MB, so that nobody finds them there again (logits of 8192 x 65536
+// bf16, forward 162 us against 185; but 8192 x 5000, which the backward pass
+// finds there, takes it 34 us instead of 29).  Outputs beyond kStreamOut bytes are
+// written past them.  With a copy of the output right behind the call: gradient
+// of 2048 x 32768 bf16 102 us against 118, 515 x 50021 fp32 70.6 and 70.8 (alone
+// 27.8 and 36.8), but 1536 x 32768 77 and 75, 1024 x 32768 56 and 47.
+constexpr int64_t kStreamIn = int64_t(256) << 20, kStreamOut = int64_t(96) << 20;
+
 // ---- norm and rotation of query and key heads ----
 constexpr int64_t kHeadMaxDim = 512;  // a head's row is held by at most one wave
 constexpr int64_t kHeadMaxRows = 0x7fffffff;
 constexpr int kHeadThreads = 256;
 
-// Lanes that share one head's row, each with two vectors of 8 elements.  Pairs
-// that lie rot / 2 apart are one lane's: the vectors of the first half of the
-// turned elements each with that of the second half, then the elements that are
-// not turned two vectors a lane.
+// Lanes that share one head's row, 16 elements each.  Pairs that lie rot / 2
+// apart are one lane's: 8 elements of the first half of the turned ones with
+// those of the second half, then the elements that are not turned, 16 a lane.
 inline int head_lanes(int dim, int rot, bool interleaved) {
   const int need = interleaved || rot == 0 ? (dim + 15) / 16 : (rot / 2 + 7) / 8 + (dim - rot + 15) / 16;
   int lanes = 4;
@@ -92,7 +101,7 @@ inline HeadSplit head_split(int64_t rows_q, int64_t rows_k) {
   const int64_t all = rows_q + rows_k, parts = std::min<int64_t>(kHeadMaxParts, (all + 63) / 64);
   HeadSplit s{0, 0};
   if (rows_k > 0) s.k = int(std::max<int64_t>(1, parts * rows_k / all));
-  if (rows_q > 0) s.q = int(std::max<int64_t>(1, parts - s.k));
+  if (rows_q > 0) s.q = int(std::max<int64_t>(1, parts - s.k));  // each at most kHeadMaxParts
   return s;
 }
 
@@ -117,7 +126,7 @@ inline int policy_parts(int64_t tokens) {
 // Workgroups that share one sequence of the preference loss.
 inline int pref_chunks(int64_t tokens, int64_t pairs) {
   const int64_t each = tokens / std::max<int64_t>(2 * pairs, 1);
-  return int(std::max<int64_t>(1, std::min<int64_t>((each + 2047) / 2048, kPrefMaxChunks)));
+  return int(std::max<int64_t>(1, std::min<int64_t>((each + 511) / 512, kPrefMaxChunks)));
 }
 
 }  // namespace muon

@@ -317,66 +317,82 @@ def route_backward(logits, indices, counts, n_tokens, dlogits, *, dgates=None, d
 
 
 @functools.lru_cache(maxsize=1024)
-def _head_strides(batch: int, token: int, head: int):
-    """(structure, its address) of a muon_head_strides."""
-    s = MuonHeadStrides(batch, token, head)
+def _head_strides(stride: Tuple[int, ...], dim: int):
+    """(structure, its address) of a muon_head_strides for a tensor's strides;
+    None where the last dimension is not contiguous."""
+    if stride[-1] != 1 and dim > 1:
+        return None
+    s = MuonHeadStrides(stride[0] if len(stride) == 4 else 0, stride[-3], stride[-2])
     return s, ctypes.addressof(s)
 
 
-def _heads(t: torch.Tensor, what: str, like: Optional[torch.Tensor] = None):
-    """Strides' structure of a tensor of heads, [batch, tokens, heads, dim] or
-    [tokens, heads, dim], that has to match `like`."""
-    shape, stride = t.shape, t.stride()
-    if like is not None:
-        if shape != like.shape:
-            raise MuonError(2, f"{what} has shape {tuple(shape)}, expected {tuple(like.shape)}")
-        if t.dtype is not like.dtype:
-            raise MuonError(3, f"{what} has dtype {t.dtype}, expected {like.dtype}")
-    if stride[-1] != 1 and shape[-1] > 1:
+def _heads(t: torch.Tensor, shape, dt: torch.dtype, what: str):
+    """Strides' structure of a tensor of heads of this shape and dtype."""
+    if t.shape != shape:
+        raise MuonError(2, f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype is not dt:
+        raise MuonError(3, f"{what} has dtype {t.dtype}, expected {dt}")
+    s = _head_strides(t.stride(), shape[-1])
+    if s is None:
         raise MuonError(1, f"{what}: the last dimension is not contiguous")
-    return _head_strides(stride[0] if len(shape) == 4 else 0, stride[-3], stride[-2])
+    return s
 
 
-def _head_sizes(q: torch.Tensor, k: Optional[torch.Tensor]) -> Tuple[int, int, int, int, int]:
-    """(batch, tokens, query heads, key heads, dim)."""
-    shape = q.shape
-    if len(shape) not in (3, 4):
+def _head_sizes(shape, keys) -> Tuple[int, int, int, int, int]:
+    """(batch, tokens, query heads, key heads, dim) of the shapes of q and k."""
+    if len(shape) == 4:
+        batch, tokens, hq, dim = shape
+    elif len(shape) == 3:
+        tokens, hq, dim = shape
+        batch = 1
+    else:
         raise MuonError(2, f"q has {len(shape)} dimensions, expected [batch, tokens, heads, dim] or [tokens, heads, dim]")
-    if k is not None:
-        ks = k.shape
-        if len(ks) != len(shape) or ks[:-2] != shape[:-2] or ks[-1] != shape[-1]:
-            raise MuonError(2, f"k has shape {tuple(ks)}, q {tuple(shape)}: they may differ in their heads only")
-        if k.dtype is not q.dtype:
-            raise MuonError(3, f"k has dtype {k.dtype}, expected {q.dtype}")
-    return (shape[0] if len(shape) == 4 else 1), shape[-3], shape[-2], (0 if k is None else k.shape[-2]), shape[-1]
+    if keys is None:
+        return batch, tokens, hq, 0, dim
+    if len(keys) != len(shape) or keys[-1] != dim or keys[-3] != tokens or (len(keys) == 4 and keys[0] != batch):
+        raise MuonError(2, f"k has shape {tuple(keys)}, q {tuple(shape)}: they may differ in their heads only")
+    return batch, tokens, hq, keys[-2], dim
 
 
 def _angles(cos, sin, positions, batch: int, tokens: int) -> Tuple:
     """(cos, sin, table rows, rot, positions, their batch stride)."""
-    if (cos is None) != (sin is None):
-        raise MuonError(1, "cos and sin come together")
-    if cos is None:
+    if cos is None or sin is None:
+        if cos is not sin:
+            raise MuonError(1, "cos and sin come together")
         return None, None, 0, 0, None, 0
-    if cos.dim() != 2 or sin.shape != cos.shape:
-        raise MuonError(2, f"cos and sin have shapes {tuple(cos.shape)} and {tuple(sin.shape)}, expected [table rows, rot / 2]")
-    rows, half = cos.shape
-    c, s = _flat(cos, rows * half, _F32, "cos"), _flat(sin, rows * half, _F32, "sin")
+    shape = cos.shape
+    if len(shape) != 2 or sin.shape != shape:
+        raise MuonError(2, f"cos and sin have shapes {tuple(shape)} and {tuple(sin.shape)}, expected [table rows, rot / 2]")
+    rows, half = shape
+    c, s = _vec(cos, rows * half, "cos"), _vec(sin, rows * half, "sin")
     if positions is None:
         return c, s, rows, 2 * half, None, 0
     if positions.dtype is not torch.int64:
         raise MuonError(3, f"positions has dtype {positions.dtype}, expected torch.int64")
-    shape = tuple(positions.shape)
-    if shape == (tokens,):
-        each = 0
-    elif shape == (batch, tokens):
-        each = positions.stride(0)
-        if batch > 1 and each != 0 and each < tokens:
-            raise MuonError(1, "positions: the sequences overlap")
-    else:
-        raise MuonError(2, f"positions has shape {shape}, expected ({tokens},) or ({batch}, {tokens})")
-    if tokens > 1 and positions.stride(-1) != 1:
+    shape, stride = positions.shape, positions.stride()
+    each = 0
+    if shape == (batch, tokens):
+        if batch > 1:
+            each = stride[0]
+            if each != 0 and each < tokens:
+                raise MuonError(1, "positions: the sequences overlap")
+    elif shape != (tokens,):
+        raise MuonError(2, f"positions has shape {tuple(shape)}, expected ({tokens},) or ({batch}, {tokens})")
+    if tokens > 1 and stride[-1] != 1:
         raise MuonError(1, "positions: the last dimension is not contiguous")
-    return c, s, rows, 2 * half, positions.data_ptr(), each if batch > 1 else 0
+    return c, s, rows, 2 * half, positions.data_ptr(), each
+
+
+def _vec(t: Optional[torch.Tensor], n: int, what: str) -> Optional[int]:
+    """_flat of a float32 argument, with less to do when nothing is wrong."""
+    if t is None:
+        return None
+    if t.dtype is torch.float32 and t.numel() == n and t.is_contiguous():
+        return t.data_ptr()
+    return _flat(t, n, _F32, what)
+
+
+_NO_STRIDES = (None, None)
 
 
 def qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, q_out, k_out, *, positions=None, interleaved: bool = False,
@@ -390,18 +406,26 @@ def qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, q_out, k_out, *, positions=No
     [batch, tokens] or [tokens] (None: 0, 1, ...): the rows of cos and sin; a
     token whose row does not exist is not turned.  q_out may be q itself, k_out k
     itself."""
-    batch, tokens, hq, hk, dim = _head_sizes(q, k)
-    sq, sqo = _heads(q, "q"), _heads(q_out, "q_out", q)
-    if (k is None) != (k_out is None):
-        raise MuonError(1, "k and k_out come together")
-    sk, sko = (None, 0) if k is None else _heads(k, "k"), (None, 0) if k is None else _heads(k_out, "k_out", k)
+    shape, dt, keys = q.shape, q.dtype, None if k is None else k.shape
+    batch, tokens, hq, hk, dim = _head_sizes(shape, keys)
+    sq, sqo = _heads(q, shape, dt, "q"), _heads(q_out, shape, dt, "q_out")
+    if k is None:
+        if k_out is not None:
+            raise MuonError(1, "k and k_out come together")
+        kp = kop = None
+        sk = sko = _NO_STRIDES
+    else:
+        if k_out is None:
+            raise MuonError(1, "k and k_out come together")
+        sk, sko = _heads(k, keys, dt, "k"), _heads(k_out, keys, dt, "k_out")
+        kp, kop = k.data_ptr(), k_out.data_ptr()
     wdt = _param_dtype(q, gamma_q, gamma_k)
     gq, gk = _param(gamma_q, wdt, dim, "gamma_q"), _param(gamma_k, wdt, dim, "gamma_k")
     c, s, rows, rot, pos, each = _angles(cos, sin, positions, batch, tokens)
     dev, st = _device(stream, q, k, gamma_q, gamma_k, cos, sin, positions, q_out, k_out)
-    _call(dev, load_library().muon_qk_norm_rope_fwd, q.data_ptr(), sq[1], None if k is None else k.data_ptr(), sk[1],
-          _dtype_code(q.dtype), batch, tokens, hq, hk, dim, gq, gk, _dtype_code(wdt), eps, c, s, rows, rot,
-          1 if interleaved else 0, pos, each, q_out.data_ptr(), sqo[1], None if k is None else k_out.data_ptr(), sko[1], st)
+    _call(dev, load_library().muon_qk_norm_rope_fwd, q.data_ptr(), sq[1], kp, sk[1], _dtype_code(dt), batch, tokens, hq, hk,
+          dim, gq, gk, _dtype_code(wdt), eps, c, s, rows, rot, 1 if interleaved else 0, pos, each, q_out.data_ptr(), sqo[1],
+          kop, sko[1], st)
 
 
 @functools.lru_cache(maxsize=256)
@@ -418,13 +442,19 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, dq, 
     q_out and k_out and the forward call's q and k: dq and dk, and dgamma_q and
     dgamma_k where given, in the gains' dtype (the `grads` of adamw_step).  dq
     may be dq_out itself, dk dk_out itself."""
-    batch, tokens, hq, hk, dim = _head_sizes(q, k)
-    sq, sdqo, sdq = _heads(q, "q"), _heads(dq_out, "dq_out", q), _heads(dq, "dq", q)
-    if (k is None) != (dk_out is None) or (k is None) != (dk is None):
-        raise MuonError(1, "k, dk_out and dk come together")
-    sk = sdko = sdk = (None, 0)
-    if k is not None:
-        sk, sdko, sdk = _heads(k, "k"), _heads(dk_out, "dk_out", k), _heads(dk, "dk", k)
+    shape, dt, keys = q.shape, q.dtype, None if k is None else k.shape
+    batch, tokens, hq, hk, dim = _head_sizes(shape, keys)
+    sq, sdqo, sdq = _heads(q, shape, dt, "q"), _heads(dq_out, shape, dt, "dq_out"), _heads(dq, shape, dt, "dq")
+    if k is None:
+        if dk_out is not None or dk is not None:
+            raise MuonError(1, "k, dk_out and dk come together")
+        kp = dkop = dkp = None
+        sk = sdko = sdk = _NO_STRIDES
+    else:
+        if dk_out is None or dk is None:
+            raise MuonError(1, "k, dk_out and dk come together")
+        sk, sdko, sdk = _heads(k, keys, dt, "k"), _heads(dk_out, keys, dt, "dk_out"), _heads(dk, keys, dt, "dk")
+        kp, dkop, dkp = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
     wdt = _param_dtype(q, gamma_q, gamma_k, dgamma_q, dgamma_k)
     gq, gk = _param(gamma_q, wdt, dim, "gamma_q"), _param(gamma_k, wdt, dim, "gamma_k")
     dgq, dgk = _param(dgamma_q, wdt, dim, "dgamma_q"), _param(dgamma_k, wdt, dim, "dgamma_k")
@@ -433,10 +463,9 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, dq, 
                       workspace)
     need = _heads_workspace(batch * tokens * hq, batch * tokens * hk, dim) if dgq or dgk else 0
     keep, ws, ws_bytes = _workspace(workspace, need, stream, dev, st)
-    ptr = (lambda t: None) if k is None else torch.Tensor.data_ptr
-    _call(dev, load_library().muon_qk_norm_rope_bwd, dq_out.data_ptr(), sdqo[1], ptr(dk_out), sdko[1], q.data_ptr(), sq[1],
-          ptr(k), sk[1], _dtype_code(q.dtype), batch, tokens, hq, hk, dim, gq, gk, _dtype_code(wdt), eps, c, s, rows,
-          rot, 1 if interleaved else 0, pos, each, dq.data_ptr(), sdq[1], ptr(dk), sdk[1], dgq, dgk, ws, ws_bytes, st)
+    _call(dev, load_library().muon_qk_norm_rope_bwd, dq_out.data_ptr(), sdqo[1], dkop, sdko[1], q.data_ptr(), sq[1], kp,
+          sk[1], _dtype_code(dt), batch, tokens, hq, hk, dim, gq, gk, _dtype_code(wdt), eps, c, s, rows, rot,
+          1 if interleaved else 0, pos, each, dq.data_ptr(), sdq[1], dkp, sdk[1], dgq, dgk, ws, ws_bytes, st)
 
 
 @functools.lru_cache(maxsize=256)
@@ -453,7 +482,7 @@ def token_logp(logits, targets, logp, lse, *, scale: float = 1.0, workspace: Opt
     outside the vocabulary (a prompt or padding token) gives 0 in both."""
     rows, vocab, ld = _matrix(logits, "logits")
     t = _flat(targets, rows, _WORD, "targets")
-    lp, ls = _flat(logp, rows, _F32, "logp"), _flat(lse, rows, _F32, "lse")
+    lp, ls = _vec(logp, rows, "logp"), _vec(lse, rows, "lse")
     dev, st = _device(stream, logits, targets, logp, lse, workspace)
     keep, ws, ws_bytes = _workspace(workspace, _logp_workspace(rows, vocab), stream, dev, st)
     _call(dev, load_library().muon_token_logp_fwd, logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, vocab, t,
@@ -467,7 +496,7 @@ def token_logp_backward(logits, targets, logp, lse, dlogp, dlogits, *, scale: fl
     rows, vocab, ld = _matrix(logits, "logits")
     ld_d = _same(dlogits, logits, "dlogits")
     t = _flat(targets, rows, _WORD, "targets")
-    lp, ls, d = _flat(logp, rows, _F32, "logp"), _flat(lse, rows, _F32, "lse"), _flat(dlogp, rows, _F32, "dlogp")
+    lp, ls, d = _vec(logp, rows, "logp"), _vec(lse, rows, "lse"), _vec(dlogp, rows, "dlogp")
     dev, st = _device(stream, logits, targets, logp, lse, dlogp, dlogits)
     _call(dev, load_library().muon_token_logp_bwd, logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, vocab, t,
           scale, lp, ls, d, dlogits.data_ptr(), ld_d, st)
@@ -490,10 +519,10 @@ def policy_loss(logp, old_logp, advantages, loss, *, ref_logp=None, weight=None,
     float: what dlogp is multiplied by.  terms receives the policy sum, the KL sum
     and the weight of the clipped tokens."""
     n = logp.numel()
-    lp, ol = _flat(logp, n, _F32, "logp"), _flat(old_logp, n, _F32, "old_logp")
-    rf, ad = _flat(ref_logp, n, _F32, "ref_logp"), _flat(advantages, n, _F32, "advantages")
-    w, g = _flat(weight, n, _F32, "weight"), _flat(dlogp, n, _F32, "dlogp")
-    up, lo, tm = _flat(dloss, 1, _F32, "dloss"), _flat(loss, 1, _F32, "loss"), _flat(terms, 3, _F32, "terms")
+    lp, ol = _vec(logp, n, "logp"), _vec(old_logp, n, "old_logp")
+    rf, ad = _vec(ref_logp, n, "ref_logp"), _vec(advantages, n, "advantages")
+    w, g = _vec(weight, n, "weight"), _vec(dlogp, n, "dlogp")
+    up, lo, tm = _vec(dloss, 1, "dloss"), _vec(loss, 1, "loss"), _vec(terms, 3, "terms")
     dev, st = _device(stream, logp, old_logp, ref_logp, advantages, weight, dlogp, dloss, loss, terms, workspace)
     keep, ws, ws_bytes = _workspace(workspace, _policy_workspace(n), stream, dev, st)
     _call(dev, load_library().muon_policy_loss, lp, ol, rf, ad, w, n, clip_low, clip_high, beta, up, lo, tm, g, ws,
@@ -519,10 +548,10 @@ def preference_loss(logp, offsets, loss, *, ref_logp=None, valid=None, weight=No
     if ends % 2 == 0:
         raise MuonError(2, f"offsets has {ends} elements, expected 2 * pairs + 1")
     pairs = ends // 2
-    lp, rf = _flat(logp, n, _F32, "logp"), _flat(ref_logp, n, _F32, "ref_logp")
+    lp, rf = _vec(logp, n, "logp"), _vec(ref_logp, n, "ref_logp")
     v, off = _flat(valid, n, _MASK, "valid"), _flat(offsets, ends, _WORD, "offsets")
-    w, rw = _flat(weight, pairs, _F32, "weight"), _flat(rewards, 2 * pairs, _F32, "rewards")
-    g, up, lo = _flat(dlogp, n, _F32, "dlogp"), _flat(dloss, 1, _F32, "dloss"), _flat(loss, 1, _F32, "loss")
+    w, rw = _vec(weight, pairs, "weight"), _vec(rewards, 2 * pairs, "rewards")
+    g, up, lo = _vec(dlogp, n, "dlogp"), _vec(dloss, 1, "dloss"), _vec(loss, 1, "loss")
     dev, st = _device(stream, logp, ref_logp, valid, offsets, weight, rewards, dlogp, dloss, loss, workspace)
     keep, ws, ws_bytes = _workspace(workspace, _preference_workspace(n, pairs), stream, dev, st)
     _call(dev, load_library().muon_preference_loss, lp, rf, v, n, off, pairs, w, beta, margin, smoothing,
