@@ -339,7 +339,8 @@ muon_status muon_preference_loss(const float* logp, const float* ref_logp, const
     a.tokens = tokens; a.pairs = pairs;
     a.beta = beta; a.margin = margin; a.smoothing = smoothing; a.average = average;
     a.loss = loss; a.rewards = rewards; a.dlogp = dlogp;
-    a.chunks = muon::pref_chunks(tokens, pairs);
+    a.lone = muon::pref_lone(tokens, pairs);
+    a.shift = muon::pref_shift(tokens, pairs);
     a.part = (double*)workspace;
     return launched(muon::run_preference_loss(a, (hipStream_t)stream));
   });

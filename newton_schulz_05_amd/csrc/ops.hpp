@@ -184,8 +184,9 @@ struct PrefArgs {
   float* loss;
   float* rewards;        // or null
   float* dlogp;          // or null
-  int chunks;
-  double* part;          // [2 pairs][chunks][2]: sum and number of tokens
+  bool lone;             // one workgroup takes all
+  int shift;             // else 2^shift workgroups take a sequence
+  double* part;          // [2 pairs][2^shift][2]: sum and number of tokens
 };
 
 // `bf16`: element type of the activations, `wbf16`: of gamma and beta.

@@ -99,7 +99,7 @@ inline size_t policy_workspace_bytes(int64_t tokens) {
   return parts > 1 ? size_t(parts) * 24 : 0;
 }
 inline size_t preference_workspace_bytes(int64_t tokens, int64_t pairs) {
-  return size_t(2 * pairs) * size_t(pref_chunks(tokens, pairs)) * 16;
+  return pref_lone(tokens, pairs) ? 0 : (size_t(2 * pairs) << pref_shift(tokens, pairs)) * 16;
 }
 
 // Sizes of a router call.

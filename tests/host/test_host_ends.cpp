@@ -110,7 +110,7 @@ int main() {
   for (int64_t n : {int64_t(0), int64_t(1), int64_t(4096), int64_t(4097), kLossMaxTokens}) {
     CHECK(policy_parts(n) >= 1 && policy_parts(n) <= kPolicyMaxParts);
     for (int64_t p : {int64_t(0), int64_t(1), kPrefMaxPairs})
-      CHECK(pref_chunks(n, p) >= 1 && pref_chunks(n, p) <= kPrefMaxChunks);
+      CHECK(pref_shift(n, p) >= 0 && (1 << pref_shift(n, p)) <= kPrefMaxChunks);
   }
   if (g_fail) return 1;
   std::puts("ALL OK");

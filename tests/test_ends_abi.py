@@ -178,7 +178,7 @@ def policy(tokens=5000, low=0.2, high=0.2, beta=0.1, ws_bytes=1 << 20, **at):
                                              a["up"], a["loss"], a["terms"], a["d"], a["ws"], ws_bytes, None)
 
 
-def pref(tokens=500, pairs=3, beta=0.1, margin=0.0, smoothing=0.1, average=0, ws_bytes=1 << 20, **at):
+def pref(tokens=500, pairs=30, beta=0.1, margin=0.0, smoothing=0.1, average=0, ws_bytes=1 << 20, **at):
     a = {**PAT, **at}
     return B.load_library().muon_preference_loss(a["lp"], a["ref"], a["valid"], tokens, a["off"], pairs, a["w"], beta, margin,
                                                  smoothing, average, a["up"], a["loss"], a["rew"], a["d"], a["ws"], ws_bytes,
@@ -223,7 +223,8 @@ def test_preference_refusals():
     lib = B.load_library()
     assert lib.muon_preference_loss_workspace_bytes(5, 1, None) == INVALID
     assert lib.muon_preference_loss_workspace_bytes(5, -1, ctypes.byref(n)) == SHAPE
-    assert lib.muon_preference_loss_workspace_bytes(500, 3, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.muon_preference_loss_workspace_bytes(500, 30, ctypes.byref(n)) == 0 and n.value > 0
+    assert lib.muon_preference_loss_workspace_bytes(500, 3, ctypes.byref(n)) == 0 and n.value == 0
 
 
 # ---- the binding -------------------------------------------------------------------
