@@ -194,7 +194,7 @@ template <bool V> using Flag = std::integral_constant<bool, V>;
 hipError_t run_logp_fwd(const LogpArgs& a, bool bf16, hipStream_t st) {
   if (a.rows == 0) return hipSuccess;
   auto go = [&](auto t, auto nt, auto u, auto stream) {
-    constexpr int NT = decltype(nt)::value, WG = 256;
+    constexpr int NT = decltype(nt)::value, WG = NT > 256 ? NT : 256;
     const int64_t groups = (a.rows + WG / NT - 1) / (WG / NT);
     hipLaunchKernelGGL((logp_fwd_kernel<decltype(t), NT, WG, decltype(u)::value, decltype(stream)::value>),
                        dim3(unsigned(std::min(groups, kOpsMaxGrid) * a.parts)), dim3(WG), 0, st, a);
@@ -205,10 +205,15 @@ hipError_t run_logp_fwd(const LogpArgs& a, bool bf16, hipStream_t st) {
     // there (30000 x 500 bf16 18.8 us, 34.6 with two waves a row of two pieces,
     // 61.0 with four; 8192 x 5000 19.0, 22.5, 28.2; 16384 x 2000 fp32 30.1, 28.4,
     // 32.0; but 600 x 5000 6.3, 5.7, 5.5).  Longer rows: four waves of four pieces
-    // (4096 x 32768 bf16 54.0 us, 57.5 with a wave; 4096 x 131072 171 and 180).
+    // (4096 x 32768 bf16 54.0 us, 57.5 with a wave; 4096 x 131072 171 and 180), or
+    // eight where there are few of them (1 x 32768 4.8 us with eight, 4.9 with
+    // sixteen; 300 x 32768 8.8 and 10.2; 300 x 5000, of 625 pieces, 5.8 and 4.6 with
+    // four).
+    constexpr int N = Piece<decltype(t)>::N;
     const bool many = a.rows >= 4096;
-    if (a.cols <= 64 * Piece<decltype(t)>::N || (a.cols <= 2048 && !many)) go(t, Num<64>{}, Num<1>{}, Flag<false>{});
-    else if (a.cols <= 1024 * Piece<decltype(t)>::N && many) go(t, Num<64>{}, Num<2>{}, Flag<false>{});
+    if (a.cols <= 64 * N || (a.cols <= 2048 && !many)) go(t, Num<64>{}, Num<1>{}, Flag<false>{});
+    else if (a.cols <= 1024 * N && many) go(t, Num<64>{}, Num<2>{}, Flag<false>{});
+    else if (a.cols > 1024 * N && a.rows < kLogpFewRows && a.parts == 1) go(t, Num<512>{}, Num<4>{}, Flag<false>{});
     else if (a.rows * a.cols * int64_t(sizeof(t)) > kStreamIn) go(t, Num<256>{}, Num<4>{}, Flag<true>{});
     else go(t, Num<256>{}, Num<4>{}, Flag<false>{});
   };

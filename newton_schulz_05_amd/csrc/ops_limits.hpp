@@ -108,12 +108,15 @@ inline HeadSplit head_split(int64_t rows_q, int64_t rows_k) {
 
 // ---- token log-probabilities ----
 constexpr int64_t kLogpMaxVocab = int64_t(1) << 24;
-// Workgroups that share one row of the forward pass: one for many rows or short
-// ones.
+// Workgroups that share one row of the forward pass, whose parts a second launch
+// joins: for few rows above 65536 words.  A row of 65536 bf16 takes one workgroup
+// 6.9 us and several 5.2, but their second launch costs the host 3 us more; one of
+// 131072 takes 10.4 and 5.2; 128 rows of 65536 8.4 and 9.2.
 constexpr int kLogpMaxParts = 64;
+constexpr int64_t kLogpFewRows = 512;
 inline int logp_parts(int64_t rows, int64_t vocab) {
-  if (rows >= 512 || vocab <= 16384) return 1;
-  const int64_t want = (512 + rows - 1) / std::max<int64_t>(rows, 1);
+  if (rows >= kLogpFewRows || vocab <= 65536) return 1;
+  const int64_t want = (kLogpFewRows + rows - 1) / std::max<int64_t>(rows, 1);
   return int(std::min<int64_t>({want, (vocab + 4095) / 4096, int64_t(kLogpMaxParts)}));
 }
 

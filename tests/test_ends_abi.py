@@ -129,13 +129,13 @@ def test_heads_backward_refusals():
 LAT = _at("x", "t", "lp", "lse", "d", "dx", "ws")
 
 
-def logp(ld=20000, dt=BF16, tokens=3, vocab=20000, scale=1.0, ws_bytes=1 << 20, **at):
+def logp(ld=80000, dt=BF16, tokens=3, vocab=80000, scale=1.0, ws_bytes=1 << 20, **at):
     a = {**LAT, **at}
     return B.load_library().muon_token_logp_fwd(a["x"], ld, dt, tokens, vocab, a["t"], scale, a["lp"], a["lse"], a["ws"],
                                                 ws_bytes, None)
 
 
-def logp_bwd(ld=20000, dt=BF16, tokens=3, vocab=20000, scale=1.0, ld_d=20000, **at):
+def logp_bwd(ld=80000, dt=BF16, tokens=3, vocab=80000, scale=1.0, ld_d=80000, **at):
     a = {**LAT, **at}
     return B.load_library().muon_token_logp_bwd(a["x"], ld, dt, tokens, vocab, a["t"], scale, a["lp"], a["lse"], a["d"],
                                                 a["dx"], ld_d, None)
@@ -147,7 +147,7 @@ def test_token_logp_refusals():
         assert call(tokens=-1) == SHAPE and call(tokens=1 << 31) == SHAPE and call(vocab=0) == SHAPE
         wide = dict(ld=1 << 25, vocab=(1 << 24) + 1, **(dict(ld_d=1 << 25) if call is logp_bwd else {}))
         assert call(**wide) == SHAPE
-        assert call(ld=19999) == INVALID
+        assert call(ld=79999) == INVALID
         for s in (0.0, -1.0, NAN, INF, 1e31):
             assert call(scale=s) == INVALID
         for n in ("x", "t", "lp", "lse"):
@@ -158,7 +158,7 @@ def test_token_logp_refusals():
     assert logp(ws=LAT["x"]) == INVALID
     assert logp(tokens=0, x=None, t=None, lp=None, lse=None, ws=None) == 0
     assert logp_bwd(dx=LAT["x"] + 2) == INVALID       # shifted, not the logits themselves
-    assert logp_bwd(dx=LAT["x"], ld_d=20001) == INVALID
+    assert logp_bwd(dx=LAT["x"], ld_d=80001) == INVALID
     assert logp_bwd(dx=LAT["d"]) == INVALID and logp_bwd(d=None) == INVALID and logp_bwd(dx=None) == INVALID
     assert logp_bwd(ld_d=7) == INVALID
     assert logp_bwd(tokens=0, x=None, t=None, lp=None, lse=None, d=None, dx=None) == 0
