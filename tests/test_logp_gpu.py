@@ -208,6 +208,37 @@ def test_strides_workspaces_and_repeats(rows, vocab, dt):
         assert e.value.status == 5
 
 
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+@pytest.mark.parametrize("vocab", [1, 5, 100, 256, 257, 500, 512, 700, 1000, 1024])
+def test_many_short_rows(vocab, dt):
+    """Rows that a wave takes several of, whole: values, masks and strides as in
+    the other forms."""
+    rows = 16387
+    x, t = _logits(rows, vocab, dt, 71), _targets(rows, vocab, 72, 0.3)
+    if vocab > 4:
+        x[torch.rand(rows, vocab, generator=torch.Generator().manual_seed(2)).to(DEV) < 0.2] = -INF
+        x[torch.arange(rows, device=DEV), t.clamp(min=0)] = 1.0
+        x[1], x[2], x[5] = -INF, -INF, 0.0
+        t[1], t[2] = 0, vocab - 1
+        x[2, vocab - 1] = 0.5
+    none = t < 0
+    clean = x.clone()
+    x[none] = NAN
+    buf = torch.full((rows * (vocab + 3) + 1,), 3.0, dtype=DTYPES[dt], device=DEV)
+    v = buf[1:].view(rows, vocab + 3)[:, :vocab]
+    v.copy_(x)
+    logp, lse = _run(x, t, 0.9)
+    assert all(torch.equal(a, b) for a, b in zip(_run(v, t, 0.9), (logp, lse)))
+    assert not logp[none].any() and not lse[none].any()
+    part = torch.arange(0, rows, 37, device=DEV)
+    part = torch.cat([part, torch.tensor([1, 2, 5, rows - 1], device=DEV)])
+    _check(clean[part], t[part], 0.9, logp[part], lse[part])
+    bad = x.clone()
+    bad[8, vocab // 2], t[8] = NAN, 0
+    got = _run(bad, t, 0.9)
+    assert torch.isnan(got[0][8]) and torch.equal(got[0][9:12], logp[9:12]) and torch.equal(got[1][:8], lse[:8])
+
+
 def test_activations_of_three_dimensions():
     x = _logits(12, 50, "f32", 17).view(3, 4, 50)
     t = _targets(12, 50, 18).view(3, 4)
