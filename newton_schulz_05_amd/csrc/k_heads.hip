@@ -28,17 +28,27 @@ __device__ __forceinline__ uint32_t quotient(uint32_t r, const FastDiv& f) {
   return f.d == 1 ? r : __umulhi(r, f.mul) >> f.shift;
 }
 
+// What does not fill its pieces: nothing; the angles alone (interleaved pairs,
+// rot no multiple of a piece); elements as well.  The last piece of a segment then
+// begins so early that it is whole: the elements that two lanes hold are written
+// by both, the same bits, and enter the sums once.  (Pieces with elements missing,
+// which segments shorter than a piece leave, take three times the instructions:
+// 2 x 4096 tokens of 24 + 8 heads of 90 bf16 50 us forward with them, 38 so.)
+enum Ragged { kWhole, kRaggedAngles, kOverlap, kRagged };
+constexpr bool ragged_angles(int rag, bool inter) { return rag == kRaggedAngles || rag == kRagged || (rag == kOverlap && inter); }
+
 // What a lane holds of every row: 16 elements in pieces of 16 bytes, n[i] of
-// them at column c[i].  A segment's pieces are dealt to its lanes in turn, so that
-// a wave's accesses are adjacent in either type.
+// them at column c[i], the first skip[i] of which another lane counts.  A
+// segment's pieces are dealt to its lanes in turn, so that a wave's accesses are
+// adjacent in either type.
 template <typename T> struct LanePart {
   static constexpr int E = Piece<T>::N, P = 16 / E;
-  int c[P], n[P];
+  int c[P], n[P], skip[P];
   bool turned;
 };
 __device__ __forceinline__ int some(int n, int most) { return n < 0 ? 0 : n > most ? most : n; }
 
-template <typename T, bool INTER> __device__ __forceinline__ LanePart<T> lane_part(int t, int dim, int rot) {
+template <int RAG, typename T, bool INTER> __device__ __forceinline__ LanePart<T> lane_part(int t, int dim, int rot) {
   constexpr int E = LanePart<T>::E, P = LanePart<T>::P;
   LanePart<T> p;
   const int half = rot / 2, first = INTER ? 0 : (half + 7) / 8;
@@ -58,12 +68,14 @@ template <typename T, bool INTER> __device__ __forceinline__ LanePart<T> lane_pa
       p.n[i] = p.n[P / 2 + i] = some(half - p.c[i], E);
     }
   }
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    p.skip[i] = RAG == kOverlap && p.n[i] > 0 ? E - p.n[i] : 0;
+    p.c[i] -= p.skip[i];
+    p.n[i] += p.skip[i];
+  }
   return p;
 }
-
-// What does not fill its pieces: nothing; the angles alone (interleaved pairs,
-// rot no multiple of a piece); elements as well.
-enum Ragged { kWhole, kRaggedAngles, kRagged };
 
 // A lane's elements of a row.
 template <typename T> struct Held {
@@ -89,6 +101,12 @@ template <int RAG, typename T> __device__ __forceinline__ void unpack_held(Held<
     for (int j = 0; j < E; ++j) v[E * i + j] = RAG != kRagged || j < n ? w[j] : 0.0f;
   }
 }
+// The elements that this lane counts, 0 for the others.
+template <int RAG, typename T> __device__ __forceinline__ void counted(const LanePart<T>& p, const float (&v)[16], float (&w)[16]) {
+  constexpr int E = LanePart<T>::E;
+#pragma unroll
+  for (int k = 0; k < 16; ++k) w[k] = RAG == kOverlap && k % E < p.skip[k / E] ? 0.0f : v[k];
+}
 template <int RAG, typename T>
 __device__ __forceinline__ void store_held(T* row, const LanePart<T>& p, bool live, const float (&v)[16], bool stream) {
   constexpr int E = LanePart<T>::E;
@@ -102,7 +120,38 @@ __device__ __forceinline__ void store_held(T* row, const LanePart<T>& p, bool li
   }
 }
 
-// N consecutive elements at p, of which n exist.
+// gamma, in fp32 whatever it is stored in; 1 if null.  Ragged pieces are read
+// like those of a row of dim.
+template <int RAG, int E, typename W> __device__ __forceinline__ void load_gamma(const W* gamma, int col, int n, int dim, float* v) {
+  float w[8];
+  Raw8<W> r;
+  if constexpr (RAG == kRagged) {
+    r = load_row8(gamma, unsigned(col), n > 0 ? dim - col : 0, dim);
+    settle8(r, n > 0 ? dim - col : 0, dim);
+  } else {
+    r = load8(gamma + col, n > 0 ? E : 0);
+  }
+  unpack8(r, w);
+#pragma unroll
+  for (int j = 0; j < E; ++j) v[j] = w[j];
+}
+template <int RAG, typename T>
+__device__ __forceinline__ void load_gamma(const void* gamma, bool bf16, const LanePart<T>& p, int dim, float (&v)[16]) {
+  constexpr int E = LanePart<T>::E;
+#pragma unroll
+  for (int i = 0; i < LanePart<T>::P; ++i) {
+    if (!gamma) {
+#pragma unroll
+      for (int j = 0; j < E; ++j) v[E * i + j] = 1.0f;
+    } else if (bf16) {
+      load_gamma<RAG, E>((const uint16_t*)gamma, p.c[i], p.n[i], dim, v + E * i);
+    } else {
+      load_gamma<RAG, E>((const float*)gamma, p.c[i], p.n[i], dim, v + E * i);
+    }
+  }
+}
+
+// N consecutive angles at p, of which n exist.
 template <int N> __device__ __forceinline__ void load_run(const float* p, int n, float* v) {
   if constexpr (N == 2) {
     if (n >= 2) {
@@ -125,28 +174,6 @@ template <int N> __device__ __forceinline__ void load_run(const float* p, int n,
     unpack8(load8(p, n), u);
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[j] = u[j];
-  }
-}
-template <int N> __device__ __forceinline__ void load_run(const uint16_t* p, int n, float* v) {
-  float u[8];
-  unpack8(load8(p, N == 8 ? n : n < N ? n : N), u);
-#pragma unroll
-  for (int j = 0; j < N; ++j) v[j] = u[j];
-}
-
-// gamma, in fp32 whatever it is stored in; 1 if null.
-template <typename T> __device__ __forceinline__ void load_gamma(const void* gamma, bool bf16, const LanePart<T>& p, float (&v)[16]) {
-  constexpr int E = LanePart<T>::E;
-#pragma unroll
-  for (int i = 0; i < LanePart<T>::P; ++i) {
-    if (!gamma) {
-#pragma unroll
-      for (int j = 0; j < E; ++j) v[E * i + j] = 1.0f;
-    } else if (bf16) {
-      load_run<E>((const uint16_t*)gamma + p.c[i], p.n[i], v + E * i);
-    } else {
-      load_run<E>((const float*)gamma + p.c[i], p.n[i], v + E * i);
-    }
   }
 }
 
@@ -178,10 +205,25 @@ __device__ __forceinline__ void load_angles(const HeadArgs& a, int64_t pos, cons
   for (int i = 0; i < Angles<T, INTER>::RUNS; ++i) {
     const int at = INTER ? p.c[i] / 2 : p.c[i];
     int n = in ? some(half - at, LEN) : 0;
-    if constexpr (RAG == kWhole) n = n > 0 ? LEN : 0;
+    if constexpr (!ragged_angles(RAG, INTER)) n = n > 0 ? LEN : 0;
     g.n[i] = n;
-    load_run<LEN>(a.cos + row * half + at, n, g.c + LEN * i);
-    load_run<LEN>(a.sin + row * half + at, n, g.s + LEN * i);
+    if constexpr (ragged_angles(RAG, INTER) && LEN == 8) {
+      const int left = n > 0 ? half - at : 0;
+      Raw8<float> c = load_row8(a.cos + row * half, unsigned(at), left, half);
+      Raw8<float> s = load_row8(a.sin + row * half, unsigned(at), left, half);
+      settle8(c, left, half);
+      settle8(s, left, half);
+      float u[8];
+      unpack8(c, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g.c[j] = u[j];
+      unpack8(s, u);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) g.s[j] = u[j];
+    } else {
+      load_run<LEN>(a.cos + row * half + at, n, g.c + LEN * i);
+      load_run<LEN>(a.sin + row * half + at, n, g.s + LEN * i);
+    }
   }
 }
 
@@ -194,7 +236,7 @@ template <int RAG, bool BACK, typename T, bool INTER> __device__ __forceinline__
 #pragma unroll
     for (int j = 0; j < LEN; ++j) {
       const int k = LEN * i + j;
-      if (RAG != kWhole && j >= g.n[i]) continue;
+      if (ragged_angles(RAG, INTER) && j >= g.n[i]) continue;
       float &a = v[INTER ? 2 * k : k], &b = v[INTER ? 2 * k + 1 : k + 8];
       const float s = BACK ? -g.s[k] : g.s[k];
       const float x = fmaf(a, g.c[k], -(b * s)), y = fmaf(b, g.c[k], a * s);
@@ -210,10 +252,10 @@ __global__ __launch_bounds__(WG) void heads_fwd_kernel(HeadArgs a) {
   const bool keys = int(blockIdx.x) >= a.q.wgs;
   const HeadRows& h = keys ? a.k : a.q;
   const uint32_t wg = keys ? blockIdx.x - a.q.wgs : blockIdx.x;
-  const LanePart<T> p = lane_part<T, INTER>(threadIdx.x % LANES, a.dim, a.rot);
+  const LanePart<T> p = lane_part<RAG, T, INTER>(threadIdx.x % LANES, a.dim, a.rot);
   const float inv = 1.0f / float(a.dim);
   float gv[16];
-  load_gamma(h.gamma, a.wbf16, p, gv);
+  load_gamma<RAG>(h.gamma, a.wbf16, p, a.dim, gv);
   for (uint64_t row = uint64_t(wg) * ROWS + threadIdx.x / LANES; row < h.rows; row += uint64_t(h.wgs) * ROWS) {
     const Place at = place(h, uint32_t(row));
     Held<T> held;
@@ -222,9 +264,10 @@ __global__ __launch_bounds__(WG) void heads_fwd_kernel(HeadArgs a) {
     load_angles<RAG>(a, at.pos, p, true, ang);
     float v[16];
     unpack_held<RAG>(held, p, true, a.dim, v);
-    float q = 0.0f;
+    float w[16], q = 0.0f;
+    counted<RAG>(p, v, w);
 #pragma unroll
-    for (int j = 0; j < 16; ++j) q = fmaf(v[j], v[j], q);
+    for (int j = 0; j < 16; ++j) q = fmaf(w[j], v[j], q);
     q = lane_sum<LANES>(q);
     const float r = rsqrtf(fmaf(q, inv, a.eps));
 #pragma unroll
@@ -241,10 +284,10 @@ __global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
   const bool keys = int(blockIdx.x) >= a.q.wgs;
   const HeadRows& h = keys ? a.k : a.q;
   const uint32_t wg = keys ? blockIdx.x - a.q.wgs : blockIdx.x;
-  const LanePart<T> p = lane_part<T, INTER>(threadIdx.x % LANES, a.dim, a.rot);
+  const LanePart<T> p = lane_part<RAG, T, INTER>(threadIdx.x % LANES, a.dim, a.rot);
   const float inv = 1.0f / float(a.dim);
   float gv[16], acc[16];
-  load_gamma(h.gamma, a.wbf16, p, gv);
+  load_gamma<RAG>(h.gamma, a.wbf16, p, a.dim, gv);
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = 0.0f;
   const uint64_t step = uint64_t(h.wgs) * ROWS;
@@ -261,11 +304,12 @@ __global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
     unpack_held<RAG>(hx, p, live, a.dim, x);
     unpack_held<RAG>(hy, p, live, a.dim, g);
     turn<RAG, true>(ang, g);
-    float q = 0.0f, dot = 0.0f;
+    float w[16], q = 0.0f, dot = 0.0f;
+    counted<RAG>(p, x, w);
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
-      q = fmaf(x[j], x[j], q);
-      dot = fmaf(g[j] * gv[j], x[j], dot);
+      q = fmaf(w[j], x[j], q);
+      dot = fmaf(g[j] * gv[j], w[j], dot);
     }
     q = lane_sum<LANES>(q);
     dot = lane_sum<LANES>(dot);
@@ -288,7 +332,7 @@ __global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
     for (int i = 0; i < LanePart<T>::P; ++i)
 #pragma unroll
       for (int j = 0; j < E; ++j)
-        if (j < p.n[i]) sums[threadIdx.x / 64][p.c[i] + j] = acc[E * i + j];
+        if (j >= p.skip[i] && j < p.n[i]) sums[threadIdx.x / 64][p.c[i] + j] = acc[E * i + j];
   }
   __syncthreads();
   for (int c = threadIdx.x; c < a.dim; c += WG) {
@@ -355,15 +399,18 @@ template <typename F> hipError_t by_kind(const HeadArgs& a, bool bf16, bool inte
   };
   typedef std::integral_constant<int, kWhole> Whole;
   typedef std::integral_constant<int, kRaggedAngles> RaggedAngles;
+  typedef std::integral_constant<int, kOverlap> Overlap;
   typedef std::integral_constant<int, kRagged> AllRagged;
-  const int half = a.rot / 2;
+  const int half = a.rot / 2, rest = a.dim - a.rot;
   auto kind = [&](auto t) {
     constexpr int E = Piece<decltype(t)>::N;
     if (inter) {
-      if (a.dim % E != 0) lanes(t, std::true_type{}, AllRagged{});
-      else half % (E / 2) != 0 ? lanes(t, std::true_type{}, RaggedAngles{}) : lanes(t, std::true_type{}, Whole{});
+      if (a.dim % E == 0) half % (E / 2) != 0 ? lanes(t, std::true_type{}, RaggedAngles{}) : lanes(t, std::true_type{}, Whole{});
+      else a.dim >= E && a.dim % 2 == 0 ? lanes(t, std::true_type{}, Overlap{}) : lanes(t, std::true_type{}, AllRagged{});
     } else {
-      a.dim % E != 0 || half % E != 0 ? lanes(t, std::false_type{}, AllRagged{}) : lanes(t, std::false_type{}, Whole{});
+      if (half % E == 0 && rest % E == 0) lanes(t, std::false_type{}, Whole{});
+      else (half == 0 || half >= E) && (rest == 0 || rest >= E) ? lanes(t, std::false_type{}, Overlap{})
+                                                               : lanes(t, std::false_type{}, AllRagged{});
     }
   };
   bf16 ? kind(uint16_t{}) : kind(float{});
