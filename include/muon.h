@@ -460,7 +460,9 @@ muon_status muon_qk_norm_rope_workspace_bytes(int64_t rows_q, int64_t rows_k, in
  *   dq, dk             : [batch, tokens, heads, dim] of dt; dq may be dq_out
  *                        itself and dk dk_out itself.
  *   dgamma_q, dgamma_k : dim elements of param_dt, overwritten; null if not
- *                        wanted. */
+ *                        wanted.  Their sums take the heads in the order in
+ *                        which q and k lie in memory: another order of the
+ *                        dimensions may change the last place. */
 muon_status muon_qk_norm_rope_bwd(const void* dq_out, const muon_head_strides* s_dqo, const void* dk_out,
                                   const muon_head_strides* s_dko, const void* q, const muon_head_strides* s_q,
                                   const void* k, const muon_head_strides* s_k, muon_dtype dt, int64_t batch,
@@ -492,7 +494,8 @@ muon_status muon_token_logp_fwd(const void* logits, int64_t ld, muon_dtype dt, i
 
 /* Its gradient: dlogit_j = scale dlogp ([j = target] - exp(z_j - lse)), the
  * target's 1 - exp(logp) formed from logp; 0 in the rows of tokens without a
- * target and those whose dlogp is 0 (they are not read).
+ * target and those whose dlogp is 0 (they are not read).  A probability below
+ * 2^-126 may be 0.
  *   logp, lse : as the forward pass wrote them.
  *   dlogp     : tokens floats, as the losses below write them.
  *   dlogits   : [tokens, vocab] of dt; may be logits itself. */

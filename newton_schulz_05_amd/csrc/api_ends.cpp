@@ -17,17 +17,6 @@ namespace {
 using namespace muon::api;
 using muon::Operand;
 
-muon::FastDiv fast_div(int64_t d) {
-  muon::FastDiv f{uint32_t(d), 0, 0};
-  if (d > 1) {
-    int s = 1;
-    while ((int64_t(1) << s) < d) ++s;
-    f.mul = uint32_t(((uint64_t(1) << (31 + s)) + uint64_t(d) - 1) / uint64_t(d));
-    f.shift = uint32_t(s - 1);
-  }
-  return f;
-}
-
 // What a call on heads is given, queries and keys alike.
 struct HeadCall {
   muon_dtype dt, param_dt;
@@ -87,7 +76,7 @@ muon::HeadRows head_rows(const HeadCall& c, const HeadTensors& h) {
   muon::HeadRows r{};
   r.x = h.x; r.dy = h.dy; r.out = h.out; r.gamma = h.gamma; r.dgamma = h.dgamma;
   r.rows = uint32_t(c.batch * c.tokens * h.heads);
-  r.n0 = r.n1 = fast_div(1);
+  r.n0 = r.n1 = muon::fast_div(1);
   if (r.rows == 0) return r;
   struct Dim {
     int64_t n, x, dy, out, pos;
@@ -95,8 +84,8 @@ muon::HeadRows head_rows(const HeadCall& c, const HeadTensors& h) {
             {c.tokens, h.s_x->token, h.s_dy ? h.s_dy->token : 0, h.s_out->token, 1},
             {h.heads, h.s_x->head, h.s_dy ? h.s_dy->head : 0, h.s_out->head, 0}};
   std::stable_sort(d, d + 3, [](const Dim& a, const Dim& b) { return (a.n > 1 ? a.x : 0) < (b.n > 1 ? b.x : 0); });
-  r.n0 = fast_div(d[0].n);
-  r.n1 = fast_div(d[1].n);
+  r.n0 = muon::fast_div(d[0].n);
+  r.n1 = muon::fast_div(d[1].n);
   for (int i = 0; i < 3; ++i) {
     r.s_x[i] = d[i].x;
     r.s_dy[i] = d[i].dy;

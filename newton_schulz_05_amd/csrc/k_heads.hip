@@ -177,6 +177,12 @@ template <int N> __device__ __forceinline__ void load_run(const float* p, int n,
   }
 }
 
+// 1 / sqrt(v), v > 0: the hardware's root takes numbers below 2^-126 for 0.
+__device__ __forceinline__ float inv_root(float v) {
+  const bool tiny = v < 1e-30f;
+  return rsqrtf(tiny ? v * 0x1p96f : v) * (tiny ? 0x1p48f : 1.0f);
+}
+
 // One row's place: offsets of its tensors, and the table's row of its angles
 // (-1: not turned).
 struct Place {
@@ -269,7 +275,7 @@ __global__ __launch_bounds__(WG) void heads_fwd_kernel(HeadArgs a) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) q = fmaf(w[j], v[j], q);
     q = lane_sum<LANES>(q);
-    const float r = rsqrtf(fmaf(q, inv, a.eps));
+    const float r = inv_root(fmaf(q, inv, a.eps));
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = v[j] * r * gv[j];
     turn<RAG, false>(ang, v);
@@ -313,7 +319,7 @@ __global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
     }
     q = lane_sum<LANES>(q);
     dot = lane_sum<LANES>(dot);
-    const float r = rsqrtf(fmaf(q, inv, a.eps)), c = dot * r * inv;
+    const float r = inv_root(fmaf(q, inv, a.eps)), c = dot * r * inv;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const float xh = x[j] * r;

@@ -56,7 +56,7 @@ __global__ __launch_bounds__(kPolicyThreads) void policy_kernel(PolicyArgs a) {
     const double pg = cut ? -adv * (adv > 0.0 ? a.high : a.low) : -gain;
     if (w != 0.0) {
       sum[0] += w * pg;
-      sum[1] += w * (e - u);
+      sum[1] += w * (u == INFINITY ? u : e - u);
       sum[2] += cut ? w : 0.0;
     }
     if (a.dlogp) a.dlogp[i] = w != 0.0 ? float(up * w * ((cut ? 0.0 : -gain) - a.beta * e)) : 0.0f;

@@ -97,11 +97,6 @@ struct RouteBwdArgs {
   void* dlogits;
 };
 
-// Quotients of numbers below 2^31 by d: floor(r mul / 2^(32 + shift)).
-struct FastDiv {
-  uint32_t d, mul, shift;
-};
-
 // The heads of queries or of keys as rows, in the order of their input's
 // memory: row r stands at (i0, i1, i2), i0 = r % n0, i1 = r / n0 % n1.
 struct HeadRows {

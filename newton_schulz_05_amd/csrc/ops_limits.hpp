@@ -80,6 +80,24 @@ constexpr int64_t kHeadMaxDim = 512;  // a head's row is held by at most one wav
 constexpr int64_t kHeadMaxRows = 0x7fffffff;
 constexpr int kHeadThreads = 256;
 
+// Quotients of numbers r below 2^31 by d: floor(r mul / 2^(32 + shift)), with mul =
+// ceil(2^(31 + s) / d) and shift = s - 1 for 2^(s - 1) < d <= 2^s.  mul d exceeds
+// 2^(31 + s) by less than 2^s, so that r times the excess stays below 2^(31 + s)
+// and the quotient below the next whole number.  d = 1 is left to the caller.
+struct FastDiv {
+  uint32_t d, mul, shift;
+};
+inline FastDiv fast_div(int64_t d) {
+  FastDiv f{uint32_t(d), 0, 0};
+  if (d > 1) {
+    int s = 1;
+    while ((int64_t(1) << s) < d) ++s;
+    f.mul = uint32_t(((uint64_t(1) << (31 + s)) + uint64_t(d) - 1) / uint64_t(d));
+    f.shift = uint32_t(s - 1);
+  }
+  return f;
+}
+
 // Lanes that share one head's row, 16 elements each.  Pairs that lie rot / 2
 // apart are one lane's: 8 elements of the first half of the turned ones with
 // those of the second half, then the elements that are not turned, 16 a lane.

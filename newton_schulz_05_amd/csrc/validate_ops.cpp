@@ -16,6 +16,54 @@ muon_status fail(muon_status s, std::string* detail, const std::string& d) {
 // Largest row count, pitch and element offset of an operand.
 constexpr int64_t kMaxExtent = int64_t(1) << 40;
 
+// Two tensors of heads with common strides, b's first byte `d` behind a's: whether
+// an entry of one meets an entry of the other.  Dimensions outermost first; what
+// lies within one is no longer than its stride, so that at most a few distances
+// t = (b's index - a's) come into question at each.
+struct HeadPair {
+  int64_t na[3], nb[3], s[3], wa, wb;
+  int64_t span(const int64_t (&n)[3], int64_t w, int from) const {
+    for (int i = from; i < 3; ++i) w += (n[i] - 1) * s[i];
+    return w;
+  }
+  bool meet(int level, int64_t d) const {
+    if (level == 3) return d < wa && -d < wb;
+    const int64_t sa = span(na, wa, level + 1), sb = span(nb, wb, level + 1);
+    if (s[level] == 0) return meet(level + 1, d);
+    auto floor_div = [](int64_t x, int64_t y) { return x / y - (x % y != 0 && x < 0); };
+    // -sb < d + t s < sa
+    const int64_t lo = std::max(floor_div(-sb - d, s[level]) + 1, 1 - na[level]);
+    const int64_t hi = std::min(-floor_div(-(sa - d), s[level]) - 1, nb[level] - 1);
+    for (int64_t t = lo; t <= hi; ++t)
+      if (meet(level + 1, d + t * s[level])) return true;
+    return false;
+  }
+};
+
+// Fills `p` if a and b have common strides.
+bool common_strides(const Operand& a, const Operand& b, HeadPair* p) {
+  if (!a.inner || !b.inner) return false;
+  struct Dim {
+    int64_t na, nb, s;
+  } d[3];
+  for (int i = 0; i < 3; ++i) {
+    if (a.n[i] > 1 && b.n[i] > 1 && a.s[i] != b.s[i]) return false;
+    d[i] = {a.n[i], b.n[i], a.n[i] > 1 ? a.s[i] : b.n[i] > 1 ? b.s[i] : 0};
+  }
+  std::sort(d, d + 3, [](const Dim& x, const Dim& y) { return x.s > y.s; });
+  for (int i = 0; i < 3; ++i) {
+    p->na[i] = d[i].na;
+    p->nb[i] = d[i].nb;
+    p->s[i] = d[i].s;
+  }
+  p->wa = a.inner;
+  p->wb = b.inner;
+  // a dimension that one tensor has alone may be shorter than what the other has within it
+  for (int i = 0; i < 3; ++i)
+    if (p->s[i] > 0 && (p->span(p->na, p->wa, i + 1) > p->s[i] || p->span(p->nb, p->wb, i + 1) > p->s[i])) return false;
+  return true;
+}
+
 }  // namespace
 
 bool overlap(const Operand& a, const Operand& b) {
@@ -24,6 +72,8 @@ bool overlap(const Operand& a, const Operand& b) {
   const uint64_t a1 = a0 + uint64_t(a.rows - 1) * uint64_t(a.pitch) + uint64_t(a.width);
   const uint64_t b1 = b0 + uint64_t(b.rows - 1) * uint64_t(b.pitch) + uint64_t(b.width);
   if (a1 <= b0 || b1 <= a0) return false;
+  HeadPair h;
+  if (common_strides(a, b, &h)) return h.meet(0, int64_t(b0 - a0));
   if (a.pitch != b.pitch || (a.rows == 1 && b.rows == 1)) return true;
   // runs of b lie d bytes after runs of a, modulo the pitch
   const uint64_t pitch = uint64_t(a.pitch);
@@ -115,7 +165,7 @@ muon_status check_route(int64_t tokens, int64_t ld, int32_t experts, int32_t k, 
 
 muon_status head_operand(const char* name, const void* p, const muon_head_strides* s, int64_t batch, int64_t tokens,
                          int64_t heads, int64_t dim, int size, bool written, Operand* op, std::string* detail) {
-  *op = {name, p, batch * tokens * heads > 0 ? 1 : 0, dim * size, dim * size, size, written, false};
+  *op = Operand{name, p, batch * tokens * heads > 0 ? 1 : 0, dim * size, dim * size, size, written, false};
   if (op->rows == 0) return MUON_OK;
   if (!s) return fail(MUON_ERR_INVALID_ARG, detail, std::string(name) + ": strides are null");
   struct Dim {
@@ -130,6 +180,12 @@ muon_status head_operand(const char* name, const void* p, const muon_head_stride
       return fail(MUON_ERR_INVALID_ARG, detail, std::string(name) + ": the dimensions do not nest (a stride is smaller than what lies within)");
     if (x.stride > kMaxExtent / x.n) return fail(MUON_ERR_SHAPE, detail, std::string(name) + ": tensor too large");
     span += (x.n - 1) * x.stride;
+  }
+  op->inner = dim * size;
+  const int64_t ns[3] = {batch, tokens, heads}, strides[3] = {s->batch, s->token, s->head};
+  for (int i = 0; i < 3; ++i) {
+    op->n[i] = ns[i];
+    op->s[i] = ns[i] > 1 ? strides[i] * size : 0;
   }
   // outermost first: dimensions that follow one another without a gap are one
   op->width = span * size;

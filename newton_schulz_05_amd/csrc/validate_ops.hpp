@@ -24,11 +24,15 @@ struct Operand {
   int align;      // bytes
   bool written;
   bool optional;  // may be null
+  // A tensor of heads also by its dimensions (batch, tokens, heads): entries, and
+  // strides in bytes; each entry is `inner` bytes.  0 inner: no such tensor.
+  int64_t n[3] = {0, 0, 0}, s[3] = {0, 0, 0}, inner = 0;
 };
 
 // Whether two operands share a byte.  Runs of one common pitch are compared
 // by their place within the pitch, so that column slices of one buffer count
-// as apart; otherwise the whole ranges are compared.
+// as apart, and so are two tensors of heads with common strides, by their
+// elements; otherwise the whole ranges are compared.
 bool overlap(const Operand& a, const Operand& b);
 
 // Null, alignment and overlap checks of a call's operands: no written operand

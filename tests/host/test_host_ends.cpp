@@ -68,8 +68,47 @@ static void check_head_operands() {
   }
 }
 
+// Overlap of two tensors of heads with common strides, against their bytes: slices
+// of tokens and of heads of one buffer, every distance.
+static void check_head_overlap() {
+  std::string d;
+  int apart = 0, met = 0;
+  for (int64_t st : {8, 9, 12})
+    for (int64_t sb : {2 * st, 3 * st, 3 * st + 5})
+      for (int64_t sh : {2, 3})
+        for (int64_t t = 1; t <= 2; ++t)
+          for (int64_t ha = 1; ha <= 2; ++ha)
+            for (int64_t hb = 1; hb <= 2; ++hb)
+              for (int64_t at = -40; at <= 40; ++at) {
+                const muon_head_strides s{sb, st, sh};
+                Operand a, b;
+                CHECK(head_operand("a", reinterpret_cast<void*>(0x1000), &s, 2, t, ha, 2, 1, true, &a, &d) == MUON_OK);
+                CHECK(head_operand("b", reinterpret_cast<void*>(uintptr_t(0x1000 + at)), &s, 2, t, hb, 2, 1, true, &b, &d) == MUON_OK);
+                std::set<int64_t> x, y;
+                bytes(2, t, ha, 2, s, &x);
+                bytes(2, t, hb, 2, s, &y);
+                bool share = false;
+                for (int64_t e : y) share = share || x.count(e + at);
+                CHECK(overlap(a, b) == share && overlap(b, a) == share);
+                ++(share ? met : apart);
+              }
+  CHECK(apart > 1000 && met > 1000);
+}
+
+static void check_fast_div() {
+  for (int64_t d = 2; d < 0x7fffffff; d = d < 3000 ? d + 1 : d * 5 / 4 + 1) {
+    const FastDiv f = fast_div(d);
+    auto q = [&](uint64_t r) { return int64_t(((r * f.mul) >> 32) >> f.shift); };
+    for (int64_t r : {int64_t(0), d - 1, d, d + 1, 2 * d - 1, 2 * d, int64_t(0x7ffffffe), int64_t(0x7fffffff),
+                      0x7fffffff / d * d, 0x7fffffff / d * d - 1, 0x40000000 / d * d, 0x40000000 / d * d - 1})
+      if (r >= 0 && r <= 0x7fffffff) CHECK(q(uint64_t(r)) == r / d);
+  }
+}
+
 int main() {
   check_head_operands();
+  check_head_overlap();
+  check_fast_div();
   std::string d;
   const int64_t top = std::numeric_limits<int64_t>::max();
   auto heads = [&](int64_t b, int64_t t, int32_t hq, int32_t hk, int64_t table, int64_t posb) {

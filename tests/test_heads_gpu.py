@@ -237,9 +237,109 @@ def test_extreme_rows():
         assert torch.equal(o2[0, keep], out[0, keep]) and torch.equal(d2[0, keep], dx[0, keep])
         assert torch.isnan(o2[0, 5]).all() and torch.isnan(o2[0, 6, 0, 60])
     # a small eps: 1 / sqrt(eps) ** 3 is beyond fp32, the gradient of a zero head is not
-    qk_norm_rope_backward(dy, None, torch.zeros_like(x), None, g, None, None, None, dx, None, eps=1e-30)
-    want, _ = R.qk_norm_rope_backward(h64(dy), np.zeros(x.shape), h64(g), *R.token_angles(cn, sn, 0, 1, 8), 0, False, 1e-30)
-    within(dx, want, 8 * U * np.abs(want), "tiny eps")
+    for eps in (1e-30, 1e-44):
+        zero = torch.zeros_like(x)
+        qk_norm_rope(zero, None, g, None, cos, sin, out, None, eps=eps)
+        assert not out.any()
+        qk_norm_rope_backward(dy, None, zero, None, g, None, None, None, dx, None, eps=eps)
+        e = float(np.float32(eps))
+        want, _ = R.qk_norm_rope_backward(h64(dy), np.zeros(x.shape), h64(g), *R.token_angles(cn, sn, 0, 1, 8), 0, False, e)
+        within(dx, want, 8 * U * np.abs(want), "tiny eps")
+
+
+def test_slices_of_tokens_of_a_packed_buffer():
+    """Some tokens of a projection's output, in place and into another buffer's:
+    queries and keys lie between one another and do not overlap."""
+    cos, sin, _, _ = _angles(32)
+    buf = draw((3, 20, 7, 32), 51).to(DEV)
+    part = buf[:, 4:15]
+    q, k = part[:, :, :4], part[:, :, 4:6]
+    qo, ko = torch.empty(3, 11, 4, 32, device=DEV), torch.empty(3, 11, 2, 32, device=DEV)
+    qk_norm_rope(q, k, None, None, cos, sin, qo, ko)
+    other = torch.full_like(buf, 3.0)
+    to = other[:, 9:]
+    qk_norm_rope(q, k, None, None, cos, sin, to[:, :, 2:6], to[:, :, :2])
+    assert torch.equal(to[:, :, 2:6], qo) and torch.equal(to[:, :, :2], ko)
+    to[:, :, :6] = 3.0
+    assert (other == 3.0).all()
+    with pytest.raises(MuonError):
+        qk_norm_rope(q, k, None, None, cos, sin, to[:, :, 2:6], to[:, :, 5:7])
+    want = buf.clone()
+    want[:, 4:15, :4], want[:, 4:15, 4:6] = qo, ko
+    qk_norm_rope(q, k, None, None, cos, sin, q, k)
+    assert torch.equal(buf, want)
+
+
+def test_heads_beyond_32_bit_offsets():
+    big = (1 << 31) + 64
+    store = torch.empty(big * 2 + 4096, dtype=torch.bfloat16, device=DEV)
+    x = draw((3, 2, 4, 64), 61).to(DEV).bfloat16()
+    cos, sin, _, _ = _angles(64)
+    want, back, dg = torch.empty_like(x), torch.empty_like(x), torch.empty(64, device=DEV)
+    g = draw((64,), 62, 0.1, 1.0).to(DEV)
+    qk_norm_rope(x, None, g, None, cos, sin, want, None)
+    qk_norm_rope_backward(want, None, x, None, g, None, cos, sin, back, None, dgamma_q=dg)
+    v = store.as_strided((3, 2, 4, 64), (big, 4 * 64, 64, 1))
+    v.copy_(x)
+    got, d2, dg2 = torch.empty_like(x), torch.empty_like(x), torch.empty_like(dg)
+    qk_norm_rope(v, None, g, None, cos, sin, got, None)
+    assert torch.equal(got, want)
+    qk_norm_rope_backward(want, None, v, None, g, None, cos, sin, d2, None, dgamma_q=dg2)
+    assert torch.equal(d2, back) and torch.equal(dg2, dg)
+    qk_norm_rope(v, None, g, None, cos, sin, v, None)
+    assert torch.equal(v, want)
+
+
+def test_large_outputs():
+    """Outputs beyond what the caches hold take other stores: the same bits."""
+    for dt in ("bf16", "f32"):
+        x = draw((1, 1, 8, 128), 71, 1.0, 0.0, DTYPES[dt]).to(DEV)
+        cos, sin, _, _ = _angles(128)
+        n = (100 << 20) // (8 * 128 * x.element_size())
+        many = x.expand(1, n, 8, 128).contiguous()
+        pos = torch.full((n,), 7, device=DEV)
+        one, out = torch.empty_like(x), torch.empty_like(many)
+        qk_norm_rope(x, None, None, None, cos, sin, one, None, positions=pos[:1])
+        qk_norm_rope(many, None, None, None, cos, sin, out, None, positions=pos)
+        assert torch.equal(out, one.expand_as(out))
+        qk_norm_rope_backward(one, None, x, None, None, None, cos, sin, one, None, positions=pos[:1])
+        qk_norm_rope_backward(out, None, many, None, None, None, cos, sin, out, None, positions=pos)
+        assert torch.equal(out, one.expand_as(out))
+
+
+def test_two_host_threads():
+    import threading
+    cos, sin, _, _ = _angles(64)
+    g = draw((64,), 80, 0.1, 1.0).to(DEV)
+    sets, bad = [], []
+    for i in range(2):
+        x = draw((1, 400 + 90 * i, 4 + i, 64), 81 + i).to(DEV)
+        o = [torch.empty_like(x), torch.empty_like(x), torch.empty_like(g)]
+        qk_norm_rope(x, None, g, None, cos, sin, o[0], None, positions=torch.arange(x.shape[1], device=DEV) % 90)
+        qk_norm_rope_backward(x, None, x, None, g, None, cos, sin, o[1], None, dgamma_q=o[2])
+        sets.append((x, o, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+
+    def work(x, want, stream):
+        try:
+            pos = torch.arange(x.shape[1], device=DEV) % 90
+            outs = [[torch.empty_like(t) for t in want] for _ in range(20)]
+            torch.cuda.synchronize()
+            for o in outs:
+                qk_norm_rope(x, None, g, None, cos, sin, o[0], None, positions=pos, stream=stream)
+                qk_norm_rope_backward(x, None, x, None, g, None, cos, sin, o[1], None, dgamma_q=o[2], stream=stream)
+            stream.synchronize()
+            if not all(torch.equal(a, b) for o in outs for a, b in zip(o, want)):
+                bad.append("outputs differ")
+        except Exception as e:  # noqa: BLE001 - reported by the test
+            bad.append(repr(e))
+
+    ts = [threading.Thread(target=work, args=s) for s in sets]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert not bad, bad
 
 
 def test_no_tokens():

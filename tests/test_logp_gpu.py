@@ -262,6 +262,46 @@ def test_rows_beyond_32_bit_offsets():
     assert torch.equal(v, dx)
 
 
+def test_many_rows_of_few_words():
+    """More rows than one launch has workgroups for."""
+    rows, vocab = 300001, 9
+    x, t = _logits(rows, vocab, "bf16", 91), _targets(rows, vocab, 92)
+    logp, lse = _run(x, t)
+    d = draw((rows,), 93).to(DEV)
+    dx = torch.full_like(x, 5.0)
+    token_logp_backward(x, t, logp, lse, d, dx)
+    part = torch.cat([torch.arange(0, rows, 3001, device=DEV), torch.tensor([rows - 1, 262143, 262144], device=DEV)])
+    _check(x[part], t[part], 1.0, logp[part], lse[part])
+    _check_grad(x[part], t[part], 1.0, logp[part], lse[part], d[part], dx[part])
+    again = torch.empty_like(x[200000:])
+    token_logp_backward(x[200000:], t[200000:], logp[200000:], lse[200000:], d[200000:], again)
+    assert torch.equal(again, dx[200000:])
+
+
+@pytest.mark.parametrize("dt", ["f32", "bf16"])
+def test_large_logits(dt):
+    """Logits and gradients beyond what the caches hold: the same bits as part by
+    part."""
+    vocab = 30011
+    rows = (260 << 20) // (vocab * (4 if dt == "f32" else 2))
+    x = torch.empty(rows, vocab, dtype=DTYPES[dt], device=DEV)
+    x.copy_(_logits(64, vocab, dt, 94).repeat(rows // 64 + 1, 1)[:rows])
+    t, d = _targets(rows, vocab, 95), draw((rows,), 96).to(DEV)
+    logp, lse = _run(x, t)
+    dx = torch.empty_like(x)
+    token_logp_backward(x, t, logp, lse, d, dx)
+    _check(x[:40], t[:40], 1.0, logp[:40], lse[:40])
+    for at in (0, rows - 600):
+        s = slice(at, at + 600)
+        a, b = _run(x[s], t[s])
+        assert torch.equal(a, logp[s]) and torch.equal(b, lse[s])
+        again = torch.empty_like(x[s])
+        token_logp_backward(x[s], t[s], a, b, d[s], again)
+        assert torch.equal(again, dx[s])
+    token_logp_backward(x, t, logp, lse, d, x)
+    assert torch.equal(x, dx)
+
+
 def test_gradient_against_differences():
     rows, vocab, scale = 7, 31, 1.5
     x, t = _logits(rows, vocab, "f32", 21), _targets(rows, vocab, 22, 0.3)

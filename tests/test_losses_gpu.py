@@ -121,6 +121,15 @@ def test_policy_extreme_ratios():
     _one(out[0], -f32(0.28) - 1 + 2 * (1 - f32(0.2)), 4, "loss")
 
 
+def test_policy_reference_beyond_reach():
+    """KL terms of tokens that one policy cannot give are infinite, not NaN."""
+    lp = torch.tensor([-INF, -1.0, -800.0], device=DEV)
+    rf = torch.tensor([-1.0, -INF, 0.0], device=DEV)
+    for i in range(3):
+        out = _policy(lp[i:i + 1], None, rf[i:i + 1], torch.zeros(1, device=DEV), None, beta=1.0)
+        assert out[0] == INF and out[1][1] == INF, i
+
+
 def test_policy_no_tokens():
     e = torch.empty(0, device=DEV)
     out = _policy(e, e, e, e, e)
