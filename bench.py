@@ -148,6 +148,63 @@ def bench_adamw(steps, warmup, elems):
                          "launches_per_step": (len(sizes) + 31) // 32}}
 
 
+def bench_ends(steps, warmup):
+    """The operators at the two ends of a training step of 16384 tokens of the
+    32-layer transformer set: norm and rotation of 32 query and 8 key heads of
+    128, forward and backward, and the log-probabilities of 8192 of the tokens
+    over 65536 words, the clipped policy loss on them and its gradient by the
+    logits.  Bytes as each reads and writes them once; each is also timed alone."""
+    import torch
+    import newton_schulz_05_amd as muon
+    b, s, hq, hk, d, rows, vocab = 4, 4096, 32, 8, 128, 8192, 65536
+    dev, bf = "cuda", torch.bfloat16
+    qkv = torch.randn(b, s, hq + 2 * hk, d, device=dev).to(bf)
+    q, k = qkv[:, :, :hq], qkv[:, :, hq:hq + hk]
+    qo, ko, dqo, dko = (torch.randn(b, h, s, d, device=dev).to(bf).transpose(1, 2) for h in (hq, hk, hq, hk))
+    dqkv = torch.empty_like(qkv)
+    gq, gk = torch.ones(d, dtype=bf, device=dev), torch.ones(d, dtype=bf, device=dev)
+    dgq, dgk = torch.empty_like(gq), torch.empty_like(gk)
+    ang = torch.arange(s, device=dev, dtype=torch.float64)[:, None] * 10000.0 ** (
+        -torch.arange(0, d, 2, device=dev, dtype=torch.float64) / d)
+    cos, sin = ang.cos().float(), ang.sin().float()
+    logits = torch.randn(rows, vocab, device=dev).to(bf)
+    targets = torch.randint(0, vocab, (rows,), device=dev)
+    logp, lse, dlogp, adv = (torch.randn(rows, device=dev) for _ in range(4))
+    w, loss = torch.full((rows,), 1.0 / rows, device=dev), torch.empty(1, device=dev)
+    dlogits = torch.empty_like(logits)
+    st = torch.cuda.current_stream()
+    n, m = b * s * (hq + hk) * d, rows * vocab
+    parts = {
+        "qk_norm_rope": (4.0 * n, lambda: muon.qk_norm_rope(q, k, gq, gk, cos, sin, qo, ko, stream=st)),
+        "token_logp": (2.0 * m, lambda: muon.token_logp(logits, targets, logp, lse, stream=st)),
+        # the policy that sampled the tokens: no token is clipped, and every row of logits has a gradient
+        "policy_loss": (16.0 * rows, lambda: muon.policy_loss(logp, None, adv, loss, weight=w, dlogp=dlogp, stream=st)),
+        "token_logp_backward": (4.0 * m, lambda: muon.token_logp_backward(logits, targets, logp, lse, dlogp, dlogits,
+                                                                         stream=st)),
+        "qk_norm_rope_backward": (6.0 * n, lambda: muon.qk_norm_rope_backward(
+            dqo, dko, q, k, gq, gk, cos, sin, dqkv[:, :, :hq], dqkv[:, :, hq:hq + hk], dgamma_q=dgq, dgamma_k=dgk,
+            stream=st)),
+    }
+
+    def fn():
+        for _, f in parts.values():
+            f()
+    ms = _events_time(fn, steps, warmup, st)
+    byt = sum(x for x, _ in parts.values())
+    alone = {name: {"ms": round(v, 5), "gb_s": round(x / (v * 1e-3) / 1e9, 1)}
+             for name, (x, f) in parts.items() for v in [_events_time(f, steps, warmup, st)]}
+    gbs = byt / (ms * 1e-3) / 1e9
+    return {"metric": "operators at the two ends of a training step (ms, GB/s)", "value": round(gbs, 1), "unit": "GB/s",
+            "n_gpus": 1, "steps": steps, "warmup": warmup, "ms_per_step": round(ms, 5), "higher_is_better": True,
+            "scaling": "weak", "vs_baseline": None, "dtype": "bf16", "data": "synthetic",
+            "config": {"workload": "heads_4x4096x40x128_logits_8192x65536", "batch": b, "seq_len": s, "heads": [hq, hk],
+                       "dim": d, "rows": rows, "vocab": vocab},
+            "alone": alone,
+            "roofline": {"bound": "hbm", "achieved": round(gbs, 1), "peak": HBM_PEAK_GBS, "unit": "GB/s",
+                         "frac": round(gbs / HBM_PEAK_GBS, 4), "traffic": None, "kernel": "logp_bwd_kernel",
+                         "launches_per_step": 7}}
+
+
 def bench_block(steps, warmup):
     """The training operators beside the step, as one block of the 32-layer
     transformer set runs them on 16384 tokens: dropout + residual add + layer
@@ -496,10 +553,10 @@ def main() -> int:
     ap.add_argument("--no-cpu-baseline", action="store_true")
     ap.add_argument("--no-extra", action="store_true",
                     help="skip the other workloads' whole-step figures reported beside the headline")
-    ap.add_argument("--op", default="step", choices=["step", "ns", "shard_update", "adamw", "block"],
+    ap.add_argument("--op", default="step", choices=["step", "ns", "shard_update", "adamw", "block", "ends"],
                     help="step: the Muon step (default); ns: muon_ns alone on the workload; "
                          "shard_update / adamw: the companion kernels; "
-                         "block: the training operators beside the step")
+                         "block: the training operators beside the step; ends: those at the two ends of one")
     ap.add_argument("--adamw-elems", type=int, default=0,
                     help="adamw: total elements of a 64-tensor stress set instead of the model's gains")
     ap.add_argument("--copy-probe", type=int, default=0, metavar="BYTES",
@@ -528,6 +585,9 @@ def main() -> int:
 
     if args.op == "block":
         print(json.dumps(bench_block(args.steps or 100, args.warmup or 10)), flush=True)
+        return 0
+    if args.op == "ends":
+        print(json.dumps(bench_ends(args.steps or 50, args.warmup or 5)), flush=True)
         return 0
 
     import torch

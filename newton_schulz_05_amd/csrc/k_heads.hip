@@ -252,6 +252,12 @@ template <int RAG, bool BACK, typename T, bool INTER> __device__ __forceinline__
   }
 }
 
+// A group of rows a workgroup, queries' workgroups before the keys'.  Bound by
+// memory: 4 x 4096 tokens of 32 + 8 heads of 128 bf16, slices of a projection's
+// output to heads before tokens, 66 us, 5.1 TB/s of the bytes that it cannot do
+// without; 285 instructions a wave, 57 % of the cycles.  Two and four groups a
+// workgroup 68.8 and 69.1 (the graph of that call 67.9), rows in the order of the
+// output instead of the input 79, tiles of 4 heads by 8 tokens 73.
 template <typename T, int LANES, bool INTER, int RAG>
 __global__ __launch_bounds__(WG) void heads_fwd_kernel(HeadArgs a) {
   constexpr int ROWS = WG / LANES;
@@ -283,6 +289,13 @@ __global__ __launch_bounds__(WG) void heads_fwd_kernel(HeadArgs a) {
   }
 }
 
+// At most kHeadMaxParts workgroups take every h.wgs-th group of rows and keep the
+// sums of dgamma in registers.  r is formed again from x, which is read anyway.
+// Bound by memory for many rows: 2 x 8192 tokens of 64 + 8 heads of 128 bf16 166 us,
+// 5.5 TB/s, and 5 for the join; 49 % of the cycles are instructions.  768
+// workgroups 173 (of a graph's 172), 512 185, 2048 199; with the next rows' loads
+// in flight over the sums 173 with 768 workgroups, 205 with 1024 (three waves a
+// SIMD instead of four).  64 tokens: 7.2 us, launches and latency.
 template <typename T, int LANES, bool INTER, int RAG>
 __global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
   constexpr int ROWS = WG / LANES, WAVES = WG / 64;
@@ -351,7 +364,7 @@ __global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
   }
 }
 
-// Joins the workgroups' sums: 16 columns a workgroup, 64 slices of the at most
+// Joins the workgroups' sums (5 us for 1024 of 128 columns): 16 columns a workgroup, 64 slices of the at most
 // 1024 parts, whose at most 16 loads are in flight at once; the slices of a wave
 // are joined across its lanes, the waves in order.  blockIdx.y 0 for queries, 1
 // for keys.

@@ -61,7 +61,11 @@ __device__ __forceinline__ void put_row(const LogpArgs& a, int64_t row, MaxSum r
 }
 
 // NT threads take a row, or with a.parts > 1 every a.parts-th run of pieces of
-// it; U pieces a thread are in flight at once.
+// it; U pieces a thread are in flight at once.  One pass: every piece raises the
+// thread's maximum first and then adds its terms, so that the old sum is scaled
+// once for 4 or 8 elements.  Long rows are bound by memory: 8192 x 65536 bf16
+// 162 us, 6.6 TB/s; two thirds of the cycles are instructions, of which the exponential is
+// the largest part (8.5 an element, it counts four).
 template <typename T, int NT, int WG, int U, bool STREAM>
 __global__ __launch_bounds__(WG) void logp_fwd_kernel(LogpArgs a) {
   constexpr int ROWS = WG / NT, NW = NT / 64, N = Piece<T>::N;
@@ -199,7 +203,8 @@ __global__ __launch_bounds__(64) void logp_join_kernel(LogpArgs a, bool bf16) {
 }
 
 // NT threads take U NT pieces of a row; blockIdx.x counts these along it,
-// blockIdx.y the rows.
+// blockIdx.y the rows.  Bound by memory: 8192 x 65536 bf16, a tenth of the rows
+// without a target, 331 us, 6.2 TB/s; rows at odd addresses (4096 x 65521) 212 us, 5.1.
 template <typename T, int NT, int WG, int U, bool STREAM>
 __global__ __launch_bounds__(WG) void logp_bwd_kernel(LogpBwdArgs a) {
   constexpr int ROWS = WG / NT, N = Piece<T>::N;

@@ -41,6 +41,10 @@ __device__ __forceinline__ void put_policy(const PolicyArgs& a, const double (&s
   }
 }
 
+// A token a thread at a time; the workgroups' sums are joined by a second launch.
+// Launches and latency: 777 tokens 3.8 us, 262144 5.6 and 1.6 for the join (1.2 us
+// of bytes), a million 12.2.  With a reduction for each of the three sums instead
+// of one for all the 262144 took 6.9 and 2.2.
 constexpr int kPolicyThreads = 1024;
 __global__ __launch_bounds__(kPolicyThreads) void policy_kernel(PolicyArgs a) {
   __shared__ double red[kPolicyThreads / 64][3];
@@ -175,6 +179,9 @@ __device__ __forceinline__ double put_pair(const PrefArgs& a, int64_t i, const P
   return p.w != 0.0 ? p.w * ((1.0 - a.smoothing) * softplus(-p.m) + a.smoothing * softplus(p.m)) : 0.0;
 }
 
+// 96 pairs of 4096 tokens: 5.4 us, and 5.7 for pref_grad_kernel, where the bytes
+// take 1.8; both are launch and latency.  With 2048 tokens a chunk instead of 512
+// the longest answers' workgroups took 14.6.
 __global__ __launch_bounds__(kPrefThreads) void pref_sum_kernel(PrefArgs a) {
   __shared__ double red[kPrefThreads / 64][2];
   const int64_t s = blockIdx.x;
@@ -248,7 +255,8 @@ __global__ __launch_bounds__(kPrefThreads) void pref_grad_kernel(PrefArgs a) {
   put_run(a, r, threadIdx.x, kPrefThreads, grad);
 }
 
-// Few pairs of few tokens: one workgroup, a wave a sequence.
+// Few pairs of few tokens: one workgroup, a wave a sequence (4 pairs of 300 5.2 us
+// in a graph, 5.8 with two launches, and 4 us less on the host).
 __global__ __launch_bounds__(1024) void pref_lone_kernel(PrefArgs a) {
   static_assert(2 * kPrefLonePairs <= 16);
   __shared__ double sums[16][2];

@@ -142,6 +142,8 @@ inline int logp_parts(int64_t rows, int64_t vocab) {
 constexpr int64_t kLossMaxTokens = int64_t(1) << 40;
 constexpr int64_t kPrefMaxPairs = int64_t(1) << 20;
 constexpr int kPolicyMaxParts = 256, kPrefMaxChunks = 64;
+// One workgroup up to four tokens a thread (4096: 7.2 us, 6.1 with two launches, which
+// cost the host 4 us more).
 inline int policy_parts(int64_t tokens) {
   return tokens <= 4096 ? 1 : int(std::min<int64_t>((tokens + 1023) / 1024, kPolicyMaxParts));
 }
