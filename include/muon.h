@@ -433,11 +433,11 @@ typedef struct {
  *   cos, sin         : [table_rows, rot / 2] floats; null if rot = 0.
  *   rot              : even, 0 .. dim.  interleaved: 0 or 1.
  *   positions        : null: token t of every sequence takes row t of cos and
- *                      sin; else token t of sequence b takes row
- *                      positions[b * positions_batch + t] (positions_batch = 0
- *                      for positions common to all sequences, else >= tokens).
- *                      A token whose row is outside 0 .. table_rows - 1 is not
- *                      turned. */
+ *                      sin (table_rows >= tokens); else token t of sequence b
+ *                      takes row positions[b * positions_batch + t]
+ *                      (positions_batch = 0 for positions common to all
+ *                      sequences, else >= tokens).  A token whose position is
+ *                      outside 0 .. table_rows - 1 is not turned. */
 muon_status muon_qk_norm_rope_fwd(const void* q, const muon_head_strides* s_q, const void* k,
                                   const muon_head_strides* s_k, muon_dtype dt, int64_t batch, int64_t tokens,
                                   int32_t heads_q, int32_t heads_k, int32_t dim, const void* gamma_q,

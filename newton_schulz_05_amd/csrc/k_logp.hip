@@ -126,17 +126,18 @@ __global__ __launch_bounds__(WG) void logp_fwd_kernel(LogpArgs a) {
   }
 }
 
-// Many short rows: a wave takes K of them at once, whole (cols <= 64 U pieces),
-// and finishes them together, a lane a row: the logarithms of one row cost a wave
-// as much as those of 64, and half of a row of 500.  Rows without a target are read
-// here, their values are not used.
-template <typename T, int U, int K>
+// Many short rows: LANES lanes take K of them at once, whole (cols <= LANES U
+// pieces), and finish them together, a lane a row: the logarithms of one row cost a
+// wave as much as those of 64, and half of a row of 500.  Rows without a target are
+// read here, their values are not used.
+template <typename T, int LANES, int U, int K>
 __global__ __launch_bounds__(256) void logp_short_kernel(LogpArgs a) {
-  constexpr int N = Piece<T>::N;
-  const int t = threadIdx.x & 63, cols = int(a.cols);
-  const int64_t step = int64_t(gridDim.x) * 4 * K;
-  for (int64_t row0 = (int64_t(blockIdx.x) * 4 + threadIdx.x / 64) * K; row0 < a.rows; row0 += step) {
-    // lane k looks after row k
+  constexpr int N = Piece<T>::N, GROUPS = 256 / LANES;
+  const int t = threadIdx.x % LANES, cols = int(a.cols);
+  const int64_t step = int64_t(gridDim.x) * (GROUPS * K);
+  for (int64_t first = int64_t(blockIdx.x) * (GROUPS * K); first < a.rows; first += step) {
+    const int64_t row0 = first + threadIdx.x / LANES * K;
+    // lane k of a group looks after row k
     const int64_t own = row0 + (t < K ? t : 0);
     const int64_t target = t < K && own < a.rows ? a.targets[own] : -1;
     const bool some = uint64_t(target) < uint64_t(a.cols);
@@ -147,21 +148,20 @@ __global__ __launch_bounds__(256) void logp_short_kernel(LogpArgs a) {
     for (int k = 0; k < K; ++k)
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int col = (i * 64 + t) * N;
+        const int col = (i * LANES + t) * N;
         const bool in = row0 + k < a.rows;
         raw[k][i].template load<false>((const T*)a.logits + (in ? row0 + k : 0) * a.ld + col, in ? cols - col : 0);
       }
     MaxSum mine{-INFINITY, 0.0f};
 #pragma unroll
     for (int k = 0; k < K; ++k) {
-      const int hit = __builtin_amdgcn_readlane(at, k);
-      if (hit < 0) continue;
+      const int hit = __shfl(at, (threadIdx.x & 63) / LANES * LANES + k, 64);
       float v[U * N];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
         float w[N];
         raw[k][i].get(w);
-        const int col = (i * 64 + t) * N;
+        const int col = (i * LANES + t) * N;
 #pragma unroll
         for (int j = 0; j < N; ++j) v[i * N + j] = w[j];
         if (col + N > cols || unsigned(hit - col) < unsigned(N)) {
@@ -172,12 +172,12 @@ __global__ __launch_bounds__(256) void logp_short_kernel(LogpArgs a) {
       float m = v[0];
 #pragma unroll
       for (int j = 1; j < U * N; ++j) m = fmaxf(m, v[j]);
-      m = lane_reduce<64>(m, [](float x, float y) { return fmaxf(x, y); });
+      m = lane_reduce<LANES>(m, [](float x, float y) { return fmaxf(x, y); });
       const float r = above(m);
       float s = 0.0f;
 #pragma unroll
       for (int j = 0; j < U * N; ++j) s += grow(v[j], r, a.scale2);
-      s = lane_sum<64>(s);
+      s = lane_sum<LANES>(s);
       if (t == k) mine = {m, s};
     }
     if (t < K && own < a.rows) put_row(a, own, mine, some, xt);
@@ -262,10 +262,10 @@ hipError_t run_logp_fwd(const LogpArgs& a, bool bf16, hipStream_t st) {
     hipLaunchKernelGGL((logp_fwd_kernel<decltype(t), NT, WG, decltype(u)::value, decltype(stream)::value>),
                        dim3(unsigned(std::min(groups, kOpsMaxGrid) * a.parts)), dim3(WG), 0, st, a);
   };
-  auto shorts = [&](auto t, auto u, auto k) {
-    constexpr int U = decltype(u)::value, K = decltype(k)::value;
-    const int64_t groups = (a.rows + 4 * K - 1) / (4 * K);
-    hipLaunchKernelGGL((logp_short_kernel<decltype(t), U, K>), dim3(unsigned(std::min(groups, kOpsMaxGrid))), dim3(256), 0,
+  auto shorts = [&](auto t, auto l, auto u, auto k) {
+    constexpr int L = decltype(l)::value, U = decltype(u)::value, K = decltype(k)::value, EACH = 256 / L * K;
+    const int64_t groups = (a.rows + EACH - 1) / EACH;
+    hipLaunchKernelGGL((logp_short_kernel<decltype(t), L, U, K>), dim3(unsigned(std::min(groups, kOpsMaxGrid))), dim3(256), 0,
                        st, a);
   };
   auto by_cols = [&](auto t) {
@@ -280,11 +280,14 @@ hipError_t run_logp_fwd(const LogpArgs& a, bool bf16, hipStream_t st) {
     // four).
     constexpr int N = Piece<decltype(t)>::N;
     const bool many = a.rows >= 4096;
-    if (a.rows >= 16384 && a.cols <= 128 * N) {
-      // 30000 x 500 bf16 13.7 us, 18.7 with a wave for each row, 60000 x 128 18.0 and
-      // 32.0, 32768 x 1000 17.3 and 23.2; eight and four rows 14.4, 18.0 and 17.9; but
-      // 8192 x 1000 7.8 and 7.6, 5000 x 500 6.7 and 5.0.
-      a.cols <= 64 * N ? shorts(t, Num<1>{}, Num<4>{}) : shorts(t, Num<2>{}, Num<2>{});
+    if (a.rows >= 4096 && a.cols <= 32 * N) {
+      // 60000 x 100 bf16 8.8 us, 19.3 with 64 lanes a row; 60000 x 256 10.4 and 18.2
+      a.cols <= 16 * N ? shorts(t, Num<16>{}, Num<1>{}, Num<4>{}) : shorts(t, Num<16>{}, Num<2>{}, Num<2>{});
+    } else if (a.rows >= 16384 && a.cols <= 128 * N) {
+      // 30000 x 500 bf16 12.1 us, 18.7 with a wave for each row, 13.7 with a wave for
+      // four; 32768 x 1000 17.3 and 23.2; but 8192 x 1000 7.8 and 7.6 with a wave for
+      // each, 5000 x 500 6.7 and 5.0.
+      a.cols <= 64 * N ? shorts(t, Num<16>{}, Num<4>{}, Num<2>{}) : shorts(t, Num<64>{}, Num<2>{}, Num<2>{});
     } else if (a.cols <= 64 * N || (a.cols <= 2048 && !many)) go(t, Num<64>{}, Num<1>{}, Flag<false>{});
     else if (a.cols <= 1024 * N && many) go(t, Num<64>{}, Num<2>{}, Flag<false>{});
     else if (a.cols > 1024 * N && a.rows < kLogpFewRows && a.parts == 1) go(t, Num<512>{}, Num<4>{}, Flag<false>{});
@@ -306,7 +309,13 @@ hipError_t run_logp_bwd(const LogpBwdArgs& args, bool bf16, hipStream_t st) {
                        dim3(unsigned(runs), unsigned(std::min<int64_t>(groups, 65535))), dim3(WG), 0, st, a);
   };
   auto by_cols = [&](auto t) {
-    if (a.cols <= 256 * Piece<decltype(t)>::N) go(t, Num<64>{}, Num<1>{}, Flag<false>{});
+    // The fewest lanes that hold a row of up to 32 pieces: 60000 x 100 bf16 8.0 us, 19.7
+    // with 64 lanes; 60000 x 256 13.0 and 19.1.  Two and four rows a lane at once:
+    // no gain.
+    constexpr int N = Piece<decltype(t)>::N;
+    if (a.cols <= 16 * N) go(t, Num<16>{}, Num<1>{}, Flag<false>{});
+    else if (a.cols <= 32 * N) go(t, Num<32>{}, Num<1>{}, Flag<false>{});
+    else if (a.cols <= 256 * N) go(t, Num<64>{}, Num<1>{}, Flag<false>{});
     else if (a.rows * a.cols * int64_t(sizeof(t)) > kStreamIn) go(t, Num<256>{}, Num<4>{}, Flag<true>{});
     else go(t, Num<256>{}, Num<4>{}, Flag<false>{});
   };

@@ -224,6 +224,8 @@ muon_status check_heads(muon_dtype dt, muon_dtype param_dt, int64_t batch, int64
   if (rot > 0) {
     if (table_rows < 0 || table_rows > kMaxExtent / rot) return fail(MUON_ERR_SHAPE, detail, "table_rows is out of range");
     if (table_rows > 0 && (!cos || !sin)) return fail(MUON_ERR_INVALID_ARG, detail, "cos or sin is null");
+    if (!positions && batch > 0 && table_rows < tokens)
+      return fail(MUON_ERR_SHAPE, detail, "cos and sin have fewer rows than there are tokens");
     if (positions && batch > 1 && positions_batch != 0 && positions_batch < tokens)
       return fail(MUON_ERR_INVALID_ARG, detail, "positions_batch must be 0 or at least tokens");
     if (positions_batch < 0 || (batch > 1 && positions_batch > kMaxExtent / batch))

@@ -404,7 +404,7 @@ def qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, q_out, k_out, *, positions=No
     output, transposed ones); k, gamma_k and k_out may be None.  cos and sin:
     [table rows, rot / 2] float32, or None for no rotation.  positions: int64,
     [batch, tokens] or [tokens] (None: 0, 1, ...): the rows of cos and sin; a
-    token whose row does not exist is not turned.  q_out may be q itself, k_out k
+    token whose position has no row is not turned.  q_out may be q itself, k_out k
     itself."""
     shape, dt, keys = q.shape, q.dtype, None if k is None else k.shape
     batch, tokens, hq, hk, dim = _head_sizes(shape, keys)

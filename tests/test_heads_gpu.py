@@ -80,7 +80,7 @@ def _case(dim, rot, inter, dt, wdt, b=2, t=5, hq=3, hk=1, lx="plain", ly="plain"
     q, k = (_in(lx, draw((b, t, h, dim), seed + i, 1.3, 0.2), dt) for i, h in enumerate((hq, hk)))
     dqo, dko = (_in(ly, draw((b, t, h, dim), seed + 5 + i, 0.4), dt) for i, h in enumerate((hq, hk)))
     gq, gk = (draw((dim,), seed + 10 + i, 0.3, 1.0, DTYPES[wdt]).to(DEV) if gains else None for i in range(2))
-    cos, sin, cn, sn = _angles(rot)
+    cos, sin, cn, sn = _angles(rot, max(97, t) if positions is None else 97)
     pos = None if positions is None else torch.as_tensor(positions).to(DEV)
     c, s = R.token_angles(cn, sn, rot, b, t, None if pos is None else pos.cpu().numpy())
     kw = dict(positions=pos, interleaved=inter, eps=EPS)
@@ -151,13 +151,17 @@ def test_positions():
     qk_norm_rope(q, None, None, None, cos, sin, out, None, positions=wide[:, 4:9], eps=EPS)
     qk_norm_rope(q, None, None, None, cos, sin, want, None, positions=wide[:, 4:9].contiguous(), eps=EPS)
     assert torch.equal(out, want)
-    # an empty table turns nothing; fewer rows than tokens turn those that have one
-    qk_norm_rope(q, None, None, None, cos[:0], sin[:0], out, None, eps=EPS)
+    # a table without rows turns nothing, one that ends early those that have a row
+    at = torch.arange(5, device=DEV)
+    qk_norm_rope(q, None, None, None, cos[:0], sin[:0], out, None, positions=at, eps=EPS)
     # (not the bits of a call without a table, whose lanes hold other elements: the squares' sum has another order)
     qk_norm_rope(q, None, None, None, cos, sin, want, None, positions=torch.full((5,), -1, device=DEV), eps=EPS)
     assert torch.equal(out, want)
-    qk_norm_rope(q, None, None, None, cos[:3].contiguous(), sin[:3].contiguous(), out, None, eps=EPS)
+    qk_norm_rope(q, None, None, None, cos[:3].contiguous(), sin[:3].contiguous(), out, None, positions=at, eps=EPS)
     assert torch.equal(out[:, 3:], want[:, 3:]) and not torch.equal(out[:, 1:3], want[:, 1:3])
+    with pytest.raises(MuonError) as e:  # without positions every token has to have a row
+        qk_norm_rope(q, None, None, None, cos[:3].contiguous(), sin[:3].contiguous(), out, None, eps=EPS)
+    assert e.value.status == 2
 
 
 def test_far_positions():
@@ -309,7 +313,7 @@ def test_large_outputs():
 
 def test_two_host_threads():
     import threading
-    cos, sin, _, _ = _angles(64)
+    cos, sin, _, _ = _angles(64, 500)
     g = draw((64,), 80, 0.1, 1.0).to(DEV)
     sets, bad = [], []
     for i in range(2):

@@ -209,11 +209,11 @@ def test_strides_workspaces_and_repeats(rows, vocab, dt):
 
 
 @pytest.mark.parametrize("dt", ["f32", "bf16"])
-@pytest.mark.parametrize("vocab", [1, 5, 100, 256, 257, 500, 512, 700, 1000, 1024])
-def test_many_short_rows(vocab, dt):
+@pytest.mark.parametrize("rows", [4097, 16387])
+@pytest.mark.parametrize("vocab", [1, 5, 64, 65, 100, 128, 129, 256, 257, 500, 512, 700, 1000, 1024])
+def test_many_short_rows(vocab, rows, dt):
     """Rows that a wave takes several of, whole: values, masks and strides as in
     the other forms."""
-    rows = 16387
     x, t = _logits(rows, vocab, dt, 71), _targets(rows, vocab, 72, 0.3)
     if vocab > 4:
         x[torch.rand(rows, vocab, generator=torch.Generator().manual_seed(2)).to(DEV) < 0.2] = -INF
