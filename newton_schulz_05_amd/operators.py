@@ -326,8 +326,17 @@ def _head_strides(stride: Tuple[int, ...], dim: int):
     return s, ctypes.addressof(s)
 
 
-def _heads(t: torch.Tensor, shape, dt: torch.dtype, what: str):
-    """Strides' structure of a tensor of heads of this shape and dtype."""
+# The operators from here on check an argument's device with the argument itself,
+# against that of the call's first tensor, and that one at the end (_stream): one
+# look at each tensor instead of two.
+
+def _elsewhere(t: torch.Tensor, what: str, dev: int) -> MuonError:
+    return MuonError(1, f"{what} is on device {t.get_device()}, expected {dev}" if t.get_device() >= 0
+                     else "every tensor must be a device tensor")
+
+
+def _heads(t: torch.Tensor, shape, dt: torch.dtype, what: str, dev: int):
+    """Strides' structure of a tensor of heads of this shape, dtype and device."""
     if t.shape != shape:
         raise MuonError(2, f"{what} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype is not dt:
@@ -335,7 +344,59 @@ def _heads(t: torch.Tensor, shape, dt: torch.dtype, what: str):
     s = _head_strides(t.stride(), shape[-1])
     if s is None:
         raise MuonError(1, f"{what}: the last dimension is not contiguous")
+    if t.get_device() != dev:
+        raise _elsewhere(t, what, dev)
     return s
+
+
+def _gain(t: Optional[torch.Tensor], dt: torch.dtype, n: int, what: str, dev: int) -> Optional[int]:
+    """_param, with the device."""
+    if t is None:
+        return None
+    if t.dtype is dt and t.numel() == n and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _param(t, dt, n, what)
+    raise _elsewhere(t, what, dev)
+
+
+def _vec(t: Optional[torch.Tensor], n: int, what: str, dev: int) -> Optional[int]:
+    """_flat of a float32 argument, with the device."""
+    if t is None:
+        return None
+    if t.dtype is torch.float32 and t.numel() == n and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _flat(t, n, _F32, what)
+    raise _elsewhere(t, what, dev)
+
+
+def _words(t: Optional[torch.Tensor], n: int, what: str, dev: int) -> Optional[int]:
+    """_flat of an int64 argument, with the device."""
+    if t is None:
+        return None
+    if t.dtype is torch.int64 and t.numel() == n and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    _flat(t, n, _WORD, what)
+    raise _elsewhere(t, what, dev)
+
+
+def _stream(stream, dev: int) -> int:
+    """Stream handle of a call on device `dev` (see _device)."""
+    if dev < 0:
+        raise MuonError(1, "every tensor must be a device tensor")
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(dev)
+    if stream.device.index != dev:
+        raise MuonError(1, f"a stream of {stream.device} for tensors on device {dev}")
+    return stream.cuda_stream
+
+
+def _scratch(given: Optional[torch.Tensor], need: int, stream, dev: int, handle: int):
+    """_workspace, with the device."""
+    if given is None and need == 0:
+        return None, None, 0
+    if given is not None and given.get_device() != dev:
+        raise _elsewhere(given, "workspace", dev)
+    return _workspace(given, need, stream, dev, handle)
 
 
 def _head_sizes(shape, keys) -> Tuple[int, int, int, int, int]:
@@ -354,7 +415,7 @@ def _head_sizes(shape, keys) -> Tuple[int, int, int, int, int]:
     return batch, tokens, hq, keys[-2], dim
 
 
-def _angles(cos, sin, positions, batch: int, tokens: int) -> Tuple:
+def _angles(cos, sin, positions, batch: int, tokens: int, dev: int) -> Tuple:
     """(cos, sin, table rows, rot, positions, their batch stride)."""
     if cos is None or sin is None:
         if cos is not sin:
@@ -364,7 +425,7 @@ def _angles(cos, sin, positions, batch: int, tokens: int) -> Tuple:
     if len(shape) != 2 or sin.shape != shape:
         raise MuonError(2, f"cos and sin have shapes {tuple(shape)} and {tuple(sin.shape)}, expected [table rows, rot / 2]")
     rows, half = shape
-    c, s = _vec(cos, rows * half, "cos"), _vec(sin, rows * half, "sin")
+    c, s = _vec(cos, rows * half, "cos", dev), _vec(sin, rows * half, "sin", dev)
     if positions is None:
         return c, s, rows, 2 * half, None, 0
     if positions.dtype is not torch.int64:
@@ -380,16 +441,9 @@ def _angles(cos, sin, positions, batch: int, tokens: int) -> Tuple:
         raise MuonError(2, f"positions has shape {tuple(shape)}, expected ({tokens},) or ({batch}, {tokens})")
     if tokens > 1 and stride[-1] != 1:
         raise MuonError(1, "positions: the last dimension is not contiguous")
+    if positions.get_device() != dev:
+        raise _elsewhere(positions, "positions", dev)
     return c, s, rows, 2 * half, positions.data_ptr(), each
-
-
-def _vec(t: Optional[torch.Tensor], n: int, what: str) -> Optional[int]:
-    """_flat of a float32 argument, with less to do when nothing is wrong."""
-    if t is None:
-        return None
-    if t.dtype is torch.float32 and t.numel() == n and t.is_contiguous():
-        return t.data_ptr()
-    return _flat(t, n, _F32, what)
 
 
 _NO_STRIDES = (None, None)
@@ -408,7 +462,8 @@ def qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, q_out, k_out, *, positions=No
     itself."""
     shape, dt, keys = q.shape, q.dtype, None if k is None else k.shape
     batch, tokens, hq, hk, dim = _head_sizes(shape, keys)
-    sq, sqo = _heads(q, shape, dt, "q"), _heads(q_out, shape, dt, "q_out")
+    dev = q.get_device()
+    sq, sqo = _heads(q, shape, dt, "q", dev), _heads(q_out, shape, dt, "q_out", dev)
     if k is None:
         if k_out is not None:
             raise MuonError(1, "k and k_out come together")
@@ -417,12 +472,12 @@ def qk_norm_rope(q, k, gamma_q, gamma_k, cos, sin, q_out, k_out, *, positions=No
     else:
         if k_out is None:
             raise MuonError(1, "k and k_out come together")
-        sk, sko = _heads(k, keys, dt, "k"), _heads(k_out, keys, dt, "k_out")
+        sk, sko = _heads(k, keys, dt, "k", dev), _heads(k_out, keys, dt, "k_out", dev)
         kp, kop = k.data_ptr(), k_out.data_ptr()
     wdt = _param_dtype(q, gamma_q, gamma_k)
-    gq, gk = _param(gamma_q, wdt, dim, "gamma_q"), _param(gamma_k, wdt, dim, "gamma_k")
-    c, s, rows, rot, pos, each = _angles(cos, sin, positions, batch, tokens)
-    dev, st = _device(stream, q, k, gamma_q, gamma_k, cos, sin, positions, q_out, k_out)
+    gq, gk = _gain(gamma_q, wdt, dim, "gamma_q", dev), _gain(gamma_k, wdt, dim, "gamma_k", dev)
+    c, s, rows, rot, pos, each = _angles(cos, sin, positions, batch, tokens, dev)
+    st = _stream(stream, dev)
     _call(dev, load_library().muon_qk_norm_rope_fwd, q.data_ptr(), sq[1], kp, sk[1], _dtype_code(dt), batch, tokens, hq, hk,
           dim, gq, gk, _dtype_code(wdt), eps, c, s, rows, rot, 1 if interleaved else 0, pos, each, q_out.data_ptr(), sqo[1],
           kop, sko[1], st)
@@ -444,7 +499,8 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, dq, 
     may be dq_out itself, dk dk_out itself."""
     shape, dt, keys = q.shape, q.dtype, None if k is None else k.shape
     batch, tokens, hq, hk, dim = _head_sizes(shape, keys)
-    sq, sdqo, sdq = _heads(q, shape, dt, "q"), _heads(dq_out, shape, dt, "dq_out"), _heads(dq, shape, dt, "dq")
+    dev = q.get_device()
+    sq, sdqo, sdq = _heads(q, shape, dt, "q", dev), _heads(dq_out, shape, dt, "dq_out", dev), _heads(dq, shape, dt, "dq", dev)
     if k is None:
         if dk_out is not None or dk is not None:
             raise MuonError(1, "k, dk_out and dk come together")
@@ -453,16 +509,15 @@ def qk_norm_rope_backward(dq_out, dk_out, q, k, gamma_q, gamma_k, cos, sin, dq, 
     else:
         if dk_out is None or dk is None:
             raise MuonError(1, "k, dk_out and dk come together")
-        sk, sdko, sdk = _heads(k, keys, dt, "k"), _heads(dk_out, keys, dt, "dk_out"), _heads(dk, keys, dt, "dk")
+        sk, sdko, sdk = _heads(k, keys, dt, "k", dev), _heads(dk_out, keys, dt, "dk_out", dev), _heads(dk, keys, dt, "dk", dev)
         kp, dkop, dkp = k.data_ptr(), dk_out.data_ptr(), dk.data_ptr()
     wdt = _param_dtype(q, gamma_q, gamma_k, dgamma_q, dgamma_k)
-    gq, gk = _param(gamma_q, wdt, dim, "gamma_q"), _param(gamma_k, wdt, dim, "gamma_k")
-    dgq, dgk = _param(dgamma_q, wdt, dim, "dgamma_q"), _param(dgamma_k, wdt, dim, "dgamma_k")
-    c, s, rows, rot, pos, each = _angles(cos, sin, positions, batch, tokens)
-    dev, st = _device(stream, q, k, dq_out, dk_out, gamma_q, gamma_k, cos, sin, positions, dq, dk, dgamma_q, dgamma_k,
-                      workspace)
+    gq, gk = _gain(gamma_q, wdt, dim, "gamma_q", dev), _gain(gamma_k, wdt, dim, "gamma_k", dev)
+    dgq, dgk = _gain(dgamma_q, wdt, dim, "dgamma_q", dev), _gain(dgamma_k, wdt, dim, "dgamma_k", dev)
+    c, s, rows, rot, pos, each = _angles(cos, sin, positions, batch, tokens, dev)
+    st = _stream(stream, dev)
     need = _heads_workspace(batch * tokens * hq, batch * tokens * hk, dim) if dgq or dgk else 0
-    keep, ws, ws_bytes = _workspace(workspace, need, stream, dev, st)
+    keep, ws, ws_bytes = _scratch(workspace, need, stream, dev, st)
     _call(dev, load_library().muon_qk_norm_rope_bwd, dq_out.data_ptr(), sdqo[1], dkop, sdko[1], q.data_ptr(), sq[1], kp,
           sk[1], _dtype_code(dt), batch, tokens, hq, hk, dim, gq, gk, _dtype_code(wdt), eps, c, s, rows, rot,
           1 if interleaved else 0, pos, each, dq.data_ptr(), sdq[1], dkp, sdk[1], dgq, dgk, ws, ws_bytes, st)
@@ -481,10 +536,11 @@ def token_logp(logits, targets, logp, lse, *, scale: float = 1.0, workspace: Opt
     the softmax's sum (muon_token_logp_fwd).  targets: int64, one a token; one
     outside the vocabulary (a prompt or padding token) gives 0 in both."""
     rows, vocab, ld = _matrix(logits, "logits")
-    t = _flat(targets, rows, _WORD, "targets")
-    lp, ls = _vec(logp, rows, "logp"), _vec(lse, rows, "lse")
-    dev, st = _device(stream, logits, targets, logp, lse, workspace)
-    keep, ws, ws_bytes = _workspace(workspace, _logp_workspace(rows, vocab), stream, dev, st)
+    dev = logits.get_device()
+    t = _words(targets, rows, "targets", dev)
+    lp, ls = _vec(logp, rows, "logp", dev), _vec(lse, rows, "lse", dev)
+    st = _stream(stream, dev)
+    keep, ws, ws_bytes = _scratch(workspace, _logp_workspace(rows, vocab), stream, dev, st)
     _call(dev, load_library().muon_token_logp_fwd, logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, vocab, t,
           scale, lp, ls, ws, ws_bytes, st)
 
@@ -494,10 +550,13 @@ def token_logp_backward(logits, targets, logp, lse, dlogp, dlogits, *, scale: fl
     the logp and lse that it wrote and the gradient dlogp that reaches logp.
     dlogits may be logits itself."""
     rows, vocab, ld = _matrix(logits, "logits")
+    dev = logits.get_device()
     ld_d = _same(dlogits, logits, "dlogits")
-    t = _flat(targets, rows, _WORD, "targets")
-    lp, ls, d = _vec(logp, rows, "logp"), _vec(lse, rows, "lse"), _vec(dlogp, rows, "dlogp")
-    dev, st = _device(stream, logits, targets, logp, lse, dlogp, dlogits)
+    if dlogits.get_device() != dev:
+        raise _elsewhere(dlogits, "dlogits", dev)
+    t = _words(targets, rows, "targets", dev)
+    lp, ls, d = _vec(logp, rows, "logp", dev), _vec(lse, rows, "lse", dev), _vec(dlogp, rows, "dlogp", dev)
+    st = _stream(stream, dev)
     _call(dev, load_library().muon_token_logp_bwd, logits.data_ptr(), ld, _dtype_code(logits.dtype), rows, vocab, t,
           scale, lp, ls, d, dlogits.data_ptr(), ld_d, st)
 
@@ -518,13 +577,13 @@ def policy_loss(logp, old_logp, advantages, loss, *, ref_logp=None, weight=None,
     None: logp itself (ratio 1); ref_logp None: no KL term; dloss, a device
     float: what dlogp is multiplied by.  terms receives the policy sum, the KL sum
     and the weight of the clipped tokens."""
-    n = logp.numel()
-    lp, ol = _vec(logp, n, "logp"), _vec(old_logp, n, "old_logp")
-    rf, ad = _vec(ref_logp, n, "ref_logp"), _vec(advantages, n, "advantages")
-    w, g = _vec(weight, n, "weight"), _vec(dlogp, n, "dlogp")
-    up, lo, tm = _vec(dloss, 1, "dloss"), _vec(loss, 1, "loss"), _vec(terms, 3, "terms")
-    dev, st = _device(stream, logp, old_logp, ref_logp, advantages, weight, dlogp, dloss, loss, terms, workspace)
-    keep, ws, ws_bytes = _workspace(workspace, _policy_workspace(n), stream, dev, st)
+    n, dev = logp.numel(), logp.get_device()
+    lp, ol = _vec(logp, n, "logp", dev), _vec(old_logp, n, "old_logp", dev)
+    rf, ad = _vec(ref_logp, n, "ref_logp", dev), _vec(advantages, n, "advantages", dev)
+    w, g = _vec(weight, n, "weight", dev), _vec(dlogp, n, "dlogp", dev)
+    up, lo, tm = _vec(dloss, 1, "dloss", dev), _vec(loss, 1, "loss", dev), _vec(terms, 3, "terms", dev)
+    st = _stream(stream, dev)
+    keep, ws, ws_bytes = _scratch(workspace, _policy_workspace(n), stream, dev, st)
     _call(dev, load_library().muon_policy_loss, lp, ol, rf, ad, w, n, clip_low, clip_high, beta, up, lo, tm, g, ws,
           ws_bytes, st)
 
@@ -544,15 +603,17 @@ def preference_loss(logp, offsets, loss, *, ref_logp=None, valid=None, weight=No
     answers in logp, the preferred ones of all pairs first.  valid: uint8 or bool,
     0 for tokens that do not count; weight: one a pair (None: 1 / pairs);
     rewards receives beta times each answer's log-ratio (average: its mean)."""
-    n, ends = logp.numel(), offsets.numel()
+    n, ends, dev = logp.numel(), offsets.numel(), logp.get_device()
     if ends % 2 == 0:
         raise MuonError(2, f"offsets has {ends} elements, expected 2 * pairs + 1")
     pairs = ends // 2
-    lp, rf = _vec(logp, n, "logp"), _vec(ref_logp, n, "ref_logp")
-    v, off = _flat(valid, n, _MASK, "valid"), _flat(offsets, ends, _WORD, "offsets")
-    w, rw = _vec(weight, pairs, "weight"), _vec(rewards, 2 * pairs, "rewards")
-    g, up, lo = _vec(dlogp, n, "dlogp"), _vec(dloss, 1, "dloss"), _vec(loss, 1, "loss")
-    dev, st = _device(stream, logp, ref_logp, valid, offsets, weight, rewards, dlogp, dloss, loss, workspace)
-    keep, ws, ws_bytes = _workspace(workspace, _preference_workspace(n, pairs), stream, dev, st)
+    lp, rf = _vec(logp, n, "logp", dev), _vec(ref_logp, n, "ref_logp", dev)
+    v, off = _flat(valid, n, _MASK, "valid"), _words(offsets, ends, "offsets", dev)
+    if valid is not None and valid.get_device() != dev:
+        raise _elsewhere(valid, "valid", dev)
+    w, rw = _vec(weight, pairs, "weight", dev), _vec(rewards, 2 * pairs, "rewards", dev)
+    g, up, lo = _vec(dlogp, n, "dlogp", dev), _vec(dloss, 1, "dloss", dev), _vec(loss, 1, "loss", dev)
+    st = _stream(stream, dev)
+    keep, ws, ws_bytes = _scratch(workspace, _preference_workspace(n, pairs), stream, dev, st)
     _call(dev, load_library().muon_preference_loss, lp, rf, v, n, off, pairs, w, beta, margin, smoothing,
           1 if average else 0, up, lo, rw, g, ws, ws_bytes, st)

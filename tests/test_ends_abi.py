@@ -281,3 +281,43 @@ def test_binding_rejects_loss_arguments_that_do_not_match():
     assert _status(O.preference_loss, f, off, one, rewards=torch.zeros(1)) == SHAPE
     assert _status(O.preference_loss, f, off, one, valid=torch.ones(4)) == DTYPE
     assert _status(O.preference_loss, f, off, one) == INVALID
+
+
+def test_binding_rejects_tensors_of_two_devices(monkeypatch):
+    """Every tensor's device is compared with the first one's (tensors whose device
+    is faked: nothing is launched)."""
+    class On(torch.Tensor):
+        def get_device(self):
+            return self.on
+
+    def put(t, dev):
+        t = t.as_subclass(On)
+        t.on = dev
+        return t
+
+    monkeypatch.setattr(O, "_call", lambda *a: pytest.fail("called"))
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    heads, vec, words = lambda: torch.zeros(2, 5, 4, 16), lambda n: torch.zeros(n), lambda *s: torch.zeros(*s, dtype=torch.int64)
+    calls = [
+        (O.qk_norm_rope, [heads(), heads(), vec(16), vec(16), torch.zeros(9, 8), torch.zeros(9, 8), heads(), heads()],
+         dict(positions=words(2, 5))),
+        (O.qk_norm_rope_backward, [heads(), heads(), heads(), heads(), vec(16), vec(16), torch.zeros(9, 8),
+                                   torch.zeros(9, 8), heads(), heads()],
+         dict(positions=words(2, 5), dgamma_q=vec(16), dgamma_k=vec(16), workspace=torch.zeros(1 << 16, dtype=torch.uint8))),
+        (O.token_logp, [torch.zeros(4, 70000), words(4), vec(4), vec(4)], dict(workspace=torch.zeros(1 << 16, dtype=torch.uint8))),
+        (O.token_logp_backward, [torch.zeros(4, 8), words(4), vec(4), vec(4), vec(4), torch.zeros(4, 8)], {}),
+        (O.policy_loss, [vec(5000), vec(5000), vec(5000), vec(1)],
+         dict(ref_logp=vec(5000), weight=vec(5000), dlogp=vec(5000), dloss=vec(1), terms=vec(3),
+              workspace=torch.zeros(1 << 16, dtype=torch.uint8))),
+        (O.preference_loss, [vec(500), words(61), vec(1)],
+         dict(ref_logp=vec(500), valid=torch.zeros(500, dtype=torch.uint8), weight=vec(30), rewards=vec(60), dlogp=vec(500),
+              dloss=vec(1), workspace=torch.zeros(1 << 16, dtype=torch.uint8))),
+    ]
+    for f, args, kw in calls:
+        count = len(args) + len(kw)
+        for odd in range(count):
+            a = [put(t, 1 if i == odd else 0) for i, t in enumerate(args)]
+            k = {n: put(t, 1 if len(args) + i == odd else 0) for i, (n, t) in enumerate(kw.items())}
+            assert _status(f, *a, **k) == INVALID, (f.__name__, odd)
+        # host tensors
+        assert _status(f, *args, **kw) == INVALID, f.__name__
