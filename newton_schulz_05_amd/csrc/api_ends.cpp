@@ -161,8 +161,10 @@ muon_status muon_qk_norm_rope_fwd(const void* q, const muon_head_strides* s_q, c
   return guarded([&](std::string* d) {
     const HeadCall c{dt, param_dt, batch, tokens, heads_q, heads_k, dim, eps, cos, sin, table_rows, rot, interleaved,
                      positions, positions_batch};
-    const HeadTensors tq{"q", "", "q_out", "gamma_q", "", q, s_q, nullptr, nullptr, q_out, s_qo, gamma_q, nullptr, heads_q};
-    const HeadTensors tk{"k", "", "k_out", "gamma_k", "", k, s_k, nullptr, nullptr, k_out, s_ko, gamma_k, nullptr, heads_k};
+    const HeadTensors tq{"q", "", "q_out", "gamma_q", "", q, s_q, nullptr, nullptr, q_out, s_qo, gamma_q, nullptr,
+                         heads_q};
+    const HeadTensors tk{"k", "", "k_out", "gamma_k", "", k, s_k, nullptr, nullptr, k_out, s_ko, gamma_k, nullptr,
+                         heads_k};
     return heads(c, tq, tk, false, nullptr, 0, stream, d);
   });
 }

@@ -22,8 +22,8 @@ namespace api {
 
 inline int64_t elem(muon_dtype dt) { return dt == MUON_BF16 ? 2 : 4; }
 
-inline Operand matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, muon_dtype dt, bool written,
-               bool optional = false) {
+inline Operand matrix(const char* name, const void* p, int64_t rows, int64_t cols, int64_t ld, muon_dtype dt,
+                      bool written, bool optional = false) {
   return {name, p, rows, cols * elem(dt), ld * elem(dt), int(elem(dt)), written, optional};
 }
 // n elements of `size` bytes.

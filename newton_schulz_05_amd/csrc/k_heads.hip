@@ -8,8 +8,8 @@
 //             dx = r (g gamma - x r mean(g gamma x r))
 //
 // A head's row is read once and held by 4 to 64 lanes, 16 elements each.  Both
-// elements of a pair are one lane's, so turning needs no exchange between lanes.  Sums are fp32; each output is rounded
-// once.
+// elements of a pair are one lane's, so turning needs no exchange between lanes.
+// Sums are fp32; each output is rounded once.
 #include "ops_dev.hpp"
 
 #include <type_traits>
@@ -35,7 +35,9 @@ __device__ __forceinline__ uint32_t quotient(uint32_t r, const FastDiv& f) {
 // which segments shorter than a piece leave, take three times the instructions:
 // 2 x 4096 tokens of 24 + 8 heads of 90 bf16 50 us forward with them, 38 so.)
 enum Ragged { kWhole, kRaggedAngles, kOverlap, kRagged };
-constexpr bool ragged_angles(int rag, bool inter) { return rag == kRaggedAngles || rag == kRagged || (rag == kOverlap && inter); }
+constexpr bool ragged_angles(int rag, bool inter) {
+  return rag == kRaggedAngles || rag == kRagged || (rag == kOverlap && inter);
+}
 
 // What a lane holds of every row: 16 elements in pieces of 16 bytes, n[i] of
 // them at column c[i], the first skip[i] of which another lane counts.  A
@@ -81,15 +83,18 @@ template <int RAG, typename T, bool INTER> __device__ __forceinline__ LanePart<T
 template <typename T> struct Held {
   Piece<T> r[LanePart<T>::P];
 };
-template <int RAG, typename T> __device__ __forceinline__ void load_held(const T* row, const LanePart<T>& p, bool live, int dim, Held<T>& h) {
+template <int RAG, typename T>
+__device__ __forceinline__ void load_held(const T* row, const LanePart<T>& p, bool live, int dim, Held<T>& h) {
 #pragma unroll
   for (int i = 0; i < LanePart<T>::P; ++i) {
     const int n = live ? p.n[i] : 0;
-    if constexpr (RAG == kRagged && sizeof(T) == 2) h.r[i].r = load_row8(row, unsigned(p.c[i]), n > 0 ? dim - p.c[i] : 0, dim);
+    if constexpr (RAG == kRagged && sizeof(T) == 2)
+      h.r[i].r = load_row8(row, unsigned(p.c[i]), n > 0 ? dim - p.c[i] : 0, dim);
     else h.r[i].template load<false>(row + p.c[i], RAG == kRagged ? n : (n > 0 ? LanePart<T>::E : 0));
   }
 }
-template <int RAG, typename T> __device__ __forceinline__ void unpack_held(Held<T> h, const LanePart<T>& p, bool live, int dim, float (&v)[16]) {
+template <int RAG, typename T>
+__device__ __forceinline__ void unpack_held(Held<T> h, const LanePart<T>& p, bool live, int dim, float (&v)[16]) {
   constexpr int E = LanePart<T>::E;
 #pragma unroll
   for (int i = 0; i < LanePart<T>::P; ++i) {
@@ -102,7 +107,8 @@ template <int RAG, typename T> __device__ __forceinline__ void unpack_held(Held<
   }
 }
 // The elements that this lane counts, 0 for the others.
-template <int RAG, typename T> __device__ __forceinline__ void counted(const LanePart<T>& p, const float (&v)[16], float (&w)[16]) {
+template <int RAG, typename T>
+__device__ __forceinline__ void counted(const LanePart<T>& p, const float (&v)[16], float (&w)[16]) {
   constexpr int E = LanePart<T>::E;
 #pragma unroll
   for (int k = 0; k < 16; ++k) w[k] = RAG == kOverlap && k % E < p.skip[k / E] ? 0.0f : v[k];
@@ -122,7 +128,8 @@ __device__ __forceinline__ void store_held(T* row, const LanePart<T>& p, bool li
 
 // gamma, in fp32 whatever it is stored in; 1 if null.  Ragged pieces are read
 // like those of a row of dim.
-template <int RAG, int E, typename W> __device__ __forceinline__ void load_gamma(const W* gamma, int col, int n, int dim, float* v) {
+template <int RAG, int E, typename W>
+__device__ __forceinline__ void load_gamma(const W* gamma, int col, int n, int dim, float* v) {
   float w[8];
   Raw8<W> r;
   if constexpr (RAG == kRagged) {
@@ -183,8 +190,8 @@ __device__ __forceinline__ float inv_root(float v) {
   return rsqrtf(tiny ? v * 0x1p96f : v) * (tiny ? 0x1p48f : 1.0f);
 }
 
-// One row's place: offsets of its tensors, and the table's row of its angles
-// (-1: not turned).
+// One row's place: offsets of its tensors, and its token's word of positions (or,
+// without positions, its row of the table).
 struct Place {
   int64_t x, dy, out, pos;
 };
@@ -201,7 +208,8 @@ template <typename T, bool INTER> struct Angles {
   int n[RUNS];
 };
 template <int RAG, typename T, bool INTER>
-__device__ __forceinline__ void load_angles(const HeadArgs& a, int64_t pos, const LanePart<T>& p, bool live, Angles<T, INTER>& g) {
+__device__ __forceinline__ void load_angles(const HeadArgs& a, int64_t pos, const LanePart<T>& p, bool live,
+                                            Angles<T, INTER>& g) {
   constexpr int LEN = Angles<T, INTER>::LEN;
   const int half = a.rot / 2;
   const bool turned = live && p.turned && half > 0;
@@ -234,7 +242,8 @@ __device__ __forceinline__ void load_angles(const HeadArgs& a, int64_t pos, cons
 }
 
 // Turns a lane's elements by its angles, or back.
-template <int RAG, bool BACK, typename T, bool INTER> __device__ __forceinline__ void turn(const Angles<T, INTER>& g, float (&v)[16]) {
+template <int RAG, bool BACK, typename T, bool INTER>
+__device__ __forceinline__ void turn(const Angles<T, INTER>& g, float (&v)[16]) {
   constexpr int LEN = Angles<T, INTER>::LEN;
 #pragma unroll
   for (int i = 0; i < Angles<T, INTER>::RUNS; ++i) {
@@ -364,10 +373,10 @@ __global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
   }
 }
 
-// Joins the workgroups' sums (5 us for 1024 of 128 columns): 16 columns a workgroup, 64 slices of the at most
-// 1024 parts, whose at most 16 loads are in flight at once; the slices of a wave
-// are joined across its lanes, the waves in order.  blockIdx.y 0 for queries, 1
-// for keys.
+// Joins the workgroups' sums (5 us for 1024 of 128 columns): 16 columns a
+// workgroup, 64 slices of the at most 1024 parts, whose at most 16 loads are in
+// flight at once; the slices of a wave are joined across its lanes, the waves in
+// order.  blockIdx.y 0 for queries, 1 for keys.
 constexpr int kCols = 16, kSlices = 64;
 __global__ __launch_bounds__(kCols* kSlices) void heads_gain_kernel(HeadArgs a) {
   constexpr int EACH = (kHeadMaxParts + kSlices - 1) / kSlices, WAVES = kCols * kSlices / 64;
@@ -424,12 +433,14 @@ template <typename F> hipError_t by_kind(const HeadArgs& a, bool bf16, bool inte
   auto kind = [&](auto t) {
     constexpr int E = Piece<decltype(t)>::N;
     if (inter) {
-      if (a.dim % E == 0) half % (E / 2) != 0 ? lanes(t, std::true_type{}, RaggedAngles{}) : lanes(t, std::true_type{}, Whole{});
-      else a.dim >= E && a.dim % 2 == 0 ? lanes(t, std::true_type{}, Overlap{}) : lanes(t, std::true_type{}, AllRagged{});
+      if (a.dim % E == 0 && half % (E / 2) == 0) lanes(t, std::true_type{}, Whole{});
+      else if (a.dim % E == 0) lanes(t, std::true_type{}, RaggedAngles{});
+      else if (a.dim >= E && a.dim % 2 == 0) lanes(t, std::true_type{}, Overlap{});
+      else lanes(t, std::true_type{}, AllRagged{});
     } else {
       if (half % E == 0 && rest % E == 0) lanes(t, std::false_type{}, Whole{});
-      else (half == 0 || half >= E) && (rest == 0 || rest >= E) ? lanes(t, std::false_type{}, Overlap{})
-                                                               : lanes(t, std::false_type{}, AllRagged{});
+      else if ((half == 0 || half >= E) && (rest == 0 || rest >= E)) lanes(t, std::false_type{}, Overlap{});
+      else lanes(t, std::false_type{}, AllRagged{});
     }
   };
   bf16 ? kind(uint16_t{}) : kind(float{});
@@ -463,7 +474,8 @@ hipError_t run_heads_bwd(const HeadArgs& args, bool bf16, bool interleaved, hipS
     return hipGetLastError();
   }
   const hipError_t e = by_kind(a, bf16, interleaved, [&](auto t, auto inter, auto rag, auto lanes) {
-    hipLaunchKernelGGL((heads_bwd_kernel<decltype(t), decltype(lanes)::value, decltype(inter)::value, decltype(rag)::value>),
+    constexpr int L = decltype(lanes)::value;
+    hipLaunchKernelGGL((heads_bwd_kernel<decltype(t), L, decltype(inter)::value, decltype(rag)::value>),
                        dim3(unsigned(a.q.wgs + a.k.wgs)), dim3(WG), 0, st, a);
   });
   if (e != hipSuccess || !((a.q.dgamma && a.q.part) || (a.k.dgamma && a.k.part))) return e;

@@ -142,14 +142,15 @@ inline int logp_parts(int64_t rows, int64_t vocab) {
 constexpr int64_t kLossMaxTokens = int64_t(1) << 40;
 constexpr int64_t kPrefMaxPairs = int64_t(1) << 20;
 constexpr int kPolicyMaxParts = 256, kPrefMaxChunks = 64;
-// One workgroup up to four tokens a thread (4096: 7.2 us, 6.1 with two launches, which
-// cost the host 4 us more).
+// One workgroup up to four tokens a thread (4096: 7.2 us, 6.1 with two launches,
+// which cost the host 4 us more).
 inline int policy_parts(int64_t tokens) {
   return tokens <= 4096 ? 1 : int(std::min<int64_t>((tokens + 1023) / 1024, kPolicyMaxParts));
 }
 // The preference loss by one workgroup, a wave a sequence; else each sequence by
-// 2^shift workgroups in two launches.
-constexpr int64_t kPrefLonePairs = 8, kPrefLoneTokens = 8192;
+// 2^shift workgroups in two launches, which cost the host 4 us more.  A pair of
+// 2 x 100 tokens 3.8 us and 5.4, 2 x 2000 7.2 and 5.5, 2 x 4096 12.3 and 5.8.
+constexpr int64_t kPrefLonePairs = 8, kPrefLoneTokens = 4096;
 inline bool pref_lone(int64_t tokens, int64_t pairs) { return pairs <= kPrefLonePairs && tokens <= kPrefLoneTokens; }
 inline int pref_shift(int64_t tokens, int64_t pairs) {
   const int64_t each = tokens / std::max<int64_t>(2 * pairs, 1);

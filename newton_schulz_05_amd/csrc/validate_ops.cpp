@@ -177,7 +177,8 @@ muon_status head_operand(const char* name, const void* p, const muon_head_stride
   for (const Dim& x : d) {
     if (x.n == 1) continue;
     if (x.stride < span)
-      return fail(MUON_ERR_INVALID_ARG, detail, std::string(name) + ": the dimensions do not nest (a stride is smaller than what lies within)");
+      return fail(MUON_ERR_INVALID_ARG, detail,
+                  std::string(name) + ": the dimensions do not nest (a stride is smaller than what lies within)");
     if (x.stride > kMaxExtent / x.n) return fail(MUON_ERR_SHAPE, detail, std::string(name) + ": tensor too large");
     span += (x.n - 1) * x.stride;
   }
@@ -222,7 +223,8 @@ muon_status check_heads(muon_dtype dt, muon_dtype param_dt, int64_t batch, int64
   if (rot < 0 || rot > dim || rot % 2 != 0)
     return fail(MUON_ERR_SHAPE, detail, "rot must be even and in 0..dim");
   if (rot > 0) {
-    if (table_rows < 0 || table_rows > kMaxExtent / rot) return fail(MUON_ERR_SHAPE, detail, "table_rows is out of range");
+    if (table_rows < 0 || table_rows > kMaxExtent / rot)
+      return fail(MUON_ERR_SHAPE, detail, "table_rows is out of range");
     if (table_rows > 0 && (!cos || !sin)) return fail(MUON_ERR_INVALID_ARG, detail, "cos or sin is null");
     if (!positions && batch > 0 && table_rows < tokens)
       return fail(MUON_ERR_SHAPE, detail, "cos and sin have fewer rows than there are tokens");

@@ -1,7 +1,8 @@
 // Argument validation of the training operators' entry points (layer norm,
-// dropout, router, query and key heads, token log-probabilities, losses).  Pure C++ (no HIP calls), like validate.hpp: each function
-// returns MUON_OK, or an error status with `detail` filled, before anything is
-// enqueued, and none of them touches device memory.
+// dropout, router, query and key heads, token log-probabilities, losses).  Pure
+// C++ (no HIP calls), like validate.hpp: each function returns MUON_OK, or an
+// error status with `detail` filled, before anything is enqueued, and none of them
+// touches device memory.
 #pragma once
 
 #include <stddef.h>

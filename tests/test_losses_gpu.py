@@ -165,7 +165,7 @@ def _answers(pairs, mean, seed, lead=0, tail=0):
     return lp, rf, off
 
 
-@pytest.mark.parametrize("pairs,mean", [(1, 1), (1, 40), (3, 7), (4, 300), (8, 900), (9, 100), (40, 5), (3, 20000),
+@pytest.mark.parametrize("pairs,mean", [(1, 1), (1, 40), (3, 7), (4, 300), (8, 250), (1, 2100), (8, 900), (9, 100), (40, 5), (3, 20000),
                                         (600, 30), (1, 200000)])
 @pytest.mark.parametrize("average", [False, True])
 def test_preference(pairs, mean, average):
