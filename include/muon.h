@@ -484,7 +484,7 @@ muon_status muon_qk_norm_rope_bwd(const void* dq_out, const muon_head_strides* s
  *   targets : tokens words.  One outside 0 .. vocab - 1 (a prompt or padding
  *             token) is none: logp = lse = 0, whatever the row holds.  So is
  *             every target of a row that is -inf throughout (lse = -inf).
- *   scale   : finite, > 0: the inverse of a temperature.
+ *   scale   : > 0, at most 1e30: the inverse of a temperature.
  *   logp, lse : tokens floats each.
  *   workspace : muon_token_logp_workspace_bytes(), 16-byte aligned. */
 muon_status muon_token_logp_workspace_bytes(int64_t tokens, int64_t vocab, size_t* bytes);
