@@ -519,7 +519,8 @@ muon_status muon_token_logp_bwd(const void* logits, int64_t ld, muon_dtype dt, i
  *   weight     : tokens floats, for a mean 1 / their number; null: 1 each.  A
  *                token of weight 0 (prompt, padding) enters nothing, whatever
  *                its other values.
- *   clip_low in [0, 1], clip_high >= 0, beta: finite.
+ *   clip_low in [0, 1], clip_high >= 0, beta: finite.  With beta = 0 the KL
+ *                terms enter terms alone, infinite ones too.
  *   dloss      : one float on the device, or null for 1.
  *   loss       : one float.  terms: null, or three: the sums of weight pg, of
  *                weight kl, and of the weights of clipped tokens.
@@ -549,7 +550,9 @@ muon_status muon_policy_loss(const float* logp, const float* old_logp, const flo
  *   pairs    : 0 .. 2^20;  tokens: < 2^40.
  *   weight   : pairs floats, or null for 1 / pairs.  A pair of weight 0 enters
  *              nothing.
- *   beta, margin : finite;  smoothing in [0, 1];  average 0 or 1.
+ *   beta, margin : finite;  smoothing in [0, 1];  average 0 or 1.  With a
+ *              smoothing of 0 or 1 the term whose factor is 0 is left out, so
+ *              that an infinite m of the right sign costs nothing.
  *   dloss    : one float on the device, or null for 1.
  *   loss     : one float.  rewards: 2 pairs floats, or null.
  *   dlogp    : tokens floats, or null if not wanted; the tokens before the

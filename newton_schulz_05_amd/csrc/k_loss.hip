@@ -30,11 +30,14 @@ template <int WG, int N> __device__ __forceinline__ void block_sum(double (&v)[N
   }
 }
 
+// A term that a factor of 0 takes out, an infinite one too.
+__device__ __forceinline__ double scaled(double f, double v) { return f != 0.0 ? f * v : 0.0; }
+
 // ---- policy loss ---------------------------------------------------------------
 
 // Policy sum, KL sum and the weight of the clipped tokens.
 __device__ __forceinline__ void put_policy(const PolicyArgs& a, const double (&s)[3]) {
-  a.loss[0] = float(s[0] + a.beta * s[1]);
+  a.loss[0] = float(s[0] + scaled(a.beta, s[1]));
   if (a.terms) {
 #pragma unroll
     for (int i = 0; i < 3; ++i) a.terms[i] = float(s[i]);
@@ -63,7 +66,7 @@ __global__ __launch_bounds__(kPolicyThreads) void policy_kernel(PolicyArgs a) {
       sum[1] += w * (u == INFINITY ? u : e - u);
       sum[2] += cut ? w : 0.0;
     }
-    if (a.dlogp) a.dlogp[i] = w != 0.0 ? float(up * w * ((cut ? 0.0 : -gain) - a.beta * e)) : 0.0f;
+    if (a.dlogp) a.dlogp[i] = w != 0.0 ? float(up * w * ((cut ? 0.0 : -gain) - scaled(a.beta, e))) : 0.0f;
   }
   block_sum<kPolicyThreads>(sum, red);
   if (threadIdx.x != 0) return;
@@ -176,7 +179,7 @@ __device__ __forceinline__ double put_pair(const PrefArgs& a, int64_t i, const P
     a.rewards[i] = float(p.x.r);
     a.rewards[a.pairs + i] = float(p.y.r);
   }
-  return p.w != 0.0 ? p.w * ((1.0 - a.smoothing) * softplus(-p.m) + a.smoothing * softplus(p.m)) : 0.0;
+  return p.w != 0.0 ? p.w * (scaled(1.0 - a.smoothing, softplus(-p.m)) + scaled(a.smoothing, softplus(p.m))) : 0.0;
 }
 
 // 96 pairs of 4096 tokens: 5.4 us, and 5.7 for pref_grad_kernel, where the bytes

@@ -128,8 +128,8 @@ def policy_loss(logp, old, ref, adv, weight, low, high, beta, dloss=1.0):
         pg_sum += w[i] * pg
         kl_sum += w[i] * kl
         cut_sum += w[i] * cut
-        dlogp[i] = dloss * w[i] * ((0.0 if cut else -gain) + beta * dkl)
-    return pg_sum + beta * kl_sum, (pg_sum, kl_sum, cut_sum), dlogp
+        dlogp[i] = dloss * w[i] * ((0.0 if cut else -gain) + (beta * dkl if beta else 0.0))
+    return pg_sum + (beta * kl_sum if beta else 0.0), (pg_sum, kl_sum, cut_sum), dlogp
 
 
 def _softplus(x):
@@ -154,7 +154,7 @@ def preference_loss(logp, ref, valid, offsets, weight, beta, margin, smoothing, 
         m = rewards[i] - rewards[p + i] - margin
         slope = 0.0
         if w != 0:
-            loss += w * ((1 - smoothing) * _softplus(-m) + smoothing * _softplus(m))
+            loss += w * sum(f * _softplus(x) for f, x in ((1 - smoothing, -m), (smoothing, m)) if f)
             with np.errstate(over="ignore"):
                 slope = dloss * w * (smoothing / (1 + np.exp(-m)) - (1 - smoothing) / (1 + np.exp(m)))
         for s, sign in ((i, 1.0), (p + i, -1.0)):

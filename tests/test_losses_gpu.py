@@ -130,6 +130,20 @@ def test_policy_reference_beyond_reach():
         assert out[0] == INF and out[1][1] == INF, i
 
 
+@pytest.mark.parametrize("n", [5, 9000])
+def test_policy_kl_only_watched(n):
+    """With beta = 0 the KL terms are reported and enter neither the loss nor its
+    gradient, infinities and NaN among them."""
+    lp, ol, rf, adv, w = _policy_inputs(n, 21, weighted=False)
+    want = _policy(lp, ol, None, adv, w, beta=0.0)
+    for bad in (-INF, INF, NAN):
+        rf[n // 2] = bad
+        out = _policy(lp, ol, rf, adv, w, beta=0.0)
+        assert torch.equal(out[0], want[0]) and torch.equal(out[2], want[2]), bad
+        assert torch.equal(out[1][::2], want[1][::2])
+        assert torch.isnan(out[1][1]) if bad != bad else out[1][1] == INF, bad
+
+
 def test_policy_no_tokens():
     e = torch.empty(0, device=DEV)
     out = _policy(e, e, e, e, e)
@@ -228,6 +242,27 @@ def test_preference_bad_offsets_stay_in_bounds():
         off = torch.tensor(o, device=DEV)
         out = _pref(lp, off)
         _check_pref(lp, off, None, None, None, out)
+
+
+@pytest.mark.parametrize("pairs", [3, 40])
+def test_preference_answers_beyond_reach(pairs):
+    """An answer that the policy cannot give has the reward -inf: a pair whose
+    rejected answer it is costs nothing without smoothing, one whose preferred
+    answer it is costs nothing with a smoothing of 1."""
+    n = 2 * pairs * 6
+    off = torch.arange(0, n + 1, 6, device=DEV)
+    lp = -torch.exp(draw((n,), 31)).to(DEV)
+    w = torch.full((pairs,), 0.25, device=DEV)
+    for seq, smoothing in ((pairs + 1, 0.0), (1, 1.0)):
+        x, v = lp.clone(), w.clone()
+        x[seq * 6 + 2], v[1] = -INF, 0.0
+        want = _pref(lp, off, w=v, smoothing=smoothing)
+        out = _pref(x, off, w=w, smoothing=smoothing)
+        assert torch.equal(out[0], want[0]) and torch.equal(out[2], want[2]) and out[1][seq] == -INF
+        out = _pref(x, off, w=w, smoothing=1.0 - smoothing)
+        assert out[0] == INF and not torch.isnan(out[2]).any()
+        out = _pref(x, off, w=w, smoothing=0.125)
+        assert out[0] == INF and not torch.isnan(out[2]).any()
 
 
 def test_preference_nothing():
