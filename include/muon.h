@@ -495,7 +495,11 @@ muon_status muon_token_logp_fwd(const void* logits, int64_t ld, muon_dtype dt, i
 /* Its gradient: dlogit_j = scale dlogp ([j = target] - exp(z_j - lse)), the
  * target's 1 - exp(logp) formed from logp; 0 in the rows of tokens without a
  * target and those whose dlogp is 0 (they are not read).  A probability below
- * 2^-126 may be 0.
+ * 2^-126 may be 0.  An offset of a whole row changes nothing, however large: where
+ * |lse| > 64 (or infinite, where z exceeds fp32), probabilities come from logp and
+ * the target's logit, and where |logp| > 64 as well, from the row's maximum and sum,
+ * formed again; a row that is -inf throughout has 0.  The second kind of row, and
+ * with dlogits = logits the first too, is one workgroup's.
  *   logp, lse : as the forward pass wrote them.
  *   dlogp     : tokens floats, as the losses below write them.
  *   dlogits   : [tokens, vocab] of dt; may be logits itself. */

@@ -250,6 +250,7 @@ muon_status muon_token_logp_bwd(const void* logits, int64_t ld, muon_dtype dt, i
     muon::LogpBwdArgs a{};
     a.logits = logits; a.targets = targets; a.rows = tokens; a.cols = vocab; a.ld = ld; a.ld_d = ld_d;
     a.scale = scale;
+    a.scale2 = float(double(scale) * 1.4426950408889634);
     a.logp = logp; a.lse = lse; a.dlogp = dlogp; a.dlogits = dlogits;
     return launched(muon::run_logp_bwd(a, dt == MUON_BF16, (hipStream_t)stream));
   });

@@ -202,49 +202,141 @@ __global__ __launch_bounds__(64) void logp_join_kernel(LogpArgs a, bool bf16) {
   if (lane == 0) put_row(a, row, mine, some, xt);
 }
 
+// Maximum and sum of a row's terms by the NT threads that share it, the target's
+// own among them.  Every thread has the result, and has read all that it reads
+// before any of them leaves.
+template <typename T, int NT> __device__ __forceinline__ MaxSum row_sum(const T* x, int cols, int t, float c, MaxSum* waves) {
+  constexpr int N = Piece<T>::N, NW = NT / 64;
+  MaxSum mine{-INFINITY, 0.0f};
+#pragma unroll 1
+  for (int col = t * N; col < cols; col += NT * N) {
+    Piece<T> raw;
+    raw.template load<false>(x + col, cols - col);
+    float v[N];
+    raw.get(v);
+#pragma unroll
+    for (int j = 0; j < N; ++j) v[j] = col + j < cols ? v[j] : -INFINITY;
+    add_block(mine, v, c);
+  }
+  mine = lanes_join<(NT < 64 ? NT : 64)>(mine, c);
+  if constexpr (NW > 1) {
+    __syncthreads();
+    if (threadIdx.x % 64 == 0) waves[threadIdx.x / 64] = mine;
+    __syncthreads();
+    mine = waves[0];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) mine = join(mine, waves[w], c);
+  }
+  return mine;
+}
+
+// One run of a row's gradient: U pieces of every thread from col0 on, of a
+// probability exp(scale (x_j - off) + base) each.  off counts where SHIFT says so.
+template <bool SHIFT, int STEP, typename T, int U, bool STREAM>
+__device__ __forceinline__ void put_gradient(const LogpBwdArgs& a, int64_t row, int col0, int at, float g, float off,
+                                             float base) {
+  constexpr int N = Piece<T>::N;
+  const int cols = int(a.cols);
+  const T* x = (const T*)a.logits + row * a.ld;
+  T* out = (T*)a.dlogits + row * a.ld_d;
+  Piece<T> raw[U];
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int col = col0 + i * STEP;
+    raw[i].template load<STREAM>(x + col, cols - col);
+  }
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int col = col0 + i * STEP;
+    float v[N];
+    raw[i].get(v);
+#pragma unroll
+    for (int j = 0; j < N; ++j)
+      v[j] = -g * __builtin_amdgcn_exp2f(fmaf(SHIFT ? v[j] - off : v[j], a.scale, base) * 1.44269504f);
+    if (unsigned(at - col) < unsigned(N)) {
+      const float own = -g * expm1f(a.logp[row]);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = col + j == at ? own : v[j];
+    }
+    Piece<T>::store(out + col, cols - col, v, a.stream_out);
+  }
+}
+template <int STEP, typename T, int U>
+__device__ __forceinline__ void put_zeros(const LogpBwdArgs& a, int64_t row, int col0) {
+  const int cols = int(a.cols);
+  T* out = (T*)a.dlogits + row * a.ld_d;
+#pragma unroll
+  for (int i = 0; i < U; ++i) {
+    const int col = col0 + i * STEP;
+    const float zero[Piece<T>::N] = {};
+    Piece<T>::store(out + col, cols - col, zero, a.stream_out);
+  }
+}
+
+// A statistic of at most this size, rounded to fp32, leaves a probability within
+// 2^-19 of itself.
+constexpr float kNear = 64.0f;
+
 // NT threads take U NT pieces of a row; blockIdx.x counts these along it,
 // blockIdx.y the rows.  Bound by memory: 8192 x 65536 bf16, a tenth of the rows
 // without a target, 331 us, 6.2 TB/s; rows at odd addresses (4096 x 65521) 212 us, 5.1.
+//
+// A probability is exp(z_j - lse) as long as lse is small.  A large one has lost what
+// it adds to the row's maximum (all of it at the lowest value, where it cannot hold
+// the logarithm of the vocabulary): the target's logit and logp take its place, which
+// an offset of the whole row does not change, or, where logp is large too, the row's
+// maximum and sum, formed again.  The latter is done for the whole row by the
+// threads of one blockIdx.x, and so is a row whose target's logit may be overwritten
+// while others still read it (dlogits in the logits' place).  Which one goes by a hash
+// of the row: row % gridDim.x leaves most compute units without such rows (8192 x
+// 65536 bf16, all rows at 1000, into another tensor 325 us; in place 385, 730 by
+// row % gridDim.x, 1490 by blockIdx.x 0; with unlikely targets as well 443).
 template <typename T, int NT, int WG, int U, bool STREAM>
-__global__ __launch_bounds__(WG) void logp_bwd_kernel(LogpBwdArgs a) {
-  constexpr int ROWS = WG / NT, N = Piece<T>::N;
+__global__ __launch_bounds__(WG, U == 1 ? 8 : 1) void logp_bwd_kernel(LogpBwdArgs a) {
+  constexpr int ROWS = WG / NT, N = Piece<T>::N, STEP = NT * N, RUN = STEP * U;
+  static_assert(NT <= 64 || ROWS == 1);  // the barriers below are a row's
+  __shared__ MaxSum waves[WG / 64];
   const int t = threadIdx.x % NT;
-  const int cols = int(a.cols), col0 = int(blockIdx.x) * (NT * N * U) + t * N;
   for (int64_t row = int64_t(blockIdx.y) * ROWS + threadIdx.x / NT; row < a.rows; row += int64_t(gridDim.y) * ROWS) {
     const int64_t target = a.targets[row];
     const float lse = a.lse[row], up = a.dlogp[row], g = up * a.scale;
-    const bool some = uint64_t(target) < uint64_t(a.cols) && up != 0.0f && lse != -INFINITY;
-    const T* x = (const T*)a.logits + row * a.ld;
-    T* out = (T*)a.dlogits + row * a.ld_d;
-    if (!some) {
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const int col = col0 + i * NT * N;
-        const float zero[N] = {};
-        Piece<T>::store(out + col, cols - col, zero, a.stream_out);
-      }
-      continue;
-    }
-    Piece<T> raw[U];
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int col = col0 + i * NT * N;
-      raw[i].template load<STREAM>(x + col, cols - col);
-    }
     const int at = int(target);
-#pragma unroll
-    for (int i = 0; i < U; ++i) {
-      const int col = col0 + i * NT * N;
-      float v[N];
-      raw[i].get(v);
-#pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = -g * __builtin_amdgcn_exp2f(fmaf(v[j], a.scale, -lse) * 1.44269504f);
-      if (unsigned(at - col) < unsigned(N)) {
-        const float own = -g * expm1f(a.logp[row]);
-#pragma unroll
-        for (int j = 0; j < N; ++j) v[j] = col + j == at ? own : v[j];
+    bool some = uint64_t(target) < uint64_t(a.cols) && up != 0.0f, whole = false;
+    float off = 0.0f, base = -lse;
+    if (some && fabsf(lse) <= kNear) {
+      // short rows are bound by instructions: a way without the subtraction, in the
+      // registers of eight waves a SIMD (30000 x 500 bf16 13.9 us, 15.2 without the
+      // former, 15.0 without the latter)
+      if constexpr (U == 1) {
+        put_gradient<false, STEP, T, U, STREAM>(a, row, int(blockIdx.x) * RUN + t * N, at, g, off, base);
+        continue;
       }
-      Piece<T>::store(out + col, cols - col, v, a.stream_out);
+    } else if (some) {
+      const T* x = (const T*)a.logits + row * a.ld;
+      const float logp = a.logp[row];
+      const bool near = fabsf(logp) <= kNear;
+      whole = !near || a.in_place;
+      if (whole && blockIdx.x != (uint32_t(row) * 2654435761u >> 16) % gridDim.x) continue;
+      if (near) {
+        off = Elem<T>::load(x + target);
+        base = logp;
+        some = off != -INFINITY;  // else the row is -inf throughout
+        if constexpr (NT > 64) {
+          asm volatile("" ::"v"(off));  // the load has returned
+          __syncthreads();
+        }
+      } else {
+        const MaxSum m = row_sum<T, NT>(x, int(a.cols), t, a.scale2, waves);
+        off = above(m.m);
+        base = -logf(m.s);
+        some = m.s != 0.0f;
+      }
+    }
+    const int from = whole ? 0 : int(blockIdx.x) * RUN, to = whole ? int(a.cols) : from + 1;
+#pragma unroll 1
+    for (int run = from; run < to; run += RUN) {
+      if (some) put_gradient<true, STEP, T, U, STREAM>(a, row, run + t * N, at, g, off, base);
+      else put_zeros<STEP, T, U>(a, row, run + t * N);
     }
   }
 }
@@ -302,6 +394,7 @@ hipError_t run_logp_fwd(const LogpArgs& a, bool bf16, hipStream_t st) {
 hipError_t run_logp_bwd(const LogpBwdArgs& args, bool bf16, hipStream_t st) {
   LogpBwdArgs a = args;
   a.stream_out = a.rows * a.cols * (bf16 ? 2 : 4) > kStreamOut;
+  a.in_place = a.dlogits == a.logits;
   auto go = [&](auto t, auto nt, auto u, auto stream) {
     constexpr int NT = decltype(nt)::value, WG = 256, U = decltype(u)::value, RUN = NT * Piece<decltype(t)>::N * U;
     const int64_t runs = (a.cols + RUN - 1) / RUN, groups = (a.rows + WG / NT - 1) / (WG / NT);

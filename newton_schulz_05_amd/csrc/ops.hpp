@@ -140,12 +140,12 @@ struct LogpBwdArgs {
   const void* logits;
   const int64_t* targets;
   int64_t rows, cols, ld, ld_d;
-  float scale;
+  float scale, scale2;
   const float* logp;
   const float* lse;
   const float* dlogp;
   void* dlogits;
-  bool stream_out;
+  bool stream_out, in_place;
 };
 
 struct PolicyArgs {

@@ -91,7 +91,22 @@ def token_logp(x, targets, scale):
     return logp, lse
 
 
+def token_logp_gradient(x, targets, scale, dlogp):
+    """The gradient of sum(dlogp * logp) by the logits, from the logits alone."""
+    out = np.zeros_like(x)
+    for i in range(x.shape[0]):
+        t = int(targets[i])
+        if not 0 <= t < x.shape[1] or dlogp[i] == 0 or np.all(x[i] == -np.inf):
+            continue
+        z = x[i] * scale
+        e = np.exp(z - z.max())
+        out[i] = -scale * dlogp[i] * e / e.sum()
+        out[i, t] = scale * dlogp[i] * np.delete(e, t).sum() / e.sum()
+    return out
+
+
 def token_logp_backward(x, targets, scale, logp, lse, dlogp):
+    """The same from given logp and lse: they are taken as exact."""
     out = np.zeros_like(x)
     for i in range(x.shape[0]):
         t = int(targets[i])
