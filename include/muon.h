@@ -423,7 +423,8 @@ typedef struct {
  * and in the first `rot` elements of y, with h = rot / 2, the pairs
  * (y_i, y_i+h) (interleaved: (y_2i, y_2i+1)) turned by the token's angles,
  *   (a, b) -> (a cos - b sin, b cos + a sin),
- * in fp32, rounded once.  The other elements keep y.
+ * in fp32, rounded once.  The other elements keep y.  Any finite head is normed:
+ * where its squares add to more than fp32 holds they are formed scaled down.
  *   q, k, q_out, k_out : [batch, tokens, heads, dim] of dt; k and k_out null
  *                      for queries alone (heads_k is then 0).  q_out may be q
  *                      itself and k_out k itself.

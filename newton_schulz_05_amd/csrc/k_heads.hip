@@ -106,12 +106,15 @@ __device__ __forceinline__ void unpack_held(Held<T> h, const LanePart<T>& p, boo
     for (int j = 0; j < E; ++j) v[E * i + j] = RAG != kRagged || j < n ? w[j] : 0.0f;
   }
 }
-// The elements that this lane counts, 0 for the others, infinite ones too.
+// Whether another lane counts element j; the elements that this lane counts, 0 for
+// the others, infinite ones too.
+template <int RAG, typename T> __device__ __forceinline__ bool skipped(const LanePart<T>& p, int j) {
+  return RAG == kOverlap && j % LanePart<T>::E < p.skip[j / LanePart<T>::E];
+}
 template <int RAG, typename T>
 __device__ __forceinline__ void counted(const LanePart<T>& p, const float (&v)[16], float (&w)[16]) {
-  constexpr int E = LanePart<T>::E;
 #pragma unroll
-  for (int k = 0; k < 16; ++k) w[k] = RAG == kOverlap && k % E < p.skip[k / E] ? 0.0f : v[k];
+  for (int j = 0; j < 16; ++j) w[j] = skipped<RAG>(p, j) ? 0.0f : v[j];
 }
 template <int RAG, typename T>
 __device__ __forceinline__ void store_held(T* row, const LanePart<T>& p, bool live, const float (&v)[16], bool stream) {
@@ -189,6 +192,12 @@ __device__ __forceinline__ float inv_root(float v) {
   const bool tiny = v < 1e-30f;
   return rsqrtf(tiny ? v * 0x1p96f : v) * (tiny ? 0x1p48f : 1.0f);
 }
+
+// What brings a row whose squares add to more than fp32 holds into the middle of
+// its range: 512 squares of 2^128 2^-80 stay below 2^106, and what goes below the
+// smallest number on the way is none of a row of 2^59 or more.  Its r is rounded to
+// the subnormal step 2^-149 where the row's mean size is above 2^126: 2^-22 at most.
+constexpr float kDown = 0x1p-80f;
 
 // One row's place: offsets of its tensors, and its token's word of positions (or,
 // without positions, its row of the table).
@@ -290,7 +299,16 @@ __global__ __launch_bounds__(WG) void heads_fwd_kernel(HeadArgs a) {
 #pragma unroll
     for (int j = 0; j < 16; ++j) q = fmaf(w[j], w[j], q);
     q = lane_sum<LANES>(q);
-    const float r = inv_root(fmaf(q, inv, a.eps));
+    float r = inv_root(fmaf(q, inv, a.eps));
+    if (q == INFINITY) {  // squares beyond fp32: of the row scaled down
+      q = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 16; ++j) {
+        const float d = v[j] * kDown;
+        q = skipped<RAG>(p, j) ? q : fmaf(d, d, q);
+      }
+      r = inv_root(fmaf(lane_sum<LANES>(q), inv, a.eps * kDown * kDown)) * kDown;
+    }
 #pragma unroll
     for (int j = 0; j < 16; ++j) v[j] = v[j] * r * gv[j];
     turn<RAG, false>(ang, v);
@@ -305,9 +323,11 @@ __global__ __launch_bounds__(WG) void heads_fwd_kernel(HeadArgs a) {
 // workgroups 173 (of a graph's 172), 512 185, 2048 199; with the next rows' loads
 // in flight over the sums 173 with 768 workgroups, 205 with 1024 (three waves a
 // SIMD instead of four).  64 tokens: 7.2 us, launches and latency.
+// Four waves a SIMD are asked for: without, fp32 interleaved heads of 33 take three
+// (21.4 us, 22.3, 26.8 with three).
 template <typename T, int LANES, bool INTER, int RAG>
-__global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
-  constexpr int ROWS = WG / LANES, WAVES = WG / 64, E = LanePart<T>::E;
+__global__ __launch_bounds__(WG, RAG == kOverlap ? 1 : 4) void heads_bwd_kernel(HeadArgs a) {
+  constexpr int ROWS = WG / LANES, WAVES = WG / 64;
   __shared__ float sums[WAVES][16 * LANES];
   const bool keys = int(blockIdx.x) >= a.q.wgs;
   const HeadRows& h = keys ? a.k : a.q;
@@ -341,21 +361,32 @@ __global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
     }
     q = lane_sum<LANES>(q);
     dot = lane_sum<LANES>(dot);
-    // An infinite gradient in an element that another lane counts has met the 0 above
-    // (taking it out in every row takes the registers of a fourth wave: 2 x 4096 tokens of 24 + 8
-    // heads of 90 bf16 44.4 us, 37.1 so).
-    if (RAG == kOverlap && dot != dot) {
-      dot = 0.0f;
+    // The sums again: squares beyond fp32, of the row scaled down; or an infinite
+    // gradient in an element that another lane counts, which has met the 0 above
+    // (taking it out in every row takes the registers of a fourth wave: 2 x 4096 tokens
+    // of 24 + 8 heads of 90 bf16 44.4 us, 37.1 so).
+    float eps = a.eps, back = 1.0f;
+    if (q == INFINITY || (RAG == kOverlap && dot != dot)) {
+      if (q == INFINITY) {
+        eps = eps * kDown * kDown;
+        back = kDown;
+      }
+      q = dot = 0.0f;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) dot = j % E < p.skip[j / E] ? dot : fmaf(g[j] * gv[j], x[j], dot);
+      for (int j = 0; j < 16; ++j) {
+        x[j] *= back;
+        q = skipped<RAG>(p, j) ? q : fmaf(x[j], x[j], q);
+        dot = skipped<RAG>(p, j) ? dot : fmaf(g[j] * gv[j], x[j], dot);
+      }
+      q = lane_sum<LANES>(q);
       dot = lane_sum<LANES>(dot);
     }
-    const float r = inv_root(fmaf(q, inv, a.eps)), c = dot * r * inv;
+    const float r = inv_root(fmaf(q, inv, eps)), c = dot * r * inv, rx = r * back;
 #pragma unroll
     for (int j = 0; j < 16; ++j) {
       const float xh = x[j] * r;
       acc[j] = fmaf(g[j], xh, acc[j]);
-      x[j] = r * fmaf(-xh, c, g[j] * gv[j]);
+      x[j] = rx * fmaf(-xh, c, g[j] * gv[j]);
     }
     store_held<RAG>((T*)h.out + at.out, p, live, x, a.stream_out);
   }
@@ -364,6 +395,7 @@ __global__ __launch_bounds__(WG) void heads_bwd_kernel(HeadArgs a) {
 #pragma unroll
   for (int j = 0; j < 16; ++j) acc[j] = across_groups<LANES>(acc[j]);
   if ((threadIdx.x & 63) < LANES) {
+    constexpr int E = LanePart<T>::E;
 #pragma unroll
     for (int i = 0; i < LanePart<T>::P; ++i)
 #pragma unroll
