@@ -323,8 +323,9 @@ __global__ __launch_bounds__(WG) void heads_fwd_kernel(HeadArgs a) {
 // workgroups 173 (of a graph's 172), 512 185, 2048 199; with the next rows' loads
 // in flight over the sums 173 with 768 workgroups, 205 with 1024 (three waves a
 // SIMD instead of four).  64 tokens: 7.2 us, launches and latency.
-// Four waves a SIMD are asked for: without, fp32 interleaved heads of 33 take three
-// (21.4 us, 22.3, 26.8 with three).
+// Four waves a SIMD are asked for: left to itself the compiler takes the registers of
+// three for fp32 interleaved pairs of odd heads (2 x 4096 tokens of 12 + 4 heads of 33
+// 26.8 us, 22.3 so); where pieces overlap it would spill.
 template <typename T, int LANES, bool INTER, int RAG>
 __global__ __launch_bounds__(WG, RAG == kOverlap ? 1 : 4) void heads_bwd_kernel(HeadArgs a) {
   constexpr int ROWS = WG / LANES, WAVES = WG / 64;
@@ -457,12 +458,13 @@ __global__ __launch_bounds__(WG) void heads_zero_kernel(HeadArgs a) {
 
 template <typename F> hipError_t by_kind(const HeadArgs& a, bool bf16, bool inter, F f) {
   auto lanes = [&](auto t, auto in, auto rag) {
+    constexpr int most = head_most_lanes(decltype(in)::value, decltype(rag)::value == kWhole, sizeof(t));
     switch (head_lanes(a.dim, a.rot, inter)) {
       case 4: f(t, in, rag, std::integral_constant<int, 4>{}); break;
       case 8: f(t, in, rag, std::integral_constant<int, 8>{}); break;
       case 16: f(t, in, rag, std::integral_constant<int, 16>{}); break;
       case 32: f(t, in, rag, std::integral_constant<int, 32>{}); break;
-      default: f(t, in, rag, std::integral_constant<int, 64>{});
+      default: if constexpr (most > 32) f(t, in, rag, std::integral_constant<int, 64>{});
     }
   };
   typedef std::integral_constant<int, kWhole> Whole;

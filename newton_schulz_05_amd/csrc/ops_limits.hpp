@@ -108,6 +108,12 @@ inline int head_lanes(int dim, int rot, bool interleaved) {
   return lanes;
 }
 
+// The most lanes it gives: interleaved pairs fill 16 elements a lane, and so do whole
+// pieces of 8; other segments, halves and the rest, may leave part of a lane empty.
+constexpr int head_most_lanes(bool interleaved, bool whole, int size) {
+  return interleaved || (whole && size == 2) ? int(kHeadMaxDim) / 16 : int(kHeadMaxDim) / 8;
+}
+
 // Workgroups of the backward pass, one partial sum of dgamma each: a fixed number
 // in all, queries and keys in proportion to their rows.
 constexpr int kHeadMaxParts = 1024;
