@@ -273,7 +273,7 @@ __device__ __forceinline__ void turn(const Angles<T, INTER>& g, float (&v)[16]) 
 // A group of rows a workgroup, queries' workgroups before the keys'.  Bound by
 // memory: 4 x 4096 tokens of 32 + 8 heads of 128 bf16, slices of a projection's
 // output to heads before tokens, 66 us, 5.1 TB/s of the bytes that it cannot do
-// without; 285 instructions a wave, 57 % of the cycles.  Two and four groups a
+// without; 289 instructions a wave, 58 % of the cycles.  Two and four groups a
 // workgroup 68.8 and 69.1 (the graph of that call 67.9), rows in the order of the
 // output instead of the input 79, tiles of 4 heads by 8 tokens 73.
 template <typename T, int LANES, bool INTER, int RAG>

@@ -402,8 +402,8 @@ hipError_t run_logp_bwd(const LogpBwdArgs& args, bool bf16, hipStream_t st) {
                        dim3(unsigned(runs), unsigned(std::min<int64_t>(groups, 65535))), dim3(WG), 0, st, a);
   };
   auto by_cols = [&](auto t) {
-    // The fewest lanes that hold a row of up to 32 pieces: 60000 x 100 bf16 8.0 us, 19.7
-    // with 64 lanes; 60000 x 256 13.0 and 19.1.  Two and four rows a lane at once:
+    // The fewest lanes that hold a row of up to 32 pieces: 60000 x 100 bf16 8.8 us, 19.7
+    // with 64 lanes; 60000 x 256 12.9 and 19.1.  Two and four rows a lane at once:
     // no gain.
     constexpr int N = Piece<decltype(t)>::N;
     if (a.cols <= 16 * N) go(t, Num<16>{}, Num<1>{}, Flag<false>{});
